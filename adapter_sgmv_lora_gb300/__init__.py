@@ -9,7 +9,11 @@ library cannot be loaded, every call raises.
 Names follow the C ABI: ``lora_build_routing``, ``lora_set_slot``,
 ``lora_shrink``, ``lora_expand``, ``lora_workspace_bytes``,
 ``lora_sgmv_apply``, ``lora_sgmv_apply_noalloc``, ``lora_base_gemm_apply``,
-``lora_get_device_status``, ``lora_last_call_path``, ``lora_status_string``.
+``lora_get_device_status``, ``lora_last_call_path``, ``lora_status_string``;
+between the projections ``lora_build_rope``, ``lora_rope_append``,
+``lora_attention_workspace_bytes``, ``lora_paged_attention``,
+``lora_kv_copy_pages`` and the page bookkeeping ``lora_pages_*`` (class
+``Pages``).
 """
 from __future__ import annotations
 
@@ -27,14 +31,18 @@ LORA_OK = 0
 STATUS_NAMES = {0: "LORA_OK", 1: "LORA_ERR_NULL", 2: "LORA_ERR_SHAPE", 3: "LORA_ERR_RANK",
                 4: "LORA_ERR_SLOT_RANGE", 5: "LORA_ERR_ROUTING", 6: "LORA_ERR_DTYPE",
                 7: "LORA_ERR_ALIGN", 8: "LORA_ERR_WORKSPACE", 9: "LORA_ERR_CUDA",
-                10: "LORA_ERR_TOO_MANY_GROUPS"}
+                10: "LORA_ERR_TOO_MANY_GROUPS", 11: "LORA_ERR_NO_PAGES"}
 DTYPE_F32, DTYPE_BF16 = 0, 1
 DEV_BAD_SLOT, DEV_BAD_OFFSETS, DEV_BAD_END, DEV_TIMEOUT, DEV_BAD_ROW = 1, 2, 4, 8, 16
+DEV_BAD_PAGE, DEV_BAD_LENGTH = 32, 64
 # Kernel families of lora_last_call_path (include/lora_sgmv.h).
 PATH_GENERIC_SHRINK, PATH_GENERIC_EXPAND = 0x1, 0x2
 PATH_MMA_SHRINK, PATH_MMA_EXPAND = 0x4, 0x8
 PATH_TC_SHRINK, PATH_TC_EXPAND = 0x10, 0x20
 PATH_PREP, PATH_BASE_GEMM = 0x80, 0x100
+PATH_ROPE, PATH_GENERIC_ROPE = 0x200, 0x400
+PATH_MMA_ATTENTION, PATH_GENERIC_ATTENTION, PATH_JOIN = 0x800, 0x1000, 0x2000
+PATH_PAGES = 0x4000
 MAX_SLICES = 3
 
 
@@ -65,6 +73,38 @@ class _Routing(ctypes.Structure):
     _fields_ = [("lora_ids", ctypes.c_void_p), ("grouped_offsets", ctypes.c_void_p),
                 ("num_groups", ctypes.c_int32), ("end", ctypes.c_int32), ("token_rows", ctypes.c_void_p),
                 ("host_grouped_offsets", ctypes.c_void_p), ("host_lora_ids", ctypes.c_void_p)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("num_tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int), ("attention_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("turns", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("q", _Heads), ("k", _Heads),
+                ("v", _Heads), ("q_out", _Heads), ("k_out", _Heads), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("cache_rows", ctypes.c_void_p)]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("q", _Heads), ("out", _Heads),
+                ("block_tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32),
+                ("lengths", ctypes.c_void_p), ("scale", ctypes.c_float), ("lse", ctypes.c_void_p)]
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("tables", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("num_free", ctypes.c_int32)]
 
 
 _lib = None
@@ -118,6 +158,29 @@ def lib():
     L.lora_last_call_path.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     L.lora_selftest_wait_timeout.restype = ctypes.c_int
     L.lora_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
+    f64 = ctypes.c_double
+    L.lora_build_rope.restype = ctypes.c_int
+    L.lora_build_rope.argtypes = [i32, f64, ctypes.c_int, f64, i32, f64, f64, vp, vp]
+    # Descriptors of repeated calls are held as ready-made pointers: plain void pointers here.
+    L.lora_rope_append.restype = ctypes.c_int
+    L.lora_rope_append.argtypes = [vp, vp, vp]
+    L.lora_attention_workspace_bytes.restype = ctypes.c_size_t
+    L.lora_attention_workspace_bytes.argtypes = [vp, vp]
+    L.lora_paged_attention.restype = ctypes.c_int
+    L.lora_paged_attention.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]
+    L.lora_kv_copy_pages.restype = ctypes.c_int
+    L.lora_kv_copy_pages.argtypes = [vp, i32, vp, vp, i32, vp]
+    pg = ctypes.POINTER(_Pages)
+    L.lora_pages_init.restype = ctypes.c_int
+    L.lora_pages_init.argtypes = [pg]
+    L.lora_pages_append.restype = ctypes.c_int
+    L.lora_pages_append.argtypes = [pg, i32, i32, vp, i32p, i32p]
+    L.lora_pages_fork.restype = ctypes.c_int
+    L.lora_pages_fork.argtypes = [pg, i32, i32, i32]
+    L.lora_pages_trim.restype = ctypes.c_int
+    L.lora_pages_trim.argtypes = [pg, i32, i32]
+    L.lora_pages_compact.restype = ctypes.c_int
+    L.lora_pages_compact.argtypes = [pg, vp, vp, i32p]
     _lib = L
     return L
 
@@ -461,3 +524,308 @@ class CallBuilder:
         _check(rc, "lora_sgmv_apply")
         self.last_path = int(self.L.lora_last_call_path(ctypes.byref(self._n)))
         self.last_launches = int(self._n.value)
+
+
+# ------------------------------------------- attention between projections --
+#
+# The objects below describe buffers for repeated calls, as CallBuilder does:
+# frozen, holding their tensors, with the C structs made once.  New values are
+# written into the tensors; other tensors need another object.
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+MAX_HEAD_DIM = 256
+
+
+def _dtype_code(t) -> int:
+    import torch
+    code = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError("tensors must be float32 or bfloat16")
+    return code
+
+
+def _on_cuda(**tensors) -> None:
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if device is not None and t.device != device:
+            raise ValueError("%s is on another device" % name)
+        device = t.device
+
+
+def _int32(name: str, t, shape) -> None:
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be an int32 tensor of shape %s" % (name, tuple(shape)))
+    if t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+
+
+def _heads(name: str, t, shape, dtype) -> _Heads:
+    if t is None:
+        return _Heads(None, 0, 0)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    if t.dtype != dtype:
+        raise ValueError("%s must have the dtype of the others" % name)
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError("%s must have unit stride in its last dimension" % name)
+    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def lora_build_rope(rotary_dim: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                    original_max_positions: int = 0, low_turns: float = 1.0, high_turns: float = 4.0,
+                    frequencies=None, attention_scale: float = 1.0) -> dict:
+    """The rotation's frequency table (host; include/lora_sgmv.h): {"turns":
+    uint64 [rotary_dim / 2], "rotary_dim", "attention_scale"}.
+
+    scaling: "none", "linear" (position interpolation), "ntk", or "parts" (by
+    parts between low_turns and high_turns turns over original_max_positions:
+    1 and 4 for Llama 3's rule, 1 and 32 for YaRN's, whose attention_scale is
+    0.1 ln(factor) + 1).  frequencies: rotary_dim / 2 radians per position
+    instead of theta's."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    D = int(rotary_dim)
+    freq = None
+    if frequencies is not None:
+        freq = np.ascontiguousarray(frequencies, dtype=np.float64)
+        if freq.shape != (D // 2,):
+            raise ValueError("frequencies must hold rotary_dim / 2 values")
+    turns = np.zeros(max(D // 2, 1), dtype=np.uint64)
+    rc = lib().lora_build_rope(D, float(theta), ROPE_SCALINGS[scaling], float(factor), int(original_max_positions),
+                               float(low_turns), float(high_turns), None if freq is None else freq.ctypes.data,
+                               turns.ctypes.data)
+    _check(rc, "lora_build_rope")
+    return {"turns": turns, "rotary_dim": D, "attention_scale": float(attention_scale)}
+
+
+@dataclass(frozen=True)
+class Rope:
+    """The frequency table on the device (int64 tensor holding the uint64 bits)."""
+    turns: object
+    rotary_dim: int
+    attention_scale: float = 1.0
+
+
+def rope_to_device(r: dict, device="cuda") -> Rope:
+    """Upload the host table from lora_build_rope."""
+    import torch
+    return Rope(torch.from_numpy(r["turns"].view(np.int64).copy()).to(device), int(r["rotary_dim"]),
+                float(r["attention_scale"]))
+
+
+@dataclass(frozen=True)
+class KVCache:
+    """One layer's paged cache: k and v [num_pages, page_size, kv_heads,
+    head_dim] with the same strides, unit in the last dimension (head-major
+    memory is a permuted view)."""
+    k: object
+    v: object
+
+    def __post_init__(self):
+        k, v = self.k, self.v
+        code = _dtype_code(k)
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be 4-D [pages, page_size, kv_heads, head_dim] of one shape and dtype")
+        if k.shape[3] > 1 and (k.stride(3) != 1 or v.stride(3) != 1):
+            raise ValueError("k and v must have unit stride in their last dimension")
+        if any(k.shape[i] > 1 and k.stride(i) != v.stride(i) for i in range(3)):
+            raise ValueError("k and v must have the same strides")
+        _on_cuda(k=k, v=v)
+        c = _KVCache(code, k.shape[0], k.shape[1], k.shape[2], k.shape[3], k.data_ptr(), v.data_ptr(), k.stride(0),
+                     k.stride(1), k.stride(2))
+        object.__setattr__(self, "_struct", c)
+        object.__setattr__(self, "_ref", ctypes.addressof(c))
+
+
+@dataclass(frozen=True)
+class KVCaches:
+    """The layers' caches for lora_kv_copy_pages."""
+    layers: Sequence[KVCache]
+
+    def __post_init__(self):
+        arr = (_KVCache * max(len(self.layers), 1))(*[c._struct for c in self.layers])
+        object.__setattr__(self, "_struct", arr)
+        object.__setattr__(self, "_ref", ctypes.addressof(arr))
+
+
+@dataclass(frozen=True)
+class RopeProblem:
+    """One lora_rope_append call: q [T, heads, head_dim], k and v [T, kv_heads,
+    head_dim] (views of a fused qkv output, for instance), q_out (may be q),
+    optionally k_out, a cache with cache_rows int32 [T], and per-head norm
+    weights [head_dim].  rope None: no rotation (then positions may be None)."""
+    q: object = None
+    k: object = None
+    v: object = None
+    q_out: object = None
+    k_out: object = None
+    rope: Optional[Rope] = None
+    positions: object = None
+    interleaved: bool = False
+    cache: Optional[KVCache] = None
+    cache_rows: object = None
+    q_weight: object = None
+    k_weight: object = None
+    eps: float = 1e-6
+
+    def __post_init__(self):
+        x = self.q if self.q is not None else self.k
+        if x is None or x.dim() != 3:
+            raise ValueError("q or k must be given, 3-D [tokens, heads, head_dim]")
+        code = _dtype_code(x)
+        T, hd = x.shape[0], x.shape[2]
+        H = self.q.shape[1] if self.q is not None else 0
+        Hk = self.k.shape[1] if self.k is not None and self.k.dim() == 3 else 0
+        rot = self.rope.rotary_dim if self.rope is not None else 0
+        _on_cuda(q=self.q, k=self.k, v=self.v, q_out=self.q_out, k_out=self.k_out, positions=self.positions,
+                 turns=self.rope.turns if self.rope is not None else None, cache_rows=self.cache_rows,
+                 cache=self.cache.k if self.cache is not None else None, q_weight=self.q_weight,
+                 k_weight=self.k_weight)
+        if self.rope is not None and self.rope.turns.numel() < rot // 2:
+            raise ValueError("turns must hold rotary_dim / 2 values")
+        for name, t in (("positions", self.positions), ("cache_rows", self.cache_rows)):
+            if t is not None:
+                _int32(name, t, (T,))
+        for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
+            if w is not None and (tuple(w.shape) != (hd,) or w.dtype != x.dtype or (hd > 1 and w.stride(0) != 1)):
+                raise ValueError("%s must be a contiguous [head_dim] tensor of q's dtype" % name)
+        ptr = lambda t: t.data_ptr() if t is not None else None
+        c = _Rope(code, T, H, Hk, hd, rot, int(bool(self.interleaved)),
+                  self.rope.attention_scale if self.rope is not None else 1.0, float(self.eps),
+                  ptr(self.rope.turns) if self.rope is not None else None, ptr(self.positions),
+                  _heads("q", self.q, (T, H, hd), x.dtype), _heads("k", self.k, (T, Hk, hd), x.dtype),
+                  _heads("v", self.v, (T, Hk, hd), x.dtype), _heads("q_out", self.q_out, (T, H, hd), x.dtype),
+                  _heads("k_out", self.k_out, (T, Hk, hd), x.dtype), ptr(self.q_weight), ptr(self.k_weight),
+                  ptr(self.cache_rows))
+        object.__setattr__(self, "_struct", c)
+        object.__setattr__(self, "_ref", ctypes.addressof(c))
+        object.__setattr__(self, "_cache_ref", self.cache._ref if self.cache is not None else None)
+
+
+def lora_rope_append(problem: RopeProblem, stream=None) -> None:
+    """Norm, rotate and store a batch's q/k/v rows in one pass (include/lora_sgmv.h)."""
+    _check(lib().lora_rope_append(problem._ref, problem._cache_ref, _stream_handle(stream)), "lora_rope_append")
+
+
+@dataclass(frozen=True)
+class AttentionProblem:
+    """One lora_paged_attention call: q and out [B, heads, head_dim] (out may
+    be q), block_tables int32 [B, max_pages], lengths int32 [B], scale (None:
+    1 / sqrt(head_dim)), optionally lse float32 [B, heads]."""
+    q: object
+    out: object
+    cache: KVCache
+    block_tables: object
+    lengths: object
+    scale: Optional[float] = None
+    lse: object = None
+
+    def __post_init__(self):
+        import torch
+        q, cc = self.q, self.cache._struct
+        if q.dim() != 3:
+            raise ValueError("q must be 3-D [sequences, heads, head_dim]")
+        B, H, hd = q.shape
+        if hd != cc.head_dim:
+            raise ValueError("q must have the cache's head_dim")
+        _on_cuda(q=q, out=self.out, block_tables=self.block_tables, lengths=self.lengths, lse=self.lse,
+                 cache=self.cache.k)
+        if self.block_tables.dim() != 2:
+            raise ValueError("block_tables must be 2-D [sequences, max_pages]")
+        M = self.block_tables.shape[1]
+        _int32("block_tables", self.block_tables, (B, M))
+        _int32("lengths", self.lengths, (B,))
+        if self.lse is not None and (self.lse.dtype != torch.float32 or tuple(self.lse.shape) != (B, H) or
+                                     not self.lse.is_contiguous()):
+            raise ValueError("lse must be a contiguous float32 [sequences, heads] tensor")
+        scale = 1.0 / hd ** 0.5 if self.scale is None else float(self.scale)
+        dt = self.cache.k.dtype
+        c = _Attention(B, H, _heads("q", q, (B, H, hd), dt), _heads("out", self.out, (B, H, hd), dt),
+                       self.block_tables.data_ptr() or None, self.block_tables.stride(0) if B > 1 else M, M,
+                       self.lengths.data_ptr(), scale, self.lse.data_ptr() if self.lse is not None else None)
+        object.__setattr__(self, "_struct", c)
+        object.__setattr__(self, "_ref", ctypes.addressof(c))
+
+
+def lora_attention_workspace_bytes(problem: AttentionProblem) -> int:
+    return int(lib().lora_attention_workspace_bytes(problem._ref, problem.cache._ref))
+
+
+def new_attention_workspace(problem: AttentionProblem):
+    """A workspace tensor of lora_attention_workspace_bytes(problem) bytes."""
+    import torch
+    nbytes = max(lora_attention_workspace_bytes(problem), 256)
+    return torch.empty((nbytes + 15) // 16 * 4, dtype=torch.float32, device=problem.q.device)
+
+
+def lora_paged_attention(problem: AttentionProblem, workspace, stream=None) -> None:
+    """Attention of one new token per sequence over its cached pages (include/lora_sgmv.h)."""
+    ws, nbytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
+    _check(lib().lora_paged_attention(problem._ref, problem.cache._ref, ws, nbytes, _stream_handle(stream)),
+           "lora_paged_attention")
+
+
+def lora_kv_copy_pages(caches: KVCaches, src, dst, stream=None) -> None:
+    """Copy pages src[i] -> dst[i] (host integers) in every layer's K and V."""
+    s = np.ascontiguousarray(src, dtype=np.int32)
+    d = np.ascontiguousarray(dst, dtype=np.int32)
+    if s.ndim != 1 or s.shape != d.shape:
+        raise ValueError("src and dst must be 1-D and the same length")
+    _check(lib().lora_kv_copy_pages(caches._ref, len(caches.layers), s.ctypes.data, d.ctypes.data, s.size,
+                                    _stream_handle(stream)), "lora_kv_copy_pages")
+
+
+class Pages:
+    """Host bookkeeping of one cache's pages (lora_pages_*): tables [max_seqs,
+    max_pages], lengths, refs and the free list are numpy arrays to read or
+    upload; only the methods change them."""
+
+    def __init__(self, num_pages: int, page_size: int, max_seqs: int, max_pages: int):
+        if min(num_pages, page_size, max_seqs, max_pages) < 1:
+            raise LoraError(2, "lora_pages_init")
+        self.tables = np.empty((max_seqs, max_pages), dtype=np.int32)
+        self.lengths = np.empty(max_seqs, dtype=np.int32)
+        self.refs = np.empty(num_pages, dtype=np.int32)
+        self.free_pages = np.empty(num_pages, dtype=np.int32)
+        self._c = _Pages(num_pages, page_size, max_seqs, max_pages, self.tables.ctypes.data, self.lengths.ctypes.data,
+                         self.refs.ctypes.data, self.free_pages.ctypes.data, 0)
+        _check(lib().lora_pages_init(ctypes.byref(self._c)), "lora_pages_init")
+
+    @property
+    def num_free(self) -> int:
+        return int(self._c.num_free)
+
+    def append(self, seq: int, num_tokens: int):
+        """(cache rows of the new tokens, page copies to run first as (src,
+        dst) pairs: at most one)."""
+        rows = np.empty(max(int(num_tokens), 0), dtype=np.int32)
+        src, dst = ctypes.c_int32(), ctypes.c_int32()
+        _check(lib().lora_pages_append(ctypes.byref(self._c), int(seq), int(num_tokens), rows.ctypes.data,
+                                       ctypes.byref(src), ctypes.byref(dst)), "lora_pages_append")
+        return rows, ([(src.value, dst.value)] if src.value >= 0 else [])
+
+    def fork(self, parent: int, child: int, num_tokens: Optional[int] = None) -> None:
+        """child shares parent's first num_tokens (None: all of them)."""
+        if num_tokens is None:
+            if not 0 <= parent < self.lengths.size:
+                raise LoraError(2, "lora_pages_fork")
+            num_tokens = int(self.lengths[parent])
+        _check(lib().lora_pages_fork(ctypes.byref(self._c), int(parent), int(child), int(num_tokens)),
+               "lora_pages_fork")
+
+    def trim(self, seq: int, num_tokens: int = 0) -> None:
+        _check(lib().lora_pages_trim(ctypes.byref(self._c), int(seq), int(num_tokens)), "lora_pages_trim")
+
+    def compact(self):
+        """(src, dst) page moves to run with lora_kv_copy_pages; the tables are already rewritten."""
+        n = ctypes.c_int32()
+        src = np.empty(self.refs.size, dtype=np.int32)
+        dst = np.empty(self.refs.size, dtype=np.int32)
+        _check(lib().lora_pages_compact(ctypes.byref(self._c), src.ctypes.data, dst.ctypes.data, ctypes.byref(n)),
+               "lora_pages_compact")
+        return src[:n.value].copy(), dst[:n.value].copy()

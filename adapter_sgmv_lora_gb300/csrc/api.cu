@@ -39,12 +39,12 @@ int device_sm_count() {
   return sms[dev];
 }
 
-namespace {
-
 void begin_call() {
   t_path_bits = 0;
   t_launches = 0;
 }
+
+namespace {
 
 std::mutex g_sym_mu;
 unsigned* g_status_ptr[64] = {nullptr};
@@ -69,10 +69,14 @@ bool status_ptrs(unsigned** word, unsigned** snap) {
   return true;
 }
 
+}  // namespace
+
 unsigned* status_ptr() {
   unsigned* w = nullptr;
   return status_ptrs(&w, nullptr) ? w : nullptr;
 }
+
+namespace {
 
 // One thread: read and clear the status word in one atomic exchange.
 __global__ void status_exchange_kernel(unsigned* word, unsigned* snap) { *snap = atomicExch(word, 0u); }
@@ -437,6 +441,7 @@ extern "C" const char* lora_status_string(lora_status_t status) {
     case LORA_ERR_WORKSPACE: return "LORA_ERR_WORKSPACE: workspace missing or too small";
     case LORA_ERR_CUDA: return "LORA_ERR_CUDA: a CUDA call failed";
     case LORA_ERR_TOO_MANY_GROUPS: return "LORA_ERR_TOO_MANY_GROUPS: more groups than adapter slots";
+    case LORA_ERR_NO_PAGES: return "LORA_ERR_NO_PAGES: not enough free cache pages";
   }
   return "unknown lora_status_t";
 }

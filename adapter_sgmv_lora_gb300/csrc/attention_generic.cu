@@ -1,0 +1,207 @@
+// attention_generic.cu -- paged decode attention in fp32 arithmetic on the
+// CUDA cores: fp32 caches, and bf16 caches whose shapes or alignments the
+// tensor-core core does not take.  The frame is attention.cuh.
+//
+// One warp works on a tile of 8 tokens held as fp32 rows in shared memory.
+// Scores: lane (r, g) takes token r and the 16-byte chunks 4 i + g of its
+// key, so a chunk of a query is one 64-byte broadcast; 16-byte chunks are
+// swizzled by the token so the 8 tokens' reads fall on different banks.
+// Output: each lane owns HD / 32 neighbouring columns and walks the 8 tokens.
+#include "attention.cuh"
+
+namespace lora {
+namespace {
+
+// ASYNC: fp32 rows on 16-byte boundaries come in by asynchronous copies; else
+// element by element, converted on the way.
+template <typename T_, int HD_, int CH_, bool ASYNC>
+struct GenericCore {
+  using T = T_;
+  static constexpr int TT = 8, W = 4, HD = HD_, CH = CH_, COMB = CH_;
+  static constexpr int STAGE_BYTES = 2 * TT * HD * 4;
+  static constexpr int STAGES = 2;
+  static constexpr int CTAS = HD <= 128 ? 2 : 1;
+  static constexpr int VPL = HD / 32;  // output columns per lane
+  static constexpr int EXTRA_BYTES = (CH * HD + W * TT * CH) * 4;
+  static_assert(CH <= 8, "");
+
+  float* q;  // [CH][HD], this CTA's queries
+  float* prob;  // [TT][CH], this warp's
+  float scale;
+  int heads;
+  float m[CH], l[CH], o[CH][VPL];
+
+  __device__ __forceinline__ GenericCore(const AttnDesc& p, uint8_t* extra)
+      : q(reinterpret_cast<float*>(extra)),
+        prob(q + CH * HD + (threadIdx.x >> 5) * TT * CH),
+        scale(p.scale * kLog2e) {}
+
+  static __device__ __forceinline__ int at(int r, int chunk) { return r * HD + ((chunk ^ (r & 7)) << 2); }
+
+  __device__ __forceinline__ void load(const AttnDesc& p, uint8_t* stage, long long off) const {
+    float* k = reinterpret_cast<float*>(stage);
+    float* v = k + TT * HD;
+    const int lane = threadIdx.x & 31;
+    const T* kg = static_cast<const T*>(p.cache.k);
+    const T* vg = static_cast<const T*>(p.cache.v);
+    if constexpr (ASYNC) {
+#pragma unroll
+      for (int i = 0; i < TT * HD / 4 / 32; ++i) {
+        const int e = i * 32 + lane, r = e / (HD / 4), c = e % (HD / 4);
+        const long long row = __shfl_sync(0xffffffffu, off, r);
+        if (c * 4 < p.cache.head_dim) {
+          const long long src = row < 0 ? 0 : row + c * 4;
+          cp_async16_zfill(k + at(r, c), kg + src, row < 0 ? 0 : 16);
+          cp_async16_zfill(v + at(r, c), vg + src, row < 0 ? 0 : 16);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < TT; ++r) {
+        const long long row = __shfl_sync(0xffffffffu, off, r);
+        for (int d = lane; d < p.cache.head_dim; d += 32) {
+          const int dst = at(r, d >> 2) + (d & 3);
+          k[dst] = row < 0 ? 0.f : to_f(kg[row + d]);
+          v[dst] = row < 0 ? 0.f : to_f(vg[row + d]);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void begin(const AttnDesc& p, int seq, int head0, int heads_) {
+    heads = heads_;
+    const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride;
+    for (int i = threadIdx.x; i < CH * HD; i += W * 32) {
+      const int h = i / HD, d = i % HD;
+      q[i] = h < heads && d < p.cache.head_dim ? to_f(src[(head0 + h) * p.q.head_stride + d]) : 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < CH; ++h) {
+      m[h] = kNegInf;
+      l[h] = 0.f;
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) o[h][e] = 0.f;
+    }
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ void tile(const AttnDesc& p, const uint8_t* stage, int n) {
+    const float* k = reinterpret_cast<const float*>(stage);
+    const float* v = k + TT * HD;
+    const int lane = threadIdx.x & 31, r = lane & 7, g = lane >> 3;
+    float s[CH] = {};
+#pragma unroll 4
+    for (int i = 0; i < HD / 16; ++i) {
+      const int c = i * 4 + g;
+      const float4 kv = *reinterpret_cast<const float4*>(k + at(r, c));
+#pragma unroll
+      for (int h = 0; h < CH; ++h) {
+        if (h < heads) {
+          const float4 qv = *reinterpret_cast<const float4*>(q + h * HD + c * 4);
+          s[h] = fmaf(kv.x, qv.x, s[h]);
+          s[h] = fmaf(kv.y, qv.y, s[h]);
+          s[h] = fmaf(kv.z, qv.z, s[h]);
+          s[h] = fmaf(kv.w, qv.w, s[h]);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < CH; ++h) {
+      if (h >= heads) continue;
+      s[h] += __shfl_xor_sync(0xffffffffu, s[h], 8);
+      s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
+      s[h] = r < n ? s[h] * scale : kNegInf;
+      float top = s[h];
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float now = fmaxf(m[h], top);
+      const float base = now == kNegInf ? 0.f : now;  // nothing but -inf so far: every weight is 0
+      const float pr = exp2f(s[h] - base);
+      const float keep = exp2f(m[h] - base);
+      m[h] = now;
+      l[h] = fmaf(l[h], keep, pr);  // this lane's token; the tokens are summed in put
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) o[h][e] *= keep;
+      if (g == 0) prob[r * CH + h] = pr;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      float vv[VPL];
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) {
+        const int d = lane * VPL + e;
+        vv[e] = v[at(j, d >> 2) + (d & 3)];
+      }
+#pragma unroll
+      for (int h = 0; h < CH; ++h) {
+        if (h >= heads) continue;
+        const float pr = prob[j * CH + h];
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) o[h][e] = fmaf(pr, vv[e], o[h][e]);
+      }
+    }
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void put(int, float* comb, float2* stat) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < CH; ++h) {
+      float sum = l[h];
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == 0) stat[h] = make_float2(m[h], sum);
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) comb[h * (HD + 4) + lane * VPL + e] = o[h][e];
+    }
+  }
+};
+
+// fp32 rows on 16-byte boundaries.
+bool async_ok(const AttnDesc& p) {
+  const CacheDesc& c = p.cache;
+  const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v);
+  return p.dtype == LORA_DTYPE_F32 && (low & 15) == 0 && c.head_dim % 4 == 0 && c.page_stride % 4 == 0 &&
+         c.token_stride % 4 == 0 && c.head_stride % 4 == 0;
+}
+
+template <typename T, int HD, bool ASYNC>
+cudaError_t by_group(const AttnDesc& p, void* ws, cudaStream_t s) {
+  if (p.group == 1) return launch_core<GenericCore<T, HD, 1, ASYNC>>(p, ws, s, LORA_PATH_GENERIC_ATTENTION);
+  return launch_core<GenericCore<T, HD, 8, ASYNC>>(p, ws, s, LORA_PATH_GENERIC_ATTENTION);
+}
+
+template <typename T, bool ASYNC>
+cudaError_t by_width(const AttnDesc& p, void* ws, cudaStream_t s) {
+  if (p.cache.head_dim <= 64) return by_group<T, 64, ASYNC>(p, ws, s);
+  if (p.cache.head_dim <= 128) return by_group<T, 128, ASYNC>(p, ws, s);
+  return by_group<T, 256, ASYNC>(p, ws, s);
+}
+
+}  // namespace
+
+CoreShape generic_attention_shape(const AttnDesc& p) {
+  const int hd = p.cache.head_dim <= 64 ? 64 : (p.cache.head_dim <= 128 ? 128 : 256);
+  CoreShape c = shape_of<GenericCore<float, 64, 8, true>>();
+  c.HD = hd;
+  c.CH = p.group == 1 ? 1 : 8;
+  c.CTAS = hd <= 128 ? 2 : 1;
+  return c;
+}
+
+cudaError_t launch_attention_generic(const AttnDesc& p, void* workspace, cudaStream_t s) {
+  if (p.dtype == LORA_DTYPE_BF16) return by_width<__nv_bfloat16, false>(p, workspace, s);
+  return async_ok(p) ? by_width<float, true>(p, workspace, s) : by_width<float, false>(p, workspace, s);
+}
+
+size_t attention_workspace_bytes(const AttnDesc& p) {
+  const CoreShape c = generic_attention_shape(p);
+  return workspace_parts(c, units_of(c, p, kMaxSmsForWorkspace)).bytes;
+}
+
+cudaError_t launch_attention(AttnDesc p, void* workspace, cudaStream_t s) {
+  return launch_attention_generic(p, workspace, s);
+}
+
+}  // namespace lora

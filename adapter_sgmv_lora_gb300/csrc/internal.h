@@ -54,6 +54,13 @@ inline cudaError_t noted(cudaError_t e, unsigned path_bits) {
   return e;
 }
 
+// Starts an entry-point call on this host thread (clears what
+// lora_last_call_path reports).  Defined in api.cu.
+void begin_call();
+// Device address of the status word on the current device (nullptr if the
+// lookup fails).  Defined in api.cu.
+unsigned* status_ptr();
+
 // Streaming multiprocessors of the current device (cached per device; 0 if
 // the query fails, which makes the split heuristics fall back to no split).
 int device_sm_count();
@@ -176,5 +183,64 @@ cudaError_t launch_tc_expand(const ProblemDesc& p, const float* u, cudaStream_t 
 // launched nothing, when the tensor maps cannot be encoded.
 size_t tc_packed_bytes(int S, int end, int n_slices, int R);
 cudaError_t launch_tc_apply_packed(const ProblemDesc& p, void* workspace, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Attention between the projections (attention_api.cu validates and calls).
+
+// One layer's paged cache, as the kernels see it (lora_kv_cache_t).
+struct CacheDesc {
+  void* k;
+  void* v;
+  long long page_stride, token_stride, head_stride;
+  int num_pages, page_size, num_kv_heads, head_dim;
+};
+
+// A [rows, heads, head_dim] view (lora_heads_t).
+struct HeadsDesc {
+  void* data;
+  long long row_stride, head_stride;
+};
+
+// A validated lora_rope_append call.
+struct RopeDesc {
+  int dtype, T, H, Hk, hd, rot, layout;
+  float attention_scale, eps;
+  const unsigned long long* turns;
+  const int* positions;
+  HeadsDesc q, k, v, q_out, k_out;
+  const void* q_weight;
+  const void* k_weight;
+  const int* cache_rows;  // nullptr: no cache
+  CacheDesc cache;
+  unsigned* status;
+};
+cudaError_t launch_rope(const RopeDesc& p, cudaStream_t s);
+
+// A validated lora_paged_attention call.
+struct AttnDesc {
+  int dtype, num_seqs, num_heads, group;  // group: query heads per key/value head
+  HeadsDesc q, out;
+  CacheDesc cache;
+  const int* tables;
+  long long table_stride;
+  int max_pages;
+  int max_len;  // max_pages * page_size, or a little below INT_MAX
+  const int* lengths;
+  float scale;
+  float* lse;  // or nullptr
+  unsigned* status;
+  // Filled in by the launcher: heads of a group are taken CH at a time
+  // (chunks per key/value head), and the workspace's three parts.
+  int chunks;
+  int4* splits;    // [units] contexts that begin before a unit and are joined there
+  float2* stats;   // [2 * units, CH] running maximum and sum of a partial result
+  float* partial;  // [2 * units, CH, HD] its unnormalised output
+};
+size_t attention_workspace_bytes(const AttnDesc& p);
+cudaError_t launch_attention(AttnDesc p, void* workspace, cudaStream_t s);
+
+// Page copies of caches with one geometry.  kv: num_caches pairs {k, v}.
+cudaError_t launch_copy_pages(const CacheDesc& geometry, int dtype, const lora_kv_cache_t* caches, int num_caches,
+                              const int* src, const int* dst, int n, cudaStream_t s);
 
 }  // namespace lora

@@ -1,0 +1,128 @@
+// page_copy.cu -- copies listed pages of every layer's K and V
+// (lora_kv_copy_pages).  Bounded by memory: each byte is read once and
+// written once.
+//
+// The list of pages and the layers' pointers travel as launch parameters (no
+// upload, so a call is one launch per table-full of copies).  A page is
+// `outer` x `mid` runs of `run` contiguous units: its three inner dimensions,
+// merged where one continues the other, so a dense page is a single run.
+#include <algorithm>
+#include <cuda_bf16.h>
+#include <utility>
+
+#include "internal.h"
+
+namespace lora {
+namespace {
+
+constexpr int kMaxTensors = 128;  // K and V of 64 layers a launch
+constexpr int kMaxCopies = 1024;  // pages a launch
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;        // units in flight per thread
+
+struct CopyTable {
+  void* tensor[kMaxTensors];
+  int2 page[kMaxCopies];  // source, destination
+};
+
+struct PageShape {  // in units of the copy
+  long long page_stride, outer_stride, mid_stride;
+  long long outer, mid, run;
+};
+
+// grid.x: chunks of one page; grid.y: tensors; grid.z: pages.  DENSE: the page
+// is one run.  I: the index type within a page (32 bits unless the page has
+// more units).
+template <typename U, bool DENSE, typename I>
+__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ CopyTable table,
+                                                              const __grid_constant__ PageShape g) {
+  const int2 page = table.page[blockIdx.z];
+  U* base = static_cast<U*>(table.tensor[blockIdx.y]);
+  const U* src = base + page.x * g.page_stride;
+  U* dst = base + page.y * g.page_stride;
+  const I run = (I)g.run, per_outer = (I)(g.mid * g.run), total = (I)(g.outer * g.mid * g.run);
+  const I first = (I)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  U v[kUnroll];
+  long long at[kUnroll];
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const I e = first + i * kThreads;
+    if (e < total) {
+      if constexpr (DENSE) {
+        at[i] = e;
+      } else {
+        const I o = e / per_outer, r = e - o * per_outer, m = r / run;
+        at[i] = o * g.outer_stride + m * g.mid_stride + (r - m * run);
+      }
+      v[i] = src[at[i]];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i)
+    if (first + i * kThreads < total) dst[at[i]] = v[i];
+}
+
+template <typename U>
+cudaError_t run(const CopyTable& t, const PageShape& g, int tensors, int pages, cudaStream_t s) {
+  const long long total = g.outer * g.mid * g.run, chunk = (long long)kThreads * kUnroll;
+  const dim3 grid((unsigned)((total + chunk - 1) / chunk), tensors, pages);
+  const bool dense = g.outer * g.mid == 1, wide = total > (1LL << 31);
+  if (wide) {
+    if (dense) copy_pages_kernel<U, true, long long><<<grid, kThreads, 0, s>>>(t, g);
+    else copy_pages_kernel<U, false, long long><<<grid, kThreads, 0, s>>>(t, g);
+  } else {
+    if (dense) copy_pages_kernel<U, true, unsigned><<<grid, kThreads, 0, s>>>(t, g);
+    else copy_pages_kernel<U, false, unsigned><<<grid, kThreads, 0, s>>>(t, g);
+  }
+  return noted(cudaGetLastError(), LORA_PATH_PAGES);
+}
+
+}  // namespace
+
+cudaError_t launch_copy_pages(const CacheDesc& c, int dtype, const lora_kv_cache_t* caches, int num_caches,
+                              const int* src, const int* dst, int n, cudaStream_t s) {
+  // Inner dimensions of a page in bytes, smallest stride first; merged while
+  // contiguous.
+  const long long es = dtype == LORA_DTYPE_BF16 ? 2 : 4;
+  std::pair<long long, int> a{c.token_stride * es, c.page_size}, b{c.head_stride * es, c.num_kv_heads};
+  if (a.second == 1) std::swap(a, b);  // b is the dimension of one, if any is
+  if (b.second > 1 && b.first < a.first) std::swap(a, b);
+  long long run_bytes = c.head_dim * es;
+  if (a.second > 1 && a.first == run_bytes) {
+    run_bytes *= a.second;
+    a = b;
+    b = {0, 1};
+    if (a.second > 1 && a.first == run_bytes) {
+      run_bytes *= a.second;
+      a = {0, 1};
+    }
+  }
+  const long long page_bytes = c.page_stride * es;
+  // The widest unit that every address and length is a multiple of.
+  unsigned long long low = (unsigned long long)run_bytes | (a.second > 1 ? a.first : 0) | (b.second > 1 ? b.first : 0) |
+                           (c.num_pages > 1 ? page_bytes : 0) | 16;
+  for (int i = 0; i < num_caches; ++i)
+    low |= reinterpret_cast<unsigned long long>(caches[i].k) | reinterpret_cast<unsigned long long>(caches[i].v);
+  const long long unit = (long long)(low & (~low + 1));
+  const PageShape g{page_bytes / unit, b.first / unit, a.first / unit, b.second, a.second, run_bytes / unit};
+  for (int c0 = 0; c0 < num_caches; c0 += kMaxTensors / 2) {
+    const int nc = std::min(num_caches - c0, kMaxTensors / 2);
+    for (int p0 = 0; p0 < n; p0 += kMaxCopies) {
+      const int np = std::min(n - p0, kMaxCopies);
+      CopyTable t;
+      for (int i = 0; i < nc; ++i) {
+        t.tensor[2 * i] = caches[c0 + i].k;
+        t.tensor[2 * i + 1] = caches[c0 + i].v;
+      }
+      for (int i = 0; i < np; ++i) t.page[i] = make_int2(src[p0 + i], dst[p0 + i]);
+      cudaError_t e = unit >= 16 ? run<uint4>(t, g, 2 * nc, np, s)
+                      : unit == 8 ? run<uint2>(t, g, 2 * nc, np, s)
+                      : unit == 4 ? run<unsigned>(t, g, 2 * nc, np, s)
+                                  : run<unsigned short>(t, g, 2 * nc, np, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace lora

@@ -57,7 +57,8 @@ typedef enum {
   LORA_ERR_ALIGN = 7,         /* pointer/stride alignment required by the call */
   LORA_ERR_WORKSPACE = 8,     /* workspace NULL or smaller than lora_workspace_bytes() */
   LORA_ERR_CUDA = 9,          /* a CUDA runtime call or kernel launch failed */
-  LORA_ERR_TOO_MANY_GROUPS = 10 /* num_groups > max_num_loras ("No free lora slots") */
+  LORA_ERR_TOO_MANY_GROUPS = 10, /* num_groups > max_num_loras ("No free lora slots") */
+  LORA_ERR_NO_PAGES = 11       /* not enough free cache pages (lora_pages_append) */
 } lora_status_t;
 
 /* Storage type of x, y and the A/B stacks of one problem. */
@@ -69,6 +70,8 @@ typedef enum { LORA_DTYPE_F32 = 0, LORA_DTYPE_BF16 = 1 } lora_dtype_t;
 #define LORA_DEV_BAD_END 4u      /* grouped_offsets[num_groups] != end */
 #define LORA_DEV_TIMEOUT 8u      /* a kernel gave up (after ~1 s) waiting for its own copies */
 #define LORA_DEV_BAD_ROW 16u     /* a token_rows entry outside [0, num_tokens) */
+#define LORA_DEV_BAD_PAGE 32u    /* a block-table page or a cache row outside the cache */
+#define LORA_DEV_BAD_LENGTH 64u  /* a sequence length below 0 or past its block table */
 
 #define LORA_MAX_SLICES 3
 
@@ -363,6 +366,234 @@ lora_status_t lora_base_gemm_apply(const lora_problem_t* problem, const lora_rou
                                    const lora_base_weight_t* base, void* workspace, size_t workspace_bytes,
                                    lora_stream_t stream);
 
+/* ==========================================================================
+ * Attention between the projections: what a served layer does with the
+ * q/k/v rows that lora_sgmv_apply or lora_base_gemm_apply leaves, before the
+ * o_proj call.  The pages have no counterpart; the conventions at the top of
+ * this file hold (caller-owned buffers, host validation before any launch,
+ * device arrays checked by the kernels, the status word).
+ * ========================================================================== */
+
+/* Widest head of the calls below. */
+#define LORA_MAX_HEAD_DIM 256
+
+/* A [rows, heads, head_dim] view: element (r, h, d) at
+ * data + r*row_stride + h*head_stride + d (strides in elements).  The q part
+ * of a fused q/k/v output y is {y, y_row_stride, head_dim}, its k part
+ * {y + n_heads*head_dim, y_row_stride, head_dim}. */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+} lora_heads_t;
+
+/*
+ * One layer's paged key/value cache.  Element (page p, token o of the page,
+ * head h, d) of K is k[p*page_stride + o*token_stride + h*head_stride + d]
+ * (elements), V the same from v.  Token-major pages ([pages, page_size,
+ * heads, head_dim]) and head-major ones ([pages, heads, page_size, head_dim])
+ * are both such views, as is one pool that holds K and V side by side.  The
+ * strides may leave gaps but no two elements may share an address
+ * (LORA_ERR_SHAPE).  "Cache row" c is token c % page_size of page
+ * c / page_size; num_pages * page_size is at most INT32_MAX.  Offsets are
+ * formed in 64 bits.
+ */
+typedef struct {
+  lora_dtype_t dtype;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  void* k;
+  void* v;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+} lora_kv_cache_t;
+
+/* How the frequencies of lora_build_rope are scaled for long contexts. */
+typedef enum {
+  LORA_ROPE_NONE = 0,
+  LORA_ROPE_LINEAR = 1,  /* position interpolation: f / factor */
+  LORA_ROPE_NTK = 2,     /* base theta * factor^(D / (D - 2)), D = rotary_dim >= 4 */
+  LORA_ROPE_PARTS = 3    /* by parts: g f + (1 - g) f / factor with
+                            g = clamp((n - low_turns) / (high_turns - low_turns), 0, 1),
+                            n = original_max_positions * f / (2 pi), the turns the
+                            pair makes over the original context */
+} lora_rope_scaling_t;
+
+/*
+ * lora_build_rope -- HOST ONLY.  The frequency of each rotated pair i <
+ * rotary_dim / 2, f_i = theta^(-2 i / rotary_dim) radians per position (or
+ * frequencies[i], when that HOST array of rotary_dim / 2 values is given),
+ * scaled, as a 64-bit fixed-point fraction of a turn:
+ *   turns[i] = floor(frac(f_i / (2 pi)) * 2^64).
+ * position * turns[i] modulo 2^64 is then the angle's fractional turn with
+ * no range reduction and no loss at long contexts; upload it for
+ * lora_rope_t.turns.  Errors: LORA_ERR_SHAPE (rotary_dim odd, < 2 or >
+ * LORA_MAX_HEAD_DIM; theta or factor not positive and finite; NTK with
+ * frequencies given or rotary_dim < 4; PARTS with original_max_positions < 1
+ * or high_turns <= low_turns; a frequency that is not finite; an unknown
+ * scaling), LORA_ERR_NULL.
+ */
+lora_status_t lora_build_rope(int32_t rotary_dim, double theta, lora_rope_scaling_t scaling, double factor,
+                              int32_t original_max_positions, double low_turns, double high_turns,
+                              const double* frequencies, uint64_t* turns);
+
+/* Which two elements of a head form pair i of the rotation. */
+typedef enum {
+  LORA_ROPE_HALVES = 0,     /* i and i + rotary_dim / 2 */
+  LORA_ROPE_INTERLEAVED = 1 /* 2 i and 2 i + 1 */
+} lora_rope_layout_t;
+
+/* One lora_rope_append call; every pointer is DEVICE memory. */
+typedef struct {
+  lora_dtype_t dtype;    /* q, k, v, their outputs, the norm weights and the cache */
+  int32_t num_tokens;
+  int32_t num_heads;     /* query heads, 0: no q */
+  int32_t num_kv_heads;  /* key (and value) heads, 0: no k */
+  int32_t head_dim;
+  int32_t rotary_dim;    /* first rotary_dim elements of a head rotate (even, 0..head_dim) */
+  lora_rope_layout_t layout;
+  float attention_scale; /* factor on the rotated elements (YaRN's sqrt(1/t)); 1 normally */
+  float eps;             /* of the norms */
+  const uint64_t* turns;     /* [rotary_dim / 2], lora_build_rope */
+  const int32_t* positions;  /* [num_tokens], any sign */
+  lora_heads_t q, k, v;      /* inputs; v only with cache rows */
+  lora_heads_t q_out;        /* may be q itself */
+  lora_heads_t k_out;        /* optional (data NULL: none); may be k itself */
+  const void* q_weight;      /* optional [head_dim]: RMS norm of each query head */
+  const void* k_weight;      /* optional [head_dim]: RMS norm of each key head */
+  const int32_t* cache_rows; /* optional [num_tokens]: cache row of each token, -1: none */
+} lora_rope_t;
+
+/*
+ * lora_rope_append -- one pass over the q/k/v rows of a batch.  For every
+ * token and head, in fp32 with one rounding to the storage type:
+ *   n = x * rsqrt(mean(x^2) + eps) * weight     (over head_dim; weight given)
+ *   pair i of the rotated part: (a, b) -> s (a cos - b sin, a sin + b cos)
+ * with s = attention_scale and the angle position * f_i; elements from
+ * rotary_dim on are n unchanged.  q goes to q_out, k to k_out (if given) and
+ * to cache row cache_rows[t] of K, v unchanged to the same row of V.  Cache
+ * rows must be distinct; a row below -1 or past the cache is not stored and
+ * raises LORA_DEV_BAD_PAGE.  cache may be NULL exactly when cache_rows is.
+ * q_out (k_out) may be q (k) itself, with the same strides, but must not
+ * overlap the inputs otherwise.  num_tokens == 0 is a valid no-op.
+ * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_SHAPE (sizes, a negative
+ * input stride, output strides that let two elements share an address, a
+ * cache whose type, heads or head_dim differ).
+ */
+lora_status_t lora_rope_append(const lora_rope_t* rope, const lora_kv_cache_t* cache, lora_stream_t stream);
+
+/* One lora_paged_attention call; every pointer is DEVICE memory. */
+typedef struct {
+  int32_t num_seqs;   /* rows of q and out */
+  int32_t num_heads;  /* a multiple of the cache's num_kv_heads: head h reads key/value head
+                         h / (num_heads / num_kv_heads) */
+  lora_heads_t q;     /* the cache's type */
+  lora_heads_t out;   /* the cache's type; may be q itself */
+  const int32_t* block_tables; /* row b lists the pages of sequence b in order */
+  int64_t table_stride;        /* entries from one row to the next */
+  int32_t max_pages;           /* entries of a row */
+  const int32_t* lengths;      /* [num_seqs]: cached tokens, the new one's included */
+  float scale;                 /* of the scores, usually 1 / sqrt(head_dim) */
+  float* lse;                  /* optional [num_seqs, num_heads]: log of the scores' exponential sum */
+} lora_attention_t;
+
+/*
+ * lora_attention_workspace_bytes -- DEVICE workspace of lora_paged_attention:
+ * the partial results of contexts that several CTAs share.  Depends on
+ * shapes only; 0 for arguments that the call would refuse.
+ */
+size_t lora_attention_workspace_bytes(const lora_attention_t* attention, const lora_kv_cache_t* cache);
+
+/*
+ * lora_paged_attention -- attention of one new token per sequence to its
+ * cached tokens: out_h = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q_h . k_j),
+ * over j < lengths[b].  A sequence of length 0 (a padding entry of a batch)
+ * gives out = 0 and lse = -inf, as does a row whose every score is -inf.
+ * Scores, softmax sums and the output's accumulation are fp32; on the bf16
+ * tensor-core path the probabilities enter the product with V as two bf16
+ * terms (16 significant bits).  Cached values past a sequence's end and
+ * block-table entries past its last page are never used.  A length below 0
+ * or above max_pages * page_size raises LORA_DEV_BAD_LENGTH, a used page id
+ * outside the cache LORA_DEV_BAD_PAGE; that sequence's rows of out and lse
+ * are left as they were, the others are computed.  The cached tokens are shared out evenly over the GPU
+ * whatever the lengths; the same lengths on the same GPU give the same bits.
+ * workspace: >= lora_attention_workspace_bytes, 16-byte aligned, contents on
+ * entry ignored; two calls that may overlap need two.
+ * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_SHAPE, LORA_ERR_WORKSPACE,
+ * LORA_ERR_ALIGN.
+ */
+lora_status_t lora_paged_attention(const lora_attention_t* attention, const lora_kv_cache_t* cache,
+                                   void* workspace, size_t workspace_bytes, lora_stream_t stream);
+
+/*
+ * lora_kv_copy_pages -- K and V of page dst[i] become those of page src[i],
+ * for every i < num_copies and every one of num_caches caches (the layers of
+ * a model: same geometry and type, else LORA_ERR_SHAPE).  src and dst are
+ * HOST arrays, read by the call.  A source may repeat (one page to many
+ * forks); a destination may not, nor be a source as well: the copies have no
+ * order among themselves (LORA_ERR_SHAPE, as for a page outside the caches).
+ * Gaps between strided rows are not touched.  Copies are exact, whatever the
+ * values.  Errors also: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_WORKSPACE (no
+ * host memory to check a long list).
+ */
+lora_status_t lora_kv_copy_pages(const lora_kv_cache_t* caches, int32_t num_caches, const int32_t* src,
+                                 const int32_t* dst, int32_t num_copies, lora_stream_t stream);
+
+/*
+ * Which page holds what: HOST bookkeeping of one cache's pages, in arrays
+ * that the caller owns.  Pages are counted by reference, so forked sequences
+ * share them; a shared page that is only partly filled is copied before
+ * either sequence writes to it (copy on write).  The calls below change these
+ * arrays alone; they return the page copies to run with lora_kv_copy_pages,
+ * enqueued before the rows are written.  On an error nothing is changed.
+ * Not thread-safe on one set of arrays.
+ */
+typedef struct {
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t max_seqs;
+  int32_t max_pages;   /* of one sequence */
+  int32_t* tables;     /* [max_seqs, max_pages] block tables; -1 past a sequence's last page */
+  int32_t* lengths;    /* [max_seqs] tokens; 0: not in use */
+  int32_t* refs;       /* [num_pages] sequences that hold the page */
+  int32_t* free_pages; /* [num_pages] stack of free pages, the next one at num_free - 1 */
+  int32_t num_free;
+} lora_pages_t;
+
+/* Every page free, every sequence empty.  LORA_ERR_NULL; LORA_ERR_SHAPE (a
+ * size < 1, num_pages * page_size > INT32_MAX). */
+lora_status_t lora_pages_init(lora_pages_t* pages);
+
+/*
+ * num_tokens >= 0 more tokens of sequence seq: takes pages as needed and
+ * writes the cache row of each new token to rows[num_tokens] (NULL allowed
+ * when num_tokens is 0).  *copy_src / *copy_dst: a page copy to run first, or
+ * -1 (at most one: the sequence's last page, when shared and partly filled).
+ * LORA_ERR_SHAPE: seq out of range, a negative count, more than max_pages
+ * pages.  LORA_ERR_NO_PAGES: not enough free pages.
+ */
+lora_status_t lora_pages_append(lora_pages_t* pages, int32_t seq, int32_t num_tokens, int32_t* rows,
+                                int32_t* copy_src, int32_t* copy_dst);
+
+/* The empty sequence child becomes the first num_tokens of parent, sharing
+ * its pages.  LORA_ERR_SHAPE: a sequence out of range, child not empty,
+ * num_tokens < 0 or above the parent's. */
+lora_status_t lora_pages_fork(lora_pages_t* pages, int32_t parent, int32_t child, int32_t num_tokens);
+
+/* Keeps the first num_tokens of seq (0: the sequence ends) and gives the pages
+ * behind them back.  LORA_ERR_SHAPE: seq or num_tokens out of range. */
+lora_status_t lora_pages_trim(lora_pages_t* pages, int32_t seq, int32_t num_tokens);
+
+/*
+ * Moves every page in use below the count of pages in use and rewrites the
+ * block tables: src[i] -> dst[i] for i < *num_copies are the copies to run
+ * (src and dst hold up to num_pages / 2 entries; no page is in both lists).
+ */
+lora_status_t lora_pages_compact(lora_pages_t* pages, int32_t* src, int32_t* dst, int32_t* num_copies);
+
 /*
  * lora_get_device_status -- reads and clears, in one atomic exchange ordered
  * after the work already on `stream`, the device status word of the current
@@ -386,6 +617,12 @@ lora_status_t lora_get_device_status(lora_stream_t stream, uint32_t* flags);
 #define LORA_PATH_TC_EXPAND 0x20u      /* persistent tcgen05 + TMA expand (long groups) */
 #define LORA_PATH_PREP 0x80u           /* load-time slot / bias preparation */
 #define LORA_PATH_BASE_GEMM 0x100u     /* base projection GEMM with the delta as K tail */
+#define LORA_PATH_ROPE 0x200u          /* norm + rotation + cache append, 16-byte accesses */
+#define LORA_PATH_GENERIC_ROPE 0x400u  /* the same, element by element (odd shapes) */
+#define LORA_PATH_MMA_ATTENTION 0x800u /* paged attention on mma.sync (bf16) */
+#define LORA_PATH_GENERIC_ATTENTION 0x1000u /* paged attention in fp32 arithmetic */
+#define LORA_PATH_JOIN 0x2000u         /* join of the contexts that CTAs shared */
+#define LORA_PATH_PAGES 0x4000u        /* page copies */
 
 /*
  * lora_last_call_path -- the OR of LORA_PATH_* bits of the kernels launched
