@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "liblora_sgmv.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "routing.cpp", "simple_kernels.cu", "sgmv_bf16.cu", "sgmv_tc.cu", "sgmv_base.cu",
-           "attention_api.cu", "pages.cpp", "rope.cu", "attention_generic.cu", "page_copy.cu"]
+           "attention_api.cu", "pages.cpp", "rope.cu", "attention_generic.cu", "attention_mma.cu",
+           "page_copy.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
               "-I", CSRC, "-I", INCLUDE]

@@ -487,6 +487,11 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
                LORA_PATH_JOIN);
 }
 
+// attention_mma.cu: bf16 on the tensor cores.  mma_attention_ok: the shapes
+// and alignments it takes.
+bool mma_attention_ok(const AttnDesc& p);
+CoreShape mma_attention_shape(const AttnDesc& p);
+cudaError_t launch_attention_mma(const AttnDesc& p, void* workspace, cudaStream_t s);
 // attention_generic.cu: fp32 arithmetic, any type, size and alignment.
 CoreShape generic_attention_shape(const AttnDesc& p);
 cudaError_t launch_attention_generic(const AttnDesc& p, void* workspace, cudaStream_t s);

@@ -195,13 +195,4 @@ cudaError_t launch_attention_generic(const AttnDesc& p, void* workspace, cudaStr
   return async_ok(p) ? by_width<float, true>(p, workspace, s) : by_width<float, false>(p, workspace, s);
 }
 
-size_t attention_workspace_bytes(const AttnDesc& p) {
-  const CoreShape c = generic_attention_shape(p);
-  return workspace_parts(c, units_of(c, p, kMaxSmsForWorkspace)).bytes;
-}
-
-cudaError_t launch_attention(AttnDesc p, void* workspace, cudaStream_t s) {
-  return launch_attention_generic(p, workspace, s);
-}
-
 }  // namespace lora

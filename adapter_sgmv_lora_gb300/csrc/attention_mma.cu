@@ -1,0 +1,215 @@
+// attention_mma.cu -- paged decode attention of bf16 caches on the tensor
+// cores (mma.sync m16n8k16, fp32 accumulation).  The frame is attention.cuh.
+//
+// One warp works on a tile of 16 tokens.  The tokens are the 16 rows of the
+// product and the query heads that share them its 8 columns, so a group of 8
+// heads fills the instruction (the other way round 8 of 16 rows would be
+// padding):
+//   S^T [16 tokens, 8 heads] = K [16, HD] Q^T       K by ldmatrix, Q in registers
+//   O^T [HD, 8 heads]       += V^T [HD, 16] P       V by transposing ldmatrix
+// P comes out of the first product with tokens along its rows and is turned
+// into the second's operand in registers (movmatrix).  It enters as two bf16
+// terms, p = hi + lo, so its rounding stays near 2^-17; one term would put an
+// error as large as the output's own rounding on top of it.
+//
+// A call reads 512 bytes of cache per token and key/value head (128 wide) and
+// does 4096 flops on them for 8 heads: at memory speed that is some 55
+// TFLOP/s, a few percent of what the instruction reaches, so the 128-row
+// tcgen05 tiles would buy nothing here and cost the softmax its place in
+// registers.  What bounds the kernel is memory.
+#include "attention.cuh"
+
+namespace lora {
+namespace {
+
+// NT: query heads a stream, in eights.
+template <int HD_, int NT>
+struct MmaCore {
+  using T = __nv_bfloat16;
+  static constexpr int TT = 16, W = 4, HD = HD_, CH = 8 * NT, COMB = 8;
+  static constexpr int STAGE_BYTES = 2 * TT * HD * 2;
+  static constexpr int STAGES = HD == 64 ? 6 : 3;
+  static constexpr int CTAS = HD <= 128 ? 2 : 1;
+  static constexpr int EXTRA_BYTES = 0;
+  static constexpr int KT = HD / 16;  // 16-wide steps of the head
+
+  uint32_t q[KT][NT][2];  // Q^T fragments
+  float o[KT][NT][4];     // O^T accumulators: rows 16 k + lane / 4 (+ 8), heads 2 (lane % 4) (+ 1)
+  float m[NT][2], l[NT][2];
+  float scale;
+
+  __device__ __forceinline__ MmaCore(const AttnDesc& p, uint8_t*) : scale(p.scale * kLog2e) {}
+
+  // Byte offset of 16-byte chunk c of row r: swizzled, so the 8 rows of an
+  // ldmatrix block fall on different banks.
+  static __device__ __forceinline__ uint32_t at(int r, int c) { return r * (HD * 2) + ((c ^ (r & 7)) << 4); }
+
+  __device__ __forceinline__ void load(const AttnDesc& p, uint8_t* stage, long long off) const {
+    const int lane = threadIdx.x & 31;
+    const T* kg = static_cast<const T*>(p.cache.k);
+    const T* vg = static_cast<const T*>(p.cache.v);
+#pragma unroll
+    for (int i = 0; i < TT * HD / 8 / 32; ++i) {
+      const int e = i * 32 + lane, r = e / (HD / 8), c = e % (HD / 8);
+      const long long row = __shfl_sync(0xffffffffu, off, r);
+      if (c * 8 < p.cache.head_dim) {
+        const long long src = row < 0 ? 0 : row + c * 8;
+        cp_async16_zfill(stage + at(r, c), kg + src, row < 0 ? 0 : 16);
+        cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, row < 0 ? 0 : 16);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void begin(const AttnDesc& p, int seq, int head0, int heads) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = n * 8 + g;
+      const T* row = src + (head0 + h) * p.q.head_stride;
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int d = k * 16 + e * 8 + t * 2;
+          q[k][n][e] = h < heads && d < p.cache.head_dim ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[k][n][e] = 0.f;
+      }
+      m[n][0] = m[n][1] = kNegInf;
+      l[n][0] = l[n][1] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void tile(const AttnDesc& p, const uint8_t* stage, int n_tokens) {
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    const uint32_t kb = smem_addr(stage), vb = kb + TT * HD * 2;
+    float s[NT][2][4] = {};  // two chains of accumulation, summed below
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      uint32_t a[4];
+      ldsm_x4(kb + at(lane & 15, 2 * k + (lane >> 4)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_bf16_16816(s[n][k & 1], a, q[k][n][0], q[k][n][1]);
+    }
+    const bool live0 = g < n_tokens, live1 = g + 8 < n_tokens;
+    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = (s[n][0][e] + s[n][1][e]) * scale;
+        if (!(e < 2 ? live0 : live1)) x[e] = kNegInf;
+      }
+      float keep[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = fmaxf(x[e], x[e + 2]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float now = fmaxf(m[n][e], top);
+        const float base = now == kNegInf ? 0.f : now;  // nothing but -inf so far: every weight is 0
+        keep[e] = exp2f(m[n][e] - base);
+        m[n][e] = now;
+        x[e] = exp2f(x[e] - base);
+        x[e + 2] = exp2f(x[e + 2] - base);
+        l[n][e] = fmaf(l[n][e], keep[e], x[e] + x[e + 2]);  // this lane's tokens; summed over lanes in put
+      }
+      split_hi_lo_bf16x2(x[0], x[1], hi[n][0], lo[n][0]);
+      split_hi_lo_bf16x2(x[2], x[3], hi[n][1], lo[n][1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        hi[n][e] = transpose_8x8(hi[n][e]);
+        lo[n][e] = transpose_8x8(lo[n][e]);
+      }
+      if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          o[k][n][0] *= keep[0];
+          o[k][n][1] *= keep[1];
+          o[k][n][2] *= keep[0];
+          o[k][n][3] *= keep[1];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      uint32_t a[4];
+      ldsm_x4_trans(vb + at((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_bf16_16816(o[k][n], a, hi[n][0], hi[n][1]);
+        mma_bf16_16816(o[k][n], a, lo[n][0], lo[n][1]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void put(int part, float* comb, float2* stat) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n != part) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (g == 0) stat[2 * t + e] = make_float2(m[n][e], sum);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          comb[(2 * t + e) * (HD + 4) + k * 16 + g] = o[k][n][e];
+          comb[(2 * t + e) * (HD + 4) + k * 16 + g + 8] = o[k][n][e + 2];
+        }
+      }
+    }
+  }
+};
+
+template <int HD>
+cudaError_t by_group(const AttnDesc& p, void* ws, cudaStream_t s) {
+  if (p.group <= 8) return launch_core<MmaCore<HD, 1>>(p, ws, s, LORA_PATH_MMA_ATTENTION);
+  return launch_core<MmaCore<HD, 2>>(p, ws, s, LORA_PATH_MMA_ATTENTION);
+}
+
+}  // namespace
+
+bool mma_attention_ok(const AttnDesc& p) {
+  const CacheDesc& c = p.cache;
+  const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v);
+  return p.dtype == LORA_DTYPE_BF16 && (low & 15) == 0 && c.head_dim % 8 == 0 && c.page_stride % 8 == 0 &&
+         c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.q.data) & 3) == 0 &&
+         p.q.row_stride % 2 == 0 && p.q.head_stride % 2 == 0;
+}
+
+CoreShape mma_attention_shape(const AttnDesc& p) {
+  const int hd = p.cache.head_dim;
+  if (p.group <= 8)
+    return hd <= 64 ? shape_of<MmaCore<64, 1>>() : (hd <= 128 ? shape_of<MmaCore<128, 1>>() : shape_of<MmaCore<256, 1>>());
+  return hd <= 64 ? shape_of<MmaCore<64, 2>>() : (hd <= 128 ? shape_of<MmaCore<128, 2>>() : shape_of<MmaCore<256, 2>>());
+}
+
+cudaError_t launch_attention_mma(const AttnDesc& p, void* workspace, cudaStream_t s) {
+  if (p.cache.head_dim <= 64) return by_group<64>(p, workspace, s);
+  if (p.cache.head_dim <= 128) return by_group<128>(p, workspace, s);
+  return by_group<256>(p, workspace, s);
+}
+
+// The workspace is sized for either core, so that it depends on shapes only
+// and not on which one the alignments allow.
+size_t attention_workspace_bytes(const AttnDesc& p) {
+  const CoreShape g = generic_attention_shape(p);
+  size_t bytes = workspace_parts(g, units_of(g, p, kMaxSmsForWorkspace)).bytes;
+  if (p.dtype == LORA_DTYPE_BF16) {
+    const CoreShape m = mma_attention_shape(p);
+    bytes = std::max(bytes, workspace_parts(m, units_of(m, p, kMaxSmsForWorkspace)).bytes);
+  }
+  return bytes;
+}
+
+cudaError_t launch_attention(const AttnDesc& p, void* workspace, cudaStream_t s) {
+  return mma_attention_ok(p) ? launch_attention_mma(p, workspace, s) : launch_attention_generic(p, workspace, s);
+}
+
+}  // namespace lora

@@ -237,7 +237,7 @@ struct AttnDesc {
   float* partial;  // [2 * units, CH, HD] its unnormalised output
 };
 size_t attention_workspace_bytes(const AttnDesc& p);
-cudaError_t launch_attention(AttnDesc p, void* workspace, cudaStream_t s);
+cudaError_t launch_attention(const AttnDesc& p, void* workspace, cudaStream_t s);
 
 // Page copies of caches with one geometry.  kv: num_caches pairs {k, v}.
 cudaError_t launch_copy_pages(const CacheDesc& geometry, int dtype, const lora_kv_cache_t* caches, int num_caches,

@@ -350,6 +350,8 @@ def test_attention(case):
     dtype, lens, H, Hk, hd, ps, order = case
     a = make_attention(lens, H, Hk, hd, ps, dtype, order)
     out, lse = run_attention(a)
+    core = lk.PATH_MMA_ATTENTION if dtype == BF and hd % 8 == 0 and order != "gap" else lk.PATH_GENERIC_ATTENTION
+    assert lk.lora_last_call_path()[0] & ~lk.PATH_JOIN == core
     check_attention(a, out, lse, 1.0 / hd ** 0.5, rows=range(0, len(lens), max(1, len(lens) // 40)))
 
 
