@@ -144,6 +144,9 @@ def test_rope_append(case, in_place):
                           cache=lk.KVCache(kc, vc),
                           cache_rows=torch.tensor(rows, dtype=torch.int32, device="cuda"), q_weight=qw, k_weight=kw)
     lk.lora_rope_append(prob)
+    v_elems = 8 if dtype == BF else 4      # per 16 bytes
+    fast = fused and order != "gap" and hd % v_elems == 0 and rot % (v_elems if inter else 2 * v_elems) == 0
+    assert lk.lora_last_call_path() == (lk.PATH_ROPE if fast else lk.PATH_GENERIC_ROPE, 1)
     torch.cuda.synchronize()
     ascale = float(np.float32(ascale))
     eps = float(np.float32(1e-6))
