@@ -180,6 +180,31 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
   return o;
 }
 
+// The same for two products, and two fused multiply-adds.
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  float2 o;
+  asm("{\n\t.reg .b64 pa, pb, pr;\n\t"
+      "mov.b64 pa, {%2, %3};\n\t"
+      "mov.b64 pb, {%4, %5};\n\t"
+      "mul.rn.f32x2 pr, pa, pb;\n\t"
+      "mov.b64 {%0, %1}, pr;\n\t}"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return o;
+}
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  float2 o;
+  asm("{\n\t.reg .b64 pa, pb, pc, pr;\n\t"
+      "mov.b64 pa, {%2, %3};\n\t"
+      "mov.b64 pb, {%4, %5};\n\t"
+      "mov.b64 pc, {%6, %7};\n\t"
+      "fma.rn.f32x2 pr, pa, pb, pc;\n\t"
+      "mov.b64 {%0, %1}, pr;\n\t}"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return o;
+}
+
 // Two floats rounded to nearest-even bf16 in one conversion, `lo` in the
 // low half (the same bits as two separate roundings, packed).
 __device__ __forceinline__ uint32_t round_pack_bf16x2(float lo, float hi) {

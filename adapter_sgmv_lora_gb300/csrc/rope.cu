@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace lora {
 namespace {
@@ -120,38 +121,63 @@ __global__ void __launch_bounds__(kGenericWarps * 32) rope_generic_kernel(const 
 }
 
 // 16-byte accesses.  A head is LPH lanes (a power of two) of two 16-byte
-// chunks each.  In the halves layout the two chunks of a rotating lane are
-// partners, chunk j of the first half and chunk j of the second, so a pair
-// meets in one lane; interleaved pairs lie within a chunk.  A lane keeps its
-// chunk position for every head it works on, so the cosines and sines of its
-// pairs stay in registers.  Block = one token (times gridDim.y shares of its
-// heads); the rows of the next heads are loaded before the present ones are
-// rotated, and the first before the angles are worked out.
-constexpr int kRopeThreads = 256;
+// chunks each, so a warp holds a group of 32 / LPH heads.  In the halves
+// layout the two chunks of a rotating lane are partners, chunk j of the first
+// half and chunk j of the second, so a pair meets in one lane; interleaved
+// pairs lie within a chunk.  A lane keeps its chunk position for every head it
+// works on, so the cosines and sines of its pairs stay in registers.
+//
+// A warp takes one token, or a share of its groups, and works the angles out
+// for itself: no block barrier.  Query, key and value heads are grouped apart,
+// so what a group needs is the same for the whole warp.  kRopeBatch groups
+// are loaded at a time (the first before the angles): 4 KB a warp in flight.
+// Products go two to an instruction (f32x2).
+constexpr int kRopeWarps = 4;  // per block
+constexpr int kRopeBatch = 4;
 
+// Four chunk elements (two for fp32) as fp32, and back.
 template <typename T>
-struct Chunk {
-  static constexpr int V = 16 / sizeof(T);
-  uint4 bits;
-  __device__ __forceinline__ float get(int e) const { return to_f(reinterpret_cast<const T*>(&bits)[e]); }
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void open(const uint4& b, float* v) {
+    const unsigned w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 close(const float* v) {
+    return make_uint4(round_pack_bf16x2(v[0], v[1]), round_pack_bf16x2(v[2], v[3]), round_pack_bf16x2(v[4], v[5]),
+                      round_pack_bf16x2(v[6], v[7]));
+  }
+};
+template <>
+struct Chunk<float> {
+  static constexpr int V = 4;
+  static __device__ __forceinline__ void open(const uint4& b, float* v) {
+    v[0] = __uint_as_float(b.x);
+    v[1] = __uint_as_float(b.y);
+    v[2] = __uint_as_float(b.z);
+    v[3] = __uint_as_float(b.w);
+  }
+  static __device__ __forceinline__ uint4 close(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
 };
 
-__device__ __forceinline__ uint4 pack_chunk(const float* v, __nv_bfloat16) {
-  __nv_bfloat162 r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  return *reinterpret_cast<const uint4*>(r);
-}
-__device__ __forceinline__ uint4 pack_chunk(const float* v, float) {
-  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-}
-
-template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeDesc p, int lph_log2) {
+template <typename T, bool INTERLEAVED, bool NORM>
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeDesc p, int lph_log2,
+                                                               int shares) {
   constexpr int V = Chunk<T>::V;
-  __shared__ float2 cs[LORA_MAX_HEAD_DIM / 2];
-  const int t = blockIdx.x;
-  const int lph = 1 << lph_log2, j = threadIdx.x & (lph - 1);
+  __shared__ float2 s_cs[kRopeWarps][LORA_MAX_HEAD_DIM / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long task = (long long)blockIdx.x * kRopeWarps + warp;
+  const int t = (int)(task / shares), share = (int)(task - (long long)t * shares);
+  if (t >= p.T) return;  // the whole warp
+  const int lph = 1 << lph_log2, j = lane & (lph - 1), sub = lane >> lph_log2, at_once = 32 >> lph_log2;
   const int half = p.rot / 2, chunks = p.hd / V, turning = half / V;  // turning: partner pairs (halves layout)
   int c0 = 2 * j, c1 = 2 * j + 1;
   if (!INTERLEAVED && j < turning) {
@@ -159,108 +185,127 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     c1 = j + turning;
   }
   const bool has0 = c0 < chunks, has1 = c1 < chunks;
-  const int heads = p.H + p.Hk + (p.cache_rows ? p.Hk : 0);
-  const int step = gridDim.y * (kRopeThreads >> lph_log2);
+  const int q_groups = (p.H + at_once - 1) >> (5 - lph_log2), k_groups = (p.Hk + at_once - 1) >> (5 - lph_log2);
+  const int groups = q_groups + (p.cache_rows ? 2 : 1) * k_groups;
 
-  auto load = [&](int h, Chunk<T>& x0, Chunk<T>& x1) {
-    if (h >= heads) return;
-    const HeadsDesc& in = h < p.H ? p.q : (h < p.H + p.Hk ? p.k : p.v);
-    const int hh = h < p.H ? h : (h < p.H + p.Hk ? h - p.H : h - p.H - p.Hk);
-    const uint4* row =
-        reinterpret_cast<const uint4*>(static_cast<const T*>(in.data) + t * in.row_stride + hh * in.head_stride);
-    if (has0) x0.bits = row[c0];
-    if (has1) x1.bits = row[c1];
+  // This lane's head of group g, among those of its kind.
+  auto head_of = [&](int g) {
+    return (g < q_groups ? g : g - q_groups - (g < q_groups + k_groups ? 0 : k_groups)) * at_once + sub;
   };
-  int h = blockIdx.y * (kRopeThreads >> lph_log2) + (threadIdx.x >> lph_log2);
-  Chunk<T> x0{}, x1{}, n0{}, n1{};
-  load(h, x0, x1);
-  long long row = cache_offset(p, t);
-  for (int i = threadIdx.x; i < half; i += kRopeThreads) cs[i] = rope_cos_sin(p, p.positions[t], i);
-  __syncthreads();
+  auto load = [&](int g, uint4 (&x)[2]) {
+    if (g >= groups) return;
+    const bool is_q = g < q_groups;
+    const HeadsDesc& in = is_q ? p.q : (g < q_groups + k_groups ? p.k : p.v);
+    const int h = head_of(g);
+    if (h >= (is_q ? p.H : p.Hk)) return;
+    const uint4* row =
+        reinterpret_cast<const uint4*>(static_cast<const T*>(in.data) + t * in.row_stride + h * in.head_stride);
+    if (has0) x[0] = row[c0];
+    if (has1) x[1] = row[c1];
+  };
+  uint4 x[kRopeBatch][2] = {};
+#pragma unroll
+  for (int i = 0; i < kRopeBatch; ++i) load(share + i * shares, x[i]);
+  const long long row = cache_offset(p, t);
+  float2* cs = s_cs[warp];
+  if (half > 0) {
+    const int position = p.positions[t];
+    for (int i = lane; i < half; i += 32) cs[i] = rope_cos_sin(p, position, i);
+    __syncwarp();
+  }
   // Halves: V pairs; interleaved: V / 2 of each chunk.
-  float2 w[V];
+  float c[V], s[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     const int i = INTERLEAVED ? (e < V / 2 ? c0 : c1) * (V / 2) + e % (V / 2) : c0 * V + e;
-    w[e] = i < half ? cs[i] : make_float2(1.f, 0.f);
+    const float2 w = i < half ? cs[i] : make_float2(1.f, 0.f);
+    c[e] = w.x;
+    s[e] = w.y;
   }
-  const bool turn = INTERLEAVED || j < turning;
 
-  for (; h - (int)(threadIdx.x >> lph_log2) < heads; h += step) {
-    load(h + step, n0, n1);
-    const bool mine = h < heads;
-    const bool is_v = h >= p.H + p.Hk, is_q = h < p.H;
-    const T* weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-    float a[V], b[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      a[e] = x0.get(e);
-      b[e] = x1.get(e);
-    }
-    if (p.q_weight || p.k_weight) {  // uniform, and so is the loop: the whole warp is here
-      float sum = 0.f;               // chunks past the head are zero
-#pragma unroll
-      for (int e = 0; e < V; ++e) sum = fmaf(a[e], a[e], fmaf(b[e], b[e], sum));
-      for (int m = lph / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-      if (weight && !is_v) {
-        const float r = rsqrtf(sum / p.hd + p.eps);
-        Chunk<T> g0{}, g1{};
-        if (has0) g0.bits = reinterpret_cast<const uint4*>(weight)[c0];
-        if (has1) g1.bits = reinterpret_cast<const uint4*>(weight)[c1];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          a[e] *= r * g0.get(e);
-          b[e] *= r * g1.get(e);
-        }
-      }
-    }
-    if (turn && !is_v) {
-      if constexpr (INTERLEAVED) {
-        // Chunks past the rotated part are skipped, not turned by 0: an
-        // infinite neighbour would come out as NaN.
+  auto work = [&](int g, const uint4 (&x)[2]) {
+    const bool is_q = g < q_groups, is_v = g >= q_groups + k_groups;
+    const int h = head_of(g);
+    uint4 r[2] = {x[0], x[1]};
+    const T* weight = NORM ? static_cast<const T*>(is_q ? p.q_weight : p.k_weight) : nullptr;
+    if (!is_v && (half > 0 || weight)) {  // else the bits go through as they are
+      float a[V], b[V];
+      Chunk<T>::open(x[0], a);
+      Chunk<T>::open(x[1], b);
+      if (NORM && weight) {
+        float2 sum2 = make_float2(0.f, 0.f);  // chunks past the head are zero
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
-          const float2 wa = w[e / 2], wb = w[V / 2 + e / 2];
-          const float a0 = a[e], a1 = a[e + 1], b0 = b[e], b1 = b[e + 1];
-          if (c0 * V < p.rot) {
-            a[e] = a0 * wa.x - a1 * wa.y;
-            a[e + 1] = a0 * wa.y + a1 * wa.x;
-          }
-          if (c1 * V < p.rot) {
-            b[e] = b0 * wb.x - b1 * wb.y;
-            b[e + 1] = b0 * wb.y + b1 * wb.x;
-          }
+          sum2 = fma_f32x2(make_float2(a[e], a[e + 1]), make_float2(a[e], a[e + 1]), sum2);
+          sum2 = fma_f32x2(make_float2(b[e], b[e + 1]), make_float2(b[e], b[e + 1]), sum2);
         }
-      } else {
+        float sum = sum2.x + sum2.y;
+        for (int m = lph / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        const float n = rsqrtf(sum / p.hd + p.eps);
+        uint4 g0 = {}, g1 = {};
+        if (has0) g0 = reinterpret_cast<const uint4*>(weight)[c0];
+        if (has1) g1 = reinterpret_cast<const uint4*>(weight)[c1];
+        float wa[V], wb[V];
+        Chunk<T>::open(g0, wa);
+        Chunk<T>::open(g1, wb);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float a0 = a[e], b0 = b[e];
-          a[e] = a0 * w[e].x - b0 * w[e].y;
-          b[e] = a0 * w[e].y + b0 * w[e].x;
+          a[e] *= n * wa[e];
+          b[e] *= n * wb[e];
         }
       }
-    }
-    uint4 r0 = x0.bits, r1 = x1.bits;
-    if ((turn || weight) && !is_v) {  // else the bits go through as they are
-      r0 = pack_chunk(a, T());
-      r1 = pack_chunk(b, T());
-    }
-    if (mine) {
-      const int hh = is_q ? h : (is_v ? h - p.H - p.Hk : h - p.H);
-      auto store = [&](void* base, long long off) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(base) + off);
-        if (has0) dst[c0] = r0;
-        if (has1) dst[c1] = r1;
-      };
-      if (is_q) {
-        store(p.q_out.data, t * p.q_out.row_stride + hh * p.q_out.head_stride);
-      } else {
-        if (!is_v && p.k_out.data) store(p.k_out.data, t * p.k_out.row_stride + hh * p.k_out.head_stride);
-        if (row >= 0) store(is_v ? p.cache.v : p.cache.k, row + hh * p.cache.head_stride);
+      // Chunks past the rotated part are skipped, not turned by 0: an
+      // infinite neighbour would come out as NaN.
+      if constexpr (INTERLEAVED) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float a0 = a[e], a1 = a[e + 1], b0 = b[e], b1 = b[e + 1];
+          const float ca = c[e / 2], sa = s[e / 2], cb = c[V / 2 + e / 2], sb = s[V / 2 + e / 2];
+          if (c0 * V < p.rot) {
+            a[e] = a0 * ca - a1 * sa;
+            a[e + 1] = a0 * sa + a1 * ca;
+          }
+          if (c1 * V < p.rot) {
+            b[e] = b0 * cb - b1 * sb;
+            b[e + 1] = b0 * sb + b1 * cb;
+          }
+        }
+      } else if (j < turning) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float2 a2 = make_float2(a[e], a[e + 1]), b2 = make_float2(b[e], b[e + 1]);
+          const float2 c2 = make_float2(c[e], c[e + 1]), s2 = make_float2(s[e], s[e + 1]);
+          const float2 ra = fma_f32x2(make_float2(-b2.x, -b2.y), s2, mul_f32x2(a2, c2));
+          const float2 rb = fma_f32x2(b2, c2, mul_f32x2(a2, s2));
+          a[e] = ra.x;
+          a[e + 1] = ra.y;
+          b[e] = rb.x;
+          b[e + 1] = rb.y;
+        }
       }
+      r[0] = Chunk<T>::close(a);
+      r[1] = Chunk<T>::close(b);
     }
-    x0 = n0;
-    x1 = n1;
+    if (h >= (is_q ? p.H : p.Hk)) return;
+    auto store = [&](void* base, long long off) {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(base) + off);
+      if (has0) dst[c0] = r[0];
+      if (has1) dst[c1] = r[1];
+    };
+    if (is_q) {
+      store(p.q_out.data, t * p.q_out.row_stride + h * p.q_out.head_stride);
+    } else {
+      if (!is_v && p.k_out.data) store(p.k_out.data, t * p.k_out.row_stride + h * p.k_out.head_stride);
+      if (row >= 0) store(is_v ? p.cache.v : p.cache.k, row + h * p.cache.head_stride);
+    }
+  };
+#pragma unroll 1
+  for (int g = share; g < groups; g += kRopeBatch * shares) {
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i)
+      if (g + i * shares < groups) work(g + i * shares, x[i]);
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) load(g + (kRopeBatch + i) * shares, x[i]);
   }
 }
 
@@ -293,23 +338,34 @@ cudaError_t launch_rope(const RopeDesc& p, cudaStream_t s) {
   const int V = p.dtype == LORA_DTYPE_BF16 ? 8 : 4;
   int lph_log2 = 0;
   while ((2 << lph_log2) < p.hd / V) ++lph_log2;
-  const int at_once = fast ? kRopeThreads >> lph_log2 : kGenericWarps;  // heads a block works on at a time
-  // A block takes one token; its heads are shared by several blocks while the
-  // batch is too small to give every SM some.
+  const int at_once = fast ? 32 >> lph_log2 : kGenericWarps;  // heads a warp (or block) works on at a time
   const int sms = device_sm_count();
-  int split = (heads + at_once - 1) / at_once;
-  while (split > 1 && (long long)p.T * split > 8LL * sms) split = (split + 1) / 2;
-  const dim3 grid(p.T, split);
   const bool bf = p.dtype == LORA_DTYPE_BF16, inter = p.layout == LORA_ROPE_INTERLEAVED;
   if (!fast) {
+    // Few tokens: their heads are shared out until every SM has work.
+    int split = (heads + at_once - 1) / at_once;
+    while (split > 1 && (long long)p.T * split > 8LL * sms) split = (split + 1) / 2;
+    const dim3 grid(p.T, split);
     if (bf) rope_generic_kernel<__nv_bfloat16><<<grid, kGenericWarps * 32, 0, s>>>(p);
     else rope_generic_kernel<float><<<grid, kGenericWarps * 32, 0, s>>>(p);
     return noted(cudaGetLastError(), LORA_PATH_GENERIC_ROPE);
   }
-  if (bf && inter) rope_kernel<__nv_bfloat16, true><<<grid, kRopeThreads, 0, s>>>(p, lph_log2);
-  else if (bf) rope_kernel<__nv_bfloat16, false><<<grid, kRopeThreads, 0, s>>>(p, lph_log2);
-  else if (inter) rope_kernel<float, true><<<grid, kRopeThreads, 0, s>>>(p, lph_log2);
-  else rope_kernel<float, false><<<grid, kRopeThreads, 0, s>>>(p, lph_log2);
+  const int groups = (p.H + at_once - 1) / at_once + (p.cache_rows ? 2 : 1) * ((p.Hk + at_once - 1) / at_once);
+  const int shares = (long long)p.T * groups <= 16LL * sms ? groups : (groups + kRopeBatch - 1) / kRopeBatch;
+  const unsigned grid = (unsigned)(((long long)p.T * shares + kRopeWarps - 1) / kRopeWarps);
+  constexpr int threads = kRopeWarps * 32;
+  auto run = [&](auto kernel) { kernel<<<grid, threads, 0, s>>>(p, lph_log2, shares); };
+  if (p.q_weight || p.k_weight) {
+    if (bf && inter) run(rope_kernel<__nv_bfloat16, true, true>);
+    else if (bf) run(rope_kernel<__nv_bfloat16, false, true>);
+    else if (inter) run(rope_kernel<float, true, true>);
+    else run(rope_kernel<float, false, true>);
+  } else {
+    if (bf && inter) run(rope_kernel<__nv_bfloat16, true, false>);
+    else if (bf) run(rope_kernel<__nv_bfloat16, false, false>);
+    else if (inter) run(rope_kernel<float, true, false>);
+    else run(rope_kernel<float, false, false>);
+  }
   return noted(cudaGetLastError(), LORA_PATH_ROPE);
 }
 
