@@ -55,6 +55,29 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 // nothing; an infinite or NaN score stays visible as NaN.
 __device__ __forceinline__ float weight_of(float a, float m) { return a == kNegInf ? 0.f : exp2f(a - m); }
 
+// The first n (all, if n >= 4) of four neighbouring outputs; one store where
+// they are whole and aligned.
+__device__ __forceinline__ void store4(float* dst, float4 v, int n) {
+  if (n >= 4 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+    *reinterpret_cast<float4*>(dst) = v;
+    return;
+  }
+  const float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < n) dst[e] = r[e];
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* dst, float4 v, int n) {
+  if (n >= 4 && (reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(round_pack_bf16x2(v.x, v.y), round_pack_bf16x2(v.z, v.w));
+    return;
+  }
+  const float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < n) dst[e] = __float2bfloat16_rn(r[e]);
+}
+
 template <int TT>
 __device__ __forceinline__ int tiles_of(const AttnDesc& p, int len) {
   if (len < 0 || len > p.max_len) return 0;  // refused: LORA_DEV_BAD_LENGTH
@@ -215,7 +238,10 @@ struct TileCursor {
 //   tile), EXTRA_BYTES (its own shared memory per CTA)
 //   Core(p, extra)            before anything else, all threads
 //   load(p, stage, off)       this warp's copies of one tile into a stage
-//   begin(p, seq, head0, heads)  new stream: its queries (all threads)
+//   fetch(p, seq, head0, heads)  starts loading a stream's queries: this
+//                             thread's share, into registers
+//   pass_on()                 puts that share into shared memory
+//   begin(p, heads)           new stream: its queries are in shared memory
 //   tile(p, stage, n)         one tile, its first n tokens
 //   put(part, o, s)           this warp's O [COMB][HD + 4] and (m, l) [COMB] of part
 template <class Core>
@@ -243,25 +269,21 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   const Piece piece = s_piece;
-  if (threadIdx.x == 0) {
-    // A unit that starts inside a stream whose beginning lies in the unit
-    // before it lists that stream for the join: how many units share it.
-    int4 split = make_int4(0, 0, 0, 0);
-    if (piece.lo < piece.hi) {
-      Segments<TT> sg;
-      sg.first(p, piece);
-      const long long begin = piece.lo - sg.t0, end = begin + sg.n;
-      if (sg.t0 > 0 && piece_start(piece.total, piece.units, u - 1) <= begin) {
-        // First unit that starts at or after the stream's end.
-        const long long v = (end * piece.units + piece.total - 1) / piece.total;
-        split = make_int4(sg.seq, sg.stream, (int)v - u + 1, 0);
-      }
-    }
-    p.splits[u] = split;
-  }
   if (piece.lo >= piece.hi) return;
 
+  // The next segment's queries travel through registers (each thread a share)
+  // into the core's shared buffer while the present segment is worked on.
+  auto heads_of = [&](const Segments<TT>& sg, int* head0) {
+    const int kv_head = sg.stream / p.chunks;
+    const int in_group = (sg.stream - kv_head * p.chunks) * CH;  // first head of the chunk
+    *head0 = kv_head * p.group + in_group;
+    return min(CH, p.group - in_group);
+  };
+  Segments<TT> seg;
+  seg.first(p, piece);
   Core core(p, extra);
+  int head0, heads = heads_of(seg, &head0);
+  core.fetch(p, seg.seq, head0, heads);
   uint8_t* my_ring = ring + warp * STAGES * Core::STAGE_BYTES;
   TileCursor<TT, W> cur;
   cur.first(p, piece, warp);
@@ -279,16 +301,19 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
 #pragma unroll 1
   for (int s = 0; s < STAGES; ++s) load(s);
 
+  core.pass_on();
+  __syncthreads();
   int stage = 0;
-  Segments<TT> seg;
-  seg.first(p, piece);
 #pragma unroll 1
-  for (; seg.valid; seg.next(p)) {
-    const int kv_head = seg.stream / p.chunks;
-    const int in_group = (seg.stream - kv_head * p.chunks) * CH;  // first head of the chunk
-    const int heads = min(CH, p.group - in_group);
-    const int head0 = kv_head * p.group + in_group;
-    core.begin(p, seg.seq, head0, heads);
+  while (true) {
+    core.begin(p, heads);
+    Segments<TT> after = seg;
+    after.next(p);
+    int after_head0 = 0, after_heads = 0;
+    if (after.valid) {
+      after_heads = heads_of(after, &after_head0);
+      core.fetch(p, after.seq, after_head0, after_heads);
+    }
     bool bad = false;
 #pragma unroll 1
     for (int t = seg.t0 + warp; t < seg.t1; t += W) {
@@ -307,6 +332,7 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
     for (int part = 0; part < CH / COMB; ++part) {
       const int part_heads = min(COMB, heads - part * COMB);
       if (part_heads <= 0) break;
+      if (part > 0) __syncthreads();
       core.put(part, comb + warp * COMB * PITCH, stat + warp * COMB);
       __syncwarp();
       if (bad && lane < COMB) stat[warp * COMB + lane].y = -1.f;
@@ -342,67 +368,125 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
         } else if (any_bad) {
           if (d == 0) atomicOr(p.status, LORA_DEV_BAD_PAGE);
         } else {
-          T* out = static_cast<T*>(p.out.data) + seg.seq * p.out.row_stride + (head0 + hc) * p.out.head_stride;
-          const float r[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (d + e < p.cache.head_dim) out[d + e] = from_f<T>(l == 0.f ? 0.f : r[e] / l);
+          T* out = static_cast<T*>(p.out.data) + seg.seq * p.out.row_stride + (head0 + hc) * p.out.head_stride + d;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          store4(out, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), p.cache.head_dim - d);
           if (d == 0 && p.lse) p.lse[(long long)seg.seq * p.num_heads + head0 + hc] = (m + log2f(l)) * kLn2;
         }
       }
-      __syncthreads();
     }
+    if (!after.valid) break;
+    core.pass_on();
+    __syncthreads();  // the join's buffer is free, the queries are there
+    seg = after;
+    head0 = after_head0;
+    heads = after_heads;
   }
   cp_async_wait<0>();
 }
 
-// Joins the partial results of the streams that several units share: block u
-// takes the stream that unit u lists, one warp per query head.  Partial 0 is
-// the end of unit u - 1, partial i the beginning of unit u - 1 + i.
-constexpr int kJoinWarps = 8;
+// Joins the partial results of the streams that several units share.  Block
+// (u, h): the stream that unit u starts inside of and unit u - 1 begins, and
+// the h-th query head of it; its warps share the partial results out and are
+// joined in warp order.  Partial 0 is the end of unit u - 1, partial i the
+// beginning of unit u - 1 + i.  Which stream that is follows from the lengths
+// alone, so it is found while the units still run; after them the statistics
+// and the outputs are one round trip to memory.
+constexpr int kJoinWarps = 4, kJoinBatch = 8;
 
-template <typename T, int HD, int CH>
+template <class Core>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ AttnDesc p) {
-  pdl_wait();
-  const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 split = p.splits[u];
-  if (split.z == 0) return;
+  using T = typename Core::T;
+  constexpr int TT = Core::TT, HD = Core::HD, CH = Core::CH, VPL = HD / 32;
+  __shared__ int4 s_split;
+  __shared__ float s_o[kJoinWarps][HD];
+  __shared__ float s_l[kJoinWarps];
+  const int u = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    const Piece piece = locate_piece<TT, Core::W>(p, u, gridDim.x);
+    int4 split = make_int4(0, 0, 0, 0);
+    if (piece.lo < piece.hi) {
+      Segments<TT> sg;
+      sg.first(p, piece);
+      const long long begin = piece.lo - sg.t0, end = begin + sg.n;
+      if (sg.t0 > 0 && piece_start(piece.total, piece.units, u - 1) <= begin) {
+        // First unit that starts at or after the stream's end.
+        const long long v = (end * piece.units + piece.total - 1) / piece.total;
+        split = make_int4(sg.seq, sg.stream, (int)v - u + 1, 0);
+      }
+    }
+    if (lane == 0) s_split = split;
+  }
+  __syncthreads();
+  pdl_wait();  // every block: the grid must not be over before the units are
+  const int4 split = s_split;
   const int kv_head = split.y / p.chunks;
   const int in_group = (split.y - kv_head * p.chunks) * CH;
-  const int heads = min(CH, p.group - in_group);
-  auto slot = [&](int i) { return (long long)(i == 0 ? 2 * (u - 1) + 1 : 2 * (u - 1 + i)); };
-  for (int h = warp; h < heads; h += kJoinWarps) {
-    float m = kNegInf;
-    bool bad = false;
-    for (int i = lane; i < split.z; i += 32) {
-      const float2 st = p.stats[slot(i) * CH + h];
-      m = fmaxf(m, st.x);
-      bad |= st.y < 0.f;
-    }
+  if (split.z == 0 || h >= p.group - in_group) return;
+  auto slot = [&](int i) { return (long long)(i == 0 ? 2 * (u - 1) + 1 : 2 * (u - 1 + i)) * CH + h; };
+  // This warp's first partial results are on their way before the statistics
+  // are looked at.
+  float v[kJoinBatch][VPL], st_l[kJoinBatch], st_m[kJoinBatch];
+  auto load = [&](int from) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (__any_sync(0xffffffffu, bad)) {
-      if (lane == 0) atomicOr(p.status, LORA_DEV_BAD_PAGE);
-      continue;
-    }
-    float l = 0.f;
-    float o[HD / 32] = {};
-#pragma unroll 4
-    for (int i = 0; i < split.z; ++i) {
-      const float2 st = p.stats[slot(i) * CH + h];
-      const float f = weight_of(st.x, m);
-      const float* v = p.partial + (slot(i) * CH + h) * HD + lane;
-      l = fmaf(st.y, f, l);
+    for (int b = 0; b < kJoinBatch; ++b) {
+      const int i = from + b * kJoinWarps;
+      st_m[b] = kNegInf;
+      st_l[b] = 0.f;
 #pragma unroll
-      for (int e = 0; e < HD / 32; ++e) o[e] = fmaf(v[e * 32], f, o[e]);
-    }
-    const int head = kv_head * p.group + in_group + h;
-    T* out = static_cast<T*>(p.out.data) + split.x * p.out.row_stride + head * p.out.head_stride;
+      for (int e = 0; e < VPL; ++e) v[b][e] = 0.f;
+      if (i < split.z) {
+        const float2 st = p.stats[slot(i)];
+        st_m[b] = st.x;
+        st_l[b] = st.y;
+        const float* src = p.partial + slot(i) * HD + lane;
 #pragma unroll
-    for (int e = 0; e < HD / 32; ++e)
-      if (lane + e * 32 < p.cache.head_dim) out[lane + e * 32] = from_f<T>(l == 0.f ? 0.f : o[e] / l);
-    if (lane == 0 && p.lse) p.lse[(long long)split.x * p.num_heads + head] = (m + log2f(l)) * kLn2;
+        for (int e = 0; e < VPL; ++e) v[b][e] = src[e * 32];
+      }
+    }
+  };
+  load(warp);
+  float m = kNegInf;
+  bool bad = false;
+  for (int i = lane; i < split.z; i += 32) {
+    const float2 st = p.stats[slot(i)];
+    m = fmaxf(m, st.x);
+    bad |= st.y < 0.f;
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (__any_sync(0xffffffffu, bad)) {  // the same in every warp
+    if (threadIdx.x == 0) atomicOr(p.status, LORA_DEV_BAD_PAGE);
+    return;
+  }
+  float l = 0.f, o[VPL] = {};
+  for (int from = warp; from < split.z; from += kJoinBatch * kJoinWarps) {
+    if (from != warp) load(from);
+#pragma unroll
+    for (int b = 0; b < kJoinBatch; ++b) {
+      const float f = weight_of(st_m[b], m);
+      l = fmaf(st_l[b], f, l);
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) o[e] = fmaf(v[b][e], f, o[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VPL; ++e) s_o[warp][e * 32 + lane] = o[e];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) l += s_l[w];
+  const int head = kv_head * p.group + in_group + h;
+  T* out = static_cast<T*>(p.out.data) + split.x * p.out.row_stride + head * p.out.head_stride;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  for (int d = threadIdx.x; d < p.cache.head_dim; d += kJoinWarps * 32) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) sum += s_o[w][d];
+    out[d] = from_f<T>(sum * inv);
+  }
+  if (threadIdx.x == 0 && p.lse) p.lse[(long long)split.x * p.num_heads + head] = (m + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------- host --
@@ -427,13 +511,12 @@ inline int units_of(const CoreShape& c, const AttnDesc& p, int sms) {
 inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct WorkspaceParts {
-  size_t stats, partial, bytes;  // offsets (splits come first), and the whole
+  size_t partial, bytes;  // offset of the outputs (the statistics come first), and the whole
 };
 
 inline WorkspaceParts workspace_parts(const CoreShape& c, int units) {
   WorkspaceParts w;
-  w.stats = round256((size_t)units * sizeof(int4));
-  w.partial = w.stats + round256((size_t)2 * units * c.CH * sizeof(float2));
+  w.partial = round256((size_t)2 * units * c.CH * sizeof(float2));
   w.bytes = w.partial + round256((size_t)2 * units * c.CH * c.HD * sizeof(float));
   return w;
 }
@@ -467,15 +550,14 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
   const int units = units_of(c, p, std::min(device_sm_count(), kMaxSmsForWorkspace));
   const WorkspaceParts w = workspace_parts(c, units);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.splits = reinterpret_cast<int4*>(ws);
-  p.stats = reinterpret_cast<float2*>(ws + w.stats);
+  p.stats = reinterpret_cast<float2*>(ws);
   p.partial = reinterpret_cast<float*>(ws + w.partial);
   cudaError_t e = allow_smem<Core>((int)smem);
   if (e != cudaSuccess) return e;
   attention_kernel<Core><<<units, Core::W * 32, smem, s>>>(p);
   if ((e = noted(cudaGetLastError(), path)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units);
+  cfg.gridDim = dim3(units, std::min(Core::CH, p.group));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -483,8 +565,7 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return noted(cudaLaunchKernelEx(&cfg, attention_join_kernel<typename Core::T, Core::HD, Core::CH>, p),
-               LORA_PATH_JOIN);
+  return noted(cudaLaunchKernelEx(&cfg, attention_join_kernel<Core>, p), LORA_PATH_JOIN);
 }
 
 // attention_mma.cu: bf16 on the tensor cores.  mma_attention_ok: the shapes

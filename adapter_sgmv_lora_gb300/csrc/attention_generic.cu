@@ -17,9 +17,9 @@ namespace {
 template <typename T_, int HD_, int CH_, bool ASYNC>
 struct GenericCore {
   using T = T_;
-  static constexpr int TT = 8, W = 4, HD = HD_, CH = CH_, COMB = CH_;
+  static constexpr int TT = 8, W = 4, HD = HD_, CH = CH_, COMB = CH_ < 4 ? CH_ : 4;
   static constexpr int STAGE_BYTES = 2 * TT * HD * 4;
-  static constexpr int STAGES = 2;
+  static constexpr int STAGES = HD == 64 ? 6 : 3;
   static constexpr int CTAS = HD <= 128 ? 2 : 1;
   static constexpr int VPL = HD / 32;  // output columns per lane
   static constexpr int EXTRA_BYTES = (CH * HD + W * TT * CH) * 4;
@@ -30,6 +30,7 @@ struct GenericCore {
   float scale;
   int heads;
   float m[CH], l[CH], o[CH][VPL];
+  float next_q[(CH * HD + W * 32 - 1) / (W * 32)];
 
   __device__ __forceinline__ GenericCore(const AttnDesc& p, uint8_t* extra)
       : q(reinterpret_cast<float*>(extra)),
@@ -68,13 +69,24 @@ struct GenericCore {
     }
   }
 
-  __device__ __forceinline__ void begin(const AttnDesc& p, int seq, int head0, int heads_) {
-    heads = heads_;
-    const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride;
-    for (int i = threadIdx.x; i < CH * HD; i += W * 32) {
-      const int h = i / HD, d = i % HD;
-      q[i] = h < heads && d < p.cache.head_dim ? to_f(src[(head0 + h) * p.q.head_stride + d]) : 0.f;
+  static constexpr int Q_PER_THREAD = (CH * HD + W * 32 - 1) / (W * 32);
+  __device__ __forceinline__ void fetch(const AttnDesc& p, int seq, int head0, int heads_) {
+    const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride + head0 * p.q.head_stride;
+#pragma unroll
+    for (int i = 0; i < Q_PER_THREAD; ++i) {
+      const int e = i * W * 32 + threadIdx.x, h = e / HD, d = e % HD;
+      next_q[i] = h < heads_ && d < p.cache.head_dim ? to_f(src[h * p.q.head_stride + d]) : 0.f;
     }
+  }
+
+  __device__ __forceinline__ void pass_on() const {
+#pragma unroll
+    for (int i = 0; i < Q_PER_THREAD; ++i)
+      if (i * W * 32 + threadIdx.x < CH * HD) q[i * W * 32 + threadIdx.x] = next_q[i];
+  }
+
+  __device__ __forceinline__ void begin(const AttnDesc&, int heads_) {
+    heads = heads_;
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
       m[h] = kNegInf;
@@ -82,7 +94,6 @@ struct GenericCore {
 #pragma unroll
       for (int e = 0; e < VPL; ++e) o[h][e] = 0.f;
     }
-    __syncthreads();
   }
 
   __device__ __forceinline__ void tile(const AttnDesc& p, const uint8_t* stage, int n) {
@@ -144,16 +155,17 @@ struct GenericCore {
     __syncwarp();
   }
 
-  __device__ __forceinline__ void put(int, float* comb, float2* stat) const {
+  __device__ __forceinline__ void put(int part, float* comb, float2* stat) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
+      if (h / COMB != part) continue;
       float sum = l[h];
 #pragma unroll
       for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == 0) stat[h] = make_float2(m[h], sum);
+      if (lane == 0) stat[h % COMB] = make_float2(m[h], sum);
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) comb[h * (HD + 4) + lane * VPL + e] = o[h][e];
+      for (int e = 0; e < VPL; ++e) comb[(h % COMB) * (HD + 4) + lane * VPL + e] = o[h][e];
     }
   }
 };

@@ -26,11 +26,11 @@ namespace {
 template <int HD_, int NT>
 struct MmaCore {
   using T = __nv_bfloat16;
-  static constexpr int TT = 16, W = 4, HD = HD_, CH = 8 * NT, COMB = 8;
+  static constexpr int TT = 16, W = 4, HD = HD_, CH = 8 * NT, COMB = 4;
   static constexpr int STAGE_BYTES = 2 * TT * HD * 2;
   static constexpr int STAGES = HD == 64 ? 6 : 3;
   static constexpr int CTAS = HD <= 128 ? 2 : 1;
-  static constexpr int EXTRA_BYTES = 0;
+  static constexpr int EXTRA_BYTES = CH * HD * 2;
   static constexpr int KT = HD / 16;  // 16-wide steps of the head
 
   uint32_t q[KT][NT][2];  // Q^T fragments
@@ -38,7 +38,11 @@ struct MmaCore {
   float m[NT][2], l[NT][2];
   float scale;
 
-  __device__ __forceinline__ MmaCore(const AttnDesc& p, uint8_t*) : scale(p.scale * kLog2e) {}
+  uint8_t* q_shared;
+  uint4 next_q[(CH * HD / 8 + W * 32 - 1) / (W * 32)];
+
+  __device__ __forceinline__ MmaCore(const AttnDesc& p, uint8_t* extra)
+      : scale(p.scale * kLog2e), q_shared(extra) {}
 
   // Byte offset of 16-byte chunk c of row r: swizzled, so the 8 rows of an
   // ldmatrix block fall on different banks.
@@ -60,23 +64,43 @@ struct MmaCore {
     }
   }
 
-  __device__ __forceinline__ void begin(const AttnDesc& p, int seq, int head0, int heads) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride;
+  // Queries in shared memory: [CH][HD], 16-byte chunks swizzled by the head.
+  static constexpr int Q_CHUNKS = CH * HD / 8, Q_PER_THREAD = (Q_CHUNKS + W * 32 - 1) / (W * 32);
+  static __device__ __forceinline__ uint32_t q_at(int h, int c) { return h * (HD * 2) + ((c ^ (h & 7)) << 4); }
+
+  __device__ __forceinline__ void fetch(const AttnDesc& p, int seq, int head0, int heads) {
+    const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride + head0 * p.q.head_stride;
+#pragma unroll
+    for (int i = 0; i < Q_PER_THREAD; ++i) {
+      const int e = i * W * 32 + threadIdx.x, h = e / (HD / 8), c = e % (HD / 8);
+      next_q[i] = make_uint4(0, 0, 0, 0);
+      if (h < heads && c * 8 < p.cache.head_dim)
+        next_q[i] = *reinterpret_cast<const uint4*>(src + h * p.q.head_stride + c * 8);
+    }
+  }
+
+  __device__ __forceinline__ void pass_on() const {
+#pragma unroll
+    for (int i = 0; i < Q_PER_THREAD; ++i) {
+      const int e = i * W * 32 + threadIdx.x, h = e / (HD / 8), c = e % (HD / 8);
+      if (Q_CHUNKS % (W * 32) == 0 || e < Q_CHUNKS) *reinterpret_cast<uint4*>(q_shared + q_at(h, c)) = next_q[i];
+    }
+  }
+
+  __device__ __forceinline__ void begin(const AttnDesc&, int) {
+    const int lane = threadIdx.x & 31;
+    // Two k steps of 8 heads per load: blocks (chunk 2 k, 2 k + 1, 2 k + 2, 2 k + 3).
+    const uint32_t qb = smem_addr(q_shared);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int h = n * 8 + g;
-      const T* row = src + (head0 + h) * p.q.head_stride;
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
+      for (int k = 0; k < KT; k += 2)
+        ldsm_x4(qb + q_at(n * 8 + (lane & 7), 2 * k + (lane >> 3)), q[k][n][0], q[k][n][1], q[k + 1][n][0],
+                q[k + 1][n][1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int d = k * 16 + e * 8 + t * 2;
-          q[k][n][e] = h < heads && d < p.cache.head_dim ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
-        }
+      for (int k = 0; k < KT; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[k][n][e] = 0.f;
-      }
       m[n][0] = m[n][1] = kNegInf;
       l[n][0] = l[n][1] = 0.f;
     }
@@ -147,21 +171,21 @@ struct MmaCore {
   }
 
   __device__ __forceinline__ void put(int part, float* comb, float2* stat) const {
+    static_assert(NT <= 2, "");
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const bool upper = NT > 1 && (part >> 1) != 0;  // picked by selection: the registers stay registers
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (n != part) continue;
+    for (int e = 0; e < 2; ++e) {
+      float sum = upper ? l[NT - 1][e] : l[0][e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = l[n][e];
+      for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (t >> 1 != (part & 1)) continue;  // this lane's heads are in the other half
+      const int h = 2 * (t & 1) + e;
+      if (g == 0) stat[h] = make_float2(upper ? m[NT - 1][e] : m[0][e], sum);
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (g == 0) stat[2 * t + e] = make_float2(m[n][e], sum);
-#pragma unroll
-        for (int k = 0; k < KT; ++k) {
-          comb[(2 * t + e) * (HD + 4) + k * 16 + g] = o[k][n][e];
-          comb[(2 * t + e) * (HD + 4) + k * 16 + g + 8] = o[k][n][e + 2];
-        }
+      for (int k = 0; k < KT; ++k) {
+        comb[h * (HD + 4) + k * 16 + g] = upper ? o[k][NT - 1][e] : o[k][0][e];
+        comb[h * (HD + 4) + k * 16 + g + 8] = upper ? o[k][NT - 1][e + 2] : o[k][0][e + 2];
       }
     }
   }
@@ -177,10 +201,10 @@ cudaError_t by_group(const AttnDesc& p, void* ws, cudaStream_t s) {
 
 bool mma_attention_ok(const AttnDesc& p) {
   const CacheDesc& c = p.cache;
-  const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v);
+  const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) |
+                   reinterpret_cast<uintptr_t>(p.q.data);
   return p.dtype == LORA_DTYPE_BF16 && (low & 15) == 0 && c.head_dim % 8 == 0 && c.page_stride % 8 == 0 &&
-         c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.q.data) & 3) == 0 &&
-         p.q.row_stride % 2 == 0 && p.q.head_stride % 2 == 0;
+         c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && p.q.row_stride % 8 == 0 && p.q.head_stride % 8 == 0;
 }
 
 CoreShape mma_attention_shape(const AttnDesc& p) {

@@ -230,9 +230,8 @@ struct AttnDesc {
   float* lse;  // or nullptr
   unsigned* status;
   // Filled in by the launcher: heads of a group are taken CH at a time
-  // (chunks per key/value head), and the workspace's three parts.
+  // (chunks per key/value head), and the workspace's two parts.
   int chunks;
-  int4* splits;    // [units] contexts that begin before a unit and are joined there
   float2* stats;   // [2 * units, CH] running maximum and sum of a partial result
   float* partial;  // [2 * units, CH, HD] its unnormalised output
 };
