@@ -9,7 +9,10 @@
 // of all streams, stream after stream, form one line that is cut into equal
 // pieces, one per CTA, so the GPU is evenly busy whatever the mix of lengths:
 // a single long context is split over every SM and a ragged batch has no
-// tail.  Every CTA works the cut out from the lengths alone.
+// tail.  Each stream also takes some places of the line for its fixed cost:
+// without them a CTA that draws many short streams ends long after the others
+// (256 ragged contexts: 25 streams against 4, 194 us against 151).  Every CTA
+// works the cut out from the lengths alone.
 //
 // Within a CTA the warps take the tiles of a piece in turn, each through its
 // own ring of asynchronous copies; a ring runs ahead across the ends of
@@ -84,56 +87,102 @@ __device__ __forceinline__ int tiles_of(const AttnDesc& p, int len) {
   return len == 0 ? 1 : (len - 1) / TT + 1;
 }
 
-// One CTA's piece of the line of tiles, [lo, hi), and the sequence it starts
-// in (whose first tile is number base).
-struct Piece {
-  long long total, lo, hi, base;
-  int units, seq;
+// The line.  A stream takes C places that stand for what a CTA spends on any
+// stream it touches (joining its warps, starting the next), then one place a
+// tile.  units pieces share the line's `total` places evenly.
+struct Line {
+  long long total, base;  // piece u: base places, the first `rest` pieces one more
+  int units, rest;
+  __device__ __forceinline__ void cut(long long total_, int units_) {
+    total = total_;
+    units = units_;
+    base = total >> 32 == 0 ? (long long)((unsigned)total / (unsigned)units) : total / units;
+    rest = (int)(total - base * units);
+  }
+  __device__ __forceinline__ long long start(int u) const { return u * base + min(u, rest); }
+  // First piece that starts at or after a place > 0.
+  __device__ __forceinline__ int first_from(long long place) const {
+    const long long wide = rest * (base + 1);
+    return place <= wide ? (int)((place + base) / (base + 1)) : rest + (int)((place - wide + base - 1) / base);
+  }
 };
 
-__device__ __forceinline__ long long piece_start(long long total, int units, int u) { return total * u / units; }
+// One piece of the line, [lo, hi), and the sequence that place lo belongs to
+// (whose first place is number origin).
+struct Piece {
+  Line line;
+  long long lo, hi, origin;
+  int seq;
+};
 
-// Executed by one full warp (every lane gets the result).
-template <int TT, int W>
+// Executed by one full warp (every lane gets the result).  Lane i counts the
+// sequences [8 i, 8 i + 8) of each 256, so up to 256 of them are read once.
+template <class Core>
 __device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_units) {
+  constexpr int PER = 8, C = Core::STREAM_COST;
   const int lane = threadIdx.x & 31;
   const int streams = p.cache.num_kv_heads * p.chunks;  // per sequence
-  long long sum = 0;
+  int n[PER];
   bool bad = false;
-  for (int b = lane; b < p.num_seqs; b += 32) {
-    const int n = tiles_of<TT>(p, p.lengths[b]);
-    bad |= n == 0;
-    sum += n;
-  }
+  long long tiles_sum = 0;
+  auto read = [&](int from) {  // places of one stream of each sequence; returns this lane's sum
+    long long sum = 0;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    for (int i = 0; i < PER; ++i) {
+      const int b = from + lane * PER + i;
+      const int tiles = b < p.num_seqs ? tiles_of<Core::TT>(p, p.lengths[b]) : 0;
+      bad |= tiles == 0 && b < p.num_seqs;
+      n[i] = tiles > 0 ? tiles + C : 0;
+      tiles_sum += tiles;
+      sum += n[i];
+    }
+    return sum;
+  };
+  long long mine = read(0), all = mine;
+  for (int from = 32 * PER; from < p.num_seqs; from += 32 * PER) all += read(from);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, d);
+    tiles_sum += __shfl_xor_sync(0xffffffffu, tiles_sum, d);
+  }
   if (u == 0 && bad) atomicOr(p.status, LORA_DEV_BAD_LENGTH);
   Piece r;
-  r.total = sum * streams;
-  const long long want = (r.total + W - 1) / W;  // a tile for every warp
-  r.units = (int)(want < 1 ? 1 : (want < max_units ? want : max_units));
-  r.lo = r.hi = r.base = 0;
+  const long long total = all * streams;
+  const long long want = (tiles_sum * streams + Core::W - 1) / Core::W;  // pieces with a tile for every warp
+  r.line.cut(total, (int)(want < 1 ? 1 : (want < max_units ? want : max_units)));
+  r.lo = r.hi = r.origin = 0;
   r.seq = 0;
-  if (u >= r.units || r.total == 0) return r;
-  r.lo = piece_start(r.total, r.units, u);
-  r.hi = piece_start(r.total, r.units, u + 1);
-  const long long want_tile = r.lo / streams;  // in units of one stream's tiles
+  if (u >= r.line.units || total == 0) return r;
+  r.lo = r.line.start(u);
+  r.hi = r.line.start(u + 1);
+  // The sequence whose one-stream places contain lo / streams.
+  const long long place = r.lo >> 32 == 0 ? (long long)((unsigned)r.lo / (unsigned)streams) : r.lo / streams;
   long long before = 0;
-  for (int c = 0; c < p.num_seqs; c += 32) {
-    const int b = c + lane;
-    const long long n = b < p.num_seqs ? tiles_of<TT>(p, p.lengths[b]) : 0;
-    long long incl = n;
+  for (int from = 0; from < p.num_seqs; from += 32 * PER) {
+    if (from > 0 || p.num_seqs > 32 * PER) mine = read(from);
+    long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += v;
     }
-    const bool here = n > 0 && want_tile >= before + incl - n && want_tile < before + incl;
-    const unsigned who = __ballot_sync(0xffffffffu, here);
+    const long long first = before + incl - mine;
+    const unsigned who = __ballot_sync(0xffffffffu, place >= first && place < first + mine);
     if (who) {
+      int seq = 0;
+      long long origin = first;
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (!found) {
+          found = place < origin + n[i];
+          seq = from + lane * PER + i;
+          if (!found) origin += n[i];
+        }
+      }
       const int src = __ffs(who) - 1;
-      r.seq = c + src;
-      r.base = (before + __shfl_sync(0xffffffffu, incl - n, src)) * streams;
+      r.seq = __shfl_sync(0xffffffffu, seq, src);
+      r.origin = __shfl_sync(0xffffffffu, origin, src) * streams;
       break;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -143,58 +192,59 @@ __device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_
 
 // Walks the segments of a piece: the tiles [t0, t1) of stream `stream` of
 // sequence `seq` (length len, n tiles).
-template <int TT>
+template <class Core>
 struct Segments {
-  long long pos, hi;  // next tile of the line after this segment; end of the piece
+  long long room;  // places of the piece from this stream's first tile on
   int seq, stream, len, n, t0, t1;
   bool valid;
 
-  __device__ __forceinline__ void clip(const AttnDesc& p) {
-    const long long room = hi - pos;
-    t1 = n - t0 <= room ? n : t0 + (int)room;
-    pos += t1 - t0;
+  __device__ __forceinline__ void clip() {
+    t1 = n <= room ? n : (int)room;
+    valid = t1 > t0;
   }
   __device__ __forceinline__ void first(const AttnDesc& p, const Piece& r) {
-    hi = r.hi;
-    pos = r.lo;
     valid = r.lo < r.hi;
     if (!valid) return;
     seq = r.seq;
     len = p.lengths[seq];
-    n = tiles_of<TT>(p, len);
-    const long long in = r.lo - r.base;
-    stream = (int)(in / n);
-    t0 = (int)(in - (long long)stream * n);
-    clip(p);
+    n = tiles_of<Core::TT>(p, len);
+    const long long in = r.lo - r.origin;
+    const int places = n + Core::STREAM_COST;
+    stream = in >> 32 == 0 ? (int)((unsigned)in / (unsigned)places) : (int)(in / places);
+    const long long tile0 = r.origin + (long long)stream * places + Core::STREAM_COST;  // place of the first tile
+    t0 = r.lo > tile0 ? (int)(r.lo - tile0) : 0;
+    room = r.hi - tile0;
+    clip();
   }
   __device__ __forceinline__ void next(const AttnDesc& p) {
-    if (pos >= hi) {
+    room -= n + Core::STREAM_COST;
+    t0 = 0;
+    if (room <= 0) {  // the piece ends before the next stream's first tile
       valid = false;
       return;
     }
     if (++stream == p.cache.num_kv_heads * p.chunks) {
       stream = 0;
-      do {  // the line has tiles left, so a sequence with tiles follows
+      do {  // the line goes on, so a sequence with tiles follows
         len = p.lengths[++seq];
-        n = tiles_of<TT>(p, len);
+        n = tiles_of<Core::TT>(p, len);
       } while (n == 0);
     }
-    t0 = 0;
-    clip(p);
+    clip();
   }
 };
 
 // One warp's walk over the tiles it loads, with its lane's token of the tile
-// looked up one tile ahead (the block-table read is in flight meanwhile).
-template <int TT, int W>
+// looked up ahead of the load (the block-table read is in flight meanwhile).
+template <class Core>
 struct TileCursor {
-  Segments<TT> seg;
+  Segments<Core> seg;
   int tile;
-  int page, slot;  // of this lane's token; page -1: no token (slot -1)
+  int page, slot;  // of this lane's token (slot -1: none)
 
   __device__ __forceinline__ void look_up(const AttnDesc& p) {
-    const int j = tile * TT + (int)(threadIdx.x & (TT - 1));
-    page = -1;
+    const int j = tile * Core::TT + (int)(threadIdx.x & (Core::TT - 1));
+    page = 0;
     slot = -1;
     if (j < seg.len) {
       const int i = (unsigned)j / (unsigned)p.cache.page_size;
@@ -205,27 +255,27 @@ struct TileCursor {
   __device__ __forceinline__ void settle(const AttnDesc& p, int warp) {
     while (seg.valid && tile >= seg.t1) {
       seg.next(p);
-      tile = seg.t0 + warp;
+      tile = warp;
     }
     if (seg.valid) look_up(p);
   }
-  __device__ __forceinline__ void first(const AttnDesc& p, const Piece& r, int warp) {
-    seg.first(p, r);
+  __device__ __forceinline__ void first(const AttnDesc& p, const Segments<Core>& sg, int warp) {
+    seg = sg;
     if (!seg.valid) return;
     tile = seg.t0 + warp;
     settle(p, warp);
   }
   __device__ __forceinline__ void next(const AttnDesc& p, int warp) {
-    tile += W;
+    if (!seg.valid) return;
+    tile += Core::W;
     settle(p, warp);
   }
   // Element offset of this lane's token in the cache (-1: none, or its page
   // is not one of the cache's).  *bad: some lane's page is not.
   __device__ __forceinline__ long long offset(const AttnDesc& p, bool* bad) const {
-    const bool none = slot < 0;
-    const bool off_cache = !none && (page < 0 || page >= p.cache.num_pages);
+    const bool off_cache = slot >= 0 && (page < 0 || page >= p.cache.num_pages);
     *bad = __any_sync(0xffffffffu, off_cache);
-    if (none || off_cache) return -1;
+    if (slot < 0 || off_cache) return -1;
     return page * p.cache.page_stride + slot * p.cache.token_stride +
            (seg.stream / p.chunks) * p.cache.head_stride;
   }
@@ -235,7 +285,8 @@ struct TileCursor {
 //   T, TT (tokens a tile), W (warps), CTAS (resident per SM), HD (padded head
 //   width), CH (query heads a stream), COMB (heads joined in shared memory at
 //   a time, CH of them in CH / COMB parts), STAGES, STAGE_BYTES (K and V of a
-//   tile), EXTRA_BYTES (its own shared memory per CTA)
+//   tile), EXTRA_BYTES (its own shared memory per CTA), STREAM_COST (places
+//   of the line that stand for a stream's fixed cost)
 //   Core(p, extra)            before anything else, all threads
 //   load(p, stage, off)       this warp's copies of one tile into a stage
 //   fetch(p, seq, head0, heads)  starts loading a stream's queries: this
@@ -251,7 +302,6 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   constexpr int COMB = Core::COMB;
   constexpr int PITCH = HD + 4;  // floats per head of the join buffer: its columns fall on different banks
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Piece s_piece;
   uint8_t* ring = smem;
   float* comb = reinterpret_cast<float*>(smem + W * STAGES * Core::STAGE_BYTES);
   float2* stat = reinterpret_cast<float2*>(comb + W * COMB * PITCH);
@@ -259,47 +309,53 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.x;
   pdl_launch_dependents();
 
-  if (warp == 0) {
-    const Piece r = locate_piece<TT, W>(p, u, gridDim.x);
-    if (lane == 0) s_piece = r;
-  }
+  const Piece piece = locate_piece<Core>(p, u, gridDim.x);
+  Segments<Core> seg;
+  seg.first(p, piece);
+  if (!seg.valid) return;  // the whole CTA
   // Columns past head_dim are never loaded and read as zero.
-  if (p.cache.head_dim < HD)
+  if (p.cache.head_dim < HD) {
     for (int i = threadIdx.x; i < W * STAGES * Core::STAGE_BYTES / 16; i += W * 32)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
-  const Piece piece = s_piece;
-  if (piece.lo >= piece.hi) return;
-
+    __syncthreads();
+  }
   // The next segment's queries travel through registers (each thread a share)
   // into the core's shared buffer while the present segment is worked on.
-  auto heads_of = [&](const Segments<TT>& sg, int* head0) {
+  auto heads_of = [&](const Segments<Core>& sg, int* head0) {
     const int kv_head = sg.stream / p.chunks;
     const int in_group = (sg.stream - kv_head * p.chunks) * CH;  // first head of the chunk
     *head0 = kv_head * p.group + in_group;
     return min(CH, p.group - in_group);
   };
-  Segments<TT> seg;
-  seg.first(p, piece);
   Core core(p, extra);
   int head0, heads = heads_of(seg, &head0);
   core.fetch(p, seg.seq, head0, heads);
   uint8_t* my_ring = ring + warp * STAGES * Core::STAGE_BYTES;
-  TileCursor<TT, W> cur;
-  cur.first(p, piece, warp);
+  TileCursor<Core> cur;
   unsigned bad_stages = 0;
-  auto load = [&](int stage) {
-    if (cur.seg.valid) {
+  auto load = [&](int stage, const TileCursor<Core>& c) {
+    if (c.seg.valid) {
       bool bad;
-      const long long off = cur.offset(p, &bad);
+      const long long off = c.offset(p, &bad);
       bad_stages = (bad_stages & ~(1u << stage)) | ((unsigned)bad << stage);
       core.load(p, my_ring + stage * Core::STAGE_BYTES, off);
-      cur.next(p, warp);
     }
     cp_async_commit();
   };
-#pragma unroll 1
-  for (int s = 0; s < STAGES; ++s) load(s);
+  {
+    // The first tiles' block-table reads all go out before any is waited for.
+    TileCursor<Core> ahead[STAGES];
+    ahead[0].first(p, seg, warp);
+#pragma unroll
+    for (int s = 1; s < STAGES; ++s) {
+      ahead[s] = ahead[s - 1];
+      ahead[s].next(p, warp);
+    }
+    cur = ahead[STAGES - 1];
+    cur.next(p, warp);
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) load(s, ahead[s]);
+  }
 
   core.pass_on();
   __syncthreads();
@@ -307,7 +363,7 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
 #pragma unroll 1
   while (true) {
     core.begin(p, heads);
-    Segments<TT> after = seg;
+    Segments<Core> after = seg;
     after.next(p);
     int after_head0 = 0, after_heads = 0;
     if (after.valid) {
@@ -322,7 +378,8 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
       bad |= (bad_stages >> stage) & 1;
       core.tile(p, my_ring + stage * Core::STAGE_BYTES, min(TT, seg.len - t * TT));
       __syncwarp();
-      load(stage);
+      load(stage, cur);
+      cur.next(p, warp);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     // Join the warps.  A sum of -1 marks a page outside the cache.
@@ -397,23 +454,20 @@ constexpr int kJoinWarps = 4, kJoinBatch = 8;
 template <class Core>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ AttnDesc p) {
   using T = typename Core::T;
-  constexpr int TT = Core::TT, HD = Core::HD, CH = Core::CH, VPL = HD / 32;
+  constexpr int HD = Core::HD, CH = Core::CH, VPL = HD / 32;
   __shared__ int4 s_split;
   __shared__ float s_o[kJoinWarps][HD];
   __shared__ float s_l[kJoinWarps];
   const int u = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
-    const Piece piece = locate_piece<TT, Core::W>(p, u, gridDim.x);
+    const Piece piece = locate_piece<Core>(p, u, gridDim.x);
     int4 split = make_int4(0, 0, 0, 0);
-    if (piece.lo < piece.hi) {
-      Segments<TT> sg;
-      sg.first(p, piece);
-      const long long begin = piece.lo - sg.t0, end = begin + sg.n;
-      if (sg.t0 > 0 && piece_start(piece.total, piece.units, u - 1) <= begin) {
-        // First unit that starts at or after the stream's end.
-        const long long v = (end * piece.units + piece.total - 1) / piece.total;
-        split = make_int4(sg.seq, sg.stream, (int)v - u + 1, 0);
-      }
+    Segments<Core> sg;
+    sg.first(p, piece);
+    if (sg.valid && sg.t0 > 0) {
+      const long long begin = piece.lo - sg.t0, end = begin + sg.n;  // places of the stream's tiles
+      if (piece.line.start(u - 1) <= begin)
+        split = make_int4(sg.seq, sg.stream, piece.line.first_from(end) - u + 1, 0);
     }
     if (lane == 0) s_split = split;
   }

@@ -22,6 +22,7 @@ struct GenericCore {
   static constexpr int STAGES = HD == 64 ? 6 : 3;
   static constexpr int CTAS = HD <= 128 ? 2 : 1;
   static constexpr int VPL = HD / 32;  // output columns per lane
+  static constexpr int STREAM_COST = 6;
   static constexpr int EXTRA_BYTES = (CH * HD + W * TT * CH) * 4;
   static_assert(CH <= 8, "");
 

@@ -30,6 +30,7 @@ struct MmaCore {
   static constexpr int STAGE_BYTES = 2 * TT * HD * 2;
   static constexpr int STAGES = HD == 64 ? 6 : 3;
   static constexpr int CTAS = HD <= 128 ? 2 : 1;
+  static constexpr int STREAM_COST = 6;
   static constexpr int EXTRA_BYTES = CH * HD * 2;
   static constexpr int KT = HD / 16;  // 16-wide steps of the head
 
