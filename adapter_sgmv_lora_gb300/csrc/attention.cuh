@@ -54,9 +54,16 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
+// 2^x, below 2^-126 zero.
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 2^(a - m) with the convention that a maximum of -inf (nothing seen) weighs
 // nothing; an infinite or NaN score stays visible as NaN.
-__device__ __forceinline__ float weight_of(float a, float m) { return a == kNegInf ? 0.f : exp2f(a - m); }
+__device__ __forceinline__ float weight_of(float a, float m) { return a == kNegInf ? 0.f : pow2(a - m); }
 
 // The first n (all, if n >= 4) of four neighbouring outputs; one store where
 // they are whole and aligned.
@@ -87,6 +94,10 @@ __device__ __forceinline__ int tiles_of(const AttnDesc& p, int len) {
   return len == 0 ? 1 : (len - 1) / TT + 1;
 }
 
+__device__ __forceinline__ long long divide(long long a, int b) {  // a >= 0, b > 0
+  return a >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // The line.  A stream takes C places that stand for what a CTA spends on any
 // stream it touches (joining its warps, starting the next), then one place a
 // tile.  units pieces share the line's `total` places evenly.
@@ -96,7 +107,7 @@ struct Line {
   __device__ __forceinline__ void cut(long long total_, int units_) {
     total = total_;
     units = units_;
-    base = total >> 32 == 0 ? (long long)((unsigned)total / (unsigned)units) : total / units;
+    base = divide(total, units);
     rest = (int)(total - base * units);
   }
   __device__ __forceinline__ long long start(int u) const { return u * base + min(u, rest); }
@@ -115,6 +126,47 @@ struct Piece {
   int seq;
 };
 
+// Sum over the warp of values below 2^32 / of any size.
+__device__ __forceinline__ long long warp_sum(unsigned v) {
+  return (long long)__reduce_add_sync(0xffffffffu, v & 0xffffu) +
+         ((long long)__reduce_add_sync(0xffffffffu, v >> 16) << 16);
+}
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// The sequence, of those one lane counted from `seq` on, whose places contain
+// `place`; I: wide enough for a place.
+template <typename I, int PER>
+__device__ __forceinline__ bool find_place(const int (&n)[PER], I mine, I before, I place, int seq, int* found_seq,
+                                           I* found_first) {
+  const int lane = threadIdx.x & 31;
+  I incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const I v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  I first = before + incl - mine;
+  const unsigned who = __ballot_sync(0xffffffffu, place >= first && place < first + mine);
+  if (!who) return false;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    found = found || place < first + (I)n[i];
+    if (!found) {
+      first += (I)n[i];
+      ++seq;
+    }
+  }
+  const int src = __ffs(who) - 1;
+  *found_seq = __shfl_sync(0xffffffffu, seq, src);
+  *found_first = __shfl_sync(0xffffffffu, first, src);
+  return true;
+}
+
 // Executed by one full warp (every lane gets the result).  Lane i counts the
 // sequences [8 i, 8 i + 8) of each 256, so up to 256 of them are read once.
 template <class Core>
@@ -122,11 +174,11 @@ __device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_
   constexpr int PER = 8, C = Core::STREAM_COST;
   const int lane = threadIdx.x & 31;
   const int streams = p.cache.num_kv_heads * p.chunks;  // per sequence
-  int n[PER];
+  int n[PER];  // places of one stream of each sequence
   bool bad = false;
-  long long tiles_sum = 0;
-  auto read = [&](int from) {  // places of one stream of each sequence; returns this lane's sum
-    long long sum = 0;
+  unsigned tiles_sum = 0, live = 0;  // of one reading
+  auto read = [&](int from) {
+    tiles_sum = live = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int b = from + lane * PER + i;
@@ -134,21 +186,28 @@ __device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_
       bad |= tiles == 0 && b < p.num_seqs;
       n[i] = tiles > 0 ? tiles + C : 0;
       tiles_sum += tiles;
-      sum += n[i];
+      live += tiles > 0;
     }
-    return sum;
   };
-  long long mine = read(0), all = mine;
-  for (int from = 32 * PER; from < p.num_seqs; from += 32 * PER) all += read(from);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, d);
-    tiles_sum += __shfl_xor_sync(0xffffffffu, tiles_sum, d);
+  read(0);
+  const bool once = p.num_seqs <= 32 * PER;
+  long long all_tiles = 0, all_live = 0;
+  if (once) {
+    all_tiles = warp_sum(tiles_sum);
+    all_live = __reduce_add_sync(0xffffffffu, live);
+  } else {
+    for (int from = 0; from < p.num_seqs; from += 32 * PER) {
+      if (from > 0) read(from);
+      all_tiles += tiles_sum;
+      all_live += live;
+    }
+    all_tiles = warp_sum(all_tiles);
+    all_live = warp_sum(all_live);
   }
   if (u == 0 && bad) atomicOr(p.status, LORA_DEV_BAD_LENGTH);
   Piece r;
-  const long long total = all * streams;
-  const long long want = (tiles_sum * streams + Core::W - 1) / Core::W;  // pieces with a tile for every warp
+  const long long one = all_tiles + C * all_live, total = one * streams;
+  const long long want = (all_tiles * streams + Core::W - 1) / Core::W;  // pieces with a tile for every warp
   r.line.cut(total, (int)(want < 1 ? 1 : (want < max_units ? want : max_units)));
   r.lo = r.hi = r.origin = 0;
   r.seq = 0;
@@ -156,38 +215,27 @@ __device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_
   r.lo = r.line.start(u);
   r.hi = r.line.start(u + 1);
   // The sequence whose one-stream places contain lo / streams.
-  const long long place = r.lo >> 32 == 0 ? (long long)((unsigned)r.lo / (unsigned)streams) : r.lo / streams;
-  long long before = 0;
-  for (int from = 0; from < p.num_seqs; from += 32 * PER) {
-    if (from > 0 || p.num_seqs > 32 * PER) mine = read(from);
-    long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
-    }
-    const long long first = before + incl - mine;
-    const unsigned who = __ballot_sync(0xffffffffu, place >= first && place < first + mine);
-    if (who) {
-      int seq = 0;
-      long long origin = first;
-      bool found = false;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (!found) {
-          found = place < origin + n[i];
-          seq = from + lane * PER + i;
-          if (!found) origin += n[i];
-        }
-      }
-      const int src = __ffs(who) - 1;
-      r.seq = __shfl_sync(0xffffffffu, seq, src);
-      r.origin = __shfl_sync(0xffffffffu, origin, src) * streams;
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+  const long long place = divide(r.lo, streams);
+  if (once && one < INT_MAX) {
+    unsigned first = 0;
+    find_place<unsigned>(n, tiles_sum + C * live, 0u, (unsigned)place, lane * PER, &r.seq, &first);
+    r.origin = (long long)first * streams;
+    return r;
   }
+  long long before = 0, first = 0;
+  for (int from = 0; from < p.num_seqs; from += 32 * PER) {
+    read(from);
+    const long long mine = (long long)tiles_sum + C * live;
+    if (find_place<long long>(n, mine, before, place, from + lane * PER, &r.seq, &first)) break;
+    before += warp_sum(mine);
+  }
+  r.origin = first * streams;
   return r;
+}
+
+// Key/value head of a stream.
+__device__ __forceinline__ int kv_head_of(const AttnDesc& p, int stream) {
+  return p.chunks == 1 ? stream : stream / p.chunks;
 }
 
 // Walks the segments of a piece: the tiles [t0, t1) of stream `stream` of
@@ -210,7 +258,7 @@ struct Segments {
     n = tiles_of<Core::TT>(p, len);
     const long long in = r.lo - r.origin;
     const int places = n + Core::STREAM_COST;
-    stream = in >> 32 == 0 ? (int)((unsigned)in / (unsigned)places) : (int)(in / places);
+    stream = (int)divide(in, places);
     const long long tile0 = r.origin + (long long)stream * places + Core::STREAM_COST;  // place of the first tile
     t0 = r.lo > tile0 ? (int)(r.lo - tile0) : 0;
     room = r.hi - tile0;
@@ -234,20 +282,22 @@ struct Segments {
   }
 };
 
-// One warp's walk over the tiles it loads, with its lane's token of the tile
-// looked up ahead of the load (the block-table read is in flight meanwhile).
+// One warp's walk over the tiles it loads, with the tile's page (or its lane's
+// token's, where a tile may cross pages) looked up ahead of the load: the
+// block-table read is in flight meanwhile.
 template <class Core>
 struct TileCursor {
   Segments<Core> seg;
   int tile;
-  int page, slot;  // of this lane's token (slot -1: none)
+  int page, slot;  // slot: token within the page; below 0: no token
 
   __device__ __forceinline__ void look_up(const AttnDesc& p) {
-    const int j = tile * Core::TT + (int)(threadIdx.x & (Core::TT - 1));
+    int j = tile * Core::TT;
+    if (!p.whole_tiles) j += (int)(threadIdx.x & (Core::TT - 1));
     page = 0;
     slot = -1;
     if (j < seg.len) {
-      const int i = (unsigned)j / (unsigned)p.cache.page_size;
+      const int i = (int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift);
       slot = j - i * p.cache.page_size;
       page = p.tables[seg.seq * p.table_stride + i];
     }
@@ -270,15 +320,17 @@ struct TileCursor {
     tile += Core::W;
     settle(p, warp);
   }
-  // Element offset of this lane's token in the cache (-1: none, or its page
-  // is not one of the cache's).  *bad: some lane's page is not.
+  // Element offset in the cache of the tile's first token, or of this lane's
+  // where tiles may cross pages.  -1: none, or its page is not one of the
+  // cache's (*bad, the same on every lane).
   __device__ __forceinline__ long long offset(const AttnDesc& p, bool* bad) const {
-    const bool off_cache = slot >= 0 && (page < 0 || page >= p.cache.num_pages);
-    *bad = __any_sync(0xffffffffu, off_cache);
+    const bool off_cache = slot >= 0 && (unsigned)page >= (unsigned)p.cache.num_pages;
+    *bad = p.whole_tiles ? off_cache : __any_sync(0xffffffffu, off_cache);
     if (slot < 0 || off_cache) return -1;
-    return page * p.cache.page_stride + slot * p.cache.token_stride +
-           (seg.stream / p.chunks) * p.cache.head_stride;
+    return page * p.cache.page_stride + slot * p.cache.token_stride + kv_head_of(p, seg.stream) * p.cache.head_stride;
   }
+  // Tokens of the tile.
+  __device__ __forceinline__ int tokens() const { return min(Core::TT, seg.len - tile * Core::TT); }
 };
 
 // The frame.  Core gives:
@@ -288,7 +340,8 @@ struct TileCursor {
 //   tile), EXTRA_BYTES (its own shared memory per CTA), STREAM_COST (places
 //   of the line that stand for a stream's fixed cost)
 //   Core(p, extra)            before anything else, all threads
-//   load(p, stage, off)       this warp's copies of one tile into a stage
+//   load(p, stage, off, n)    this warp's copies of one tile into a stage:
+//                             off as TileCursor::offset gives it, n tokens
 //   fetch(p, seq, head0, heads)  starts loading a stream's queries: this
 //                             thread's share, into registers
 //   pass_on()                 puts that share into shared memory
@@ -322,7 +375,7 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   // The next segment's queries travel through registers (each thread a share)
   // into the core's shared buffer while the present segment is worked on.
   auto heads_of = [&](const Segments<Core>& sg, int* head0) {
-    const int kv_head = sg.stream / p.chunks;
+    const int kv_head = kv_head_of(p, sg.stream);
     const int in_group = (sg.stream - kv_head * p.chunks) * CH;  // first head of the chunk
     *head0 = kv_head * p.group + in_group;
     return min(CH, p.group - in_group);
@@ -338,7 +391,7 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
       bool bad;
       const long long off = c.offset(p, &bad);
       bad_stages = (bad_stages & ~(1u << stage)) | ((unsigned)bad << stage);
-      core.load(p, my_ring + stage * Core::STAGE_BYTES, off);
+      core.load(p, my_ring + stage * Core::STAGE_BYTES, off, c.tokens());
     }
     cp_async_commit();
   };
@@ -601,6 +654,13 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
                           (size_t)Core::W * Core::COMB * ((Core::HD + 4) * 4 + 8) + Core::EXTRA_BYTES;
   static_assert(smem <= 227 * 1024 - 256, "a CTA's shared memory");
   p.chunks = chunks_of(c, p);
+  // page_size <= 2^log: magic = ceil(2^(31 + log) / page_size) is below 2^32
+  // and exact for tokens below 2^31.
+  int log = 0;
+  while ((1LL << log) < p.cache.page_size) ++log;
+  p.page_shift = 31 + log;
+  p.page_magic = (unsigned)(((1ULL << p.page_shift) + p.cache.page_size - 1) / p.cache.page_size);
+  p.whole_tiles = p.cache.page_size % Core::TT == 0;
   const int units = units_of(c, p, std::min(device_sm_count(), kMaxSmsForWorkspace));
   const WorkspaceParts w = workspace_parts(c, units);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -2,11 +2,11 @@
 // CUDA cores: fp32 caches, and bf16 caches whose shapes or alignments the
 // tensor-core core does not take.  The frame is attention.cuh.
 //
-// One warp works on a tile of 8 tokens held as fp32 rows in shared memory.
-// Scores: lane (r, g) takes token r and the 16-byte chunks 4 i + g of its
-// key, so a chunk of a query is one 64-byte broadcast; 16-byte chunks are
-// swizzled by the token so the 8 tokens' reads fall on different banks.
-// Output: each lane owns HD / 32 neighbouring columns and walks the 8 tokens.
+// One warp works on a tile of TT = 8 or 16 tokens held as fp32 rows in shared
+// memory.  Scores: lane (r, g) takes token r and every (32 / TT)-th 16-byte
+// chunk of its key, so the queries come as broadcasts; the chunks are swizzled
+// by the token so that 8 tokens' reads fall on different banks.  Output: each
+// lane owns HD / 32 neighbouring columns and walks the tokens.
 #include "attention.cuh"
 
 namespace lora {
@@ -17,9 +17,10 @@ namespace {
 template <typename T_, int HD_, int CH_, bool ASYNC>
 struct GenericCore {
   using T = T_;
-  static constexpr int TT = 8, W = 4, HD = HD_, CH = CH_, COMB = CH_ < 4 ? CH_ : 4;
+  // 16 tokens where a tile of them is small: the fixed steps of a tile weigh less.
+  static constexpr int TT = HD_ == 64 ? 16 : 8, GROUPS = 32 / TT, W = 4, HD = HD_, CH = CH_, COMB = CH_ < 4 ? CH_ : 4;
   static constexpr int STAGE_BYTES = 2 * TT * HD * 4;
-  static constexpr int STAGES = HD == 64 ? 6 : 3;
+  static constexpr int STAGES = 3;
   static constexpr int CTAS = HD <= 128 ? 2 : 1;
   static constexpr int VPL = HD / 32;  // output columns per lane
   static constexpr int STREAM_COST = 6;
@@ -40,12 +41,14 @@ struct GenericCore {
 
   static __device__ __forceinline__ int at(int r, int chunk) { return r * HD + ((chunk ^ (r & 7)) << 2); }
 
-  __device__ __forceinline__ void load(const AttnDesc& p, uint8_t* stage, long long off) const {
+  __device__ __forceinline__ void load(const AttnDesc& p, uint8_t* stage, long long off, int n) const {
     float* k = reinterpret_cast<float*>(stage);
     float* v = k + TT * HD;
     const int lane = threadIdx.x & 31;
     const T* kg = static_cast<const T*>(p.cache.k);
     const T* vg = static_cast<const T*>(p.cache.v);
+    // Offset of each row (lane r knows row r's), -1: none.
+    if (p.whole_tiles) off = off < 0 || (lane & (TT - 1)) >= n ? -1 : off + (lane & (TT - 1)) * p.cache.token_stride;
     if constexpr (ASYNC) {
 #pragma unroll
       for (int i = 0; i < TT * HD / 4 / 32; ++i) {
@@ -100,11 +103,11 @@ struct GenericCore {
   __device__ __forceinline__ void tile(const AttnDesc& p, const uint8_t* stage, int n) {
     const float* k = reinterpret_cast<const float*>(stage);
     const float* v = k + TT * HD;
-    const int lane = threadIdx.x & 31, r = lane & 7, g = lane >> 3;
+    const int lane = threadIdx.x & 31, r = lane % TT, g = lane / TT;
     float s[CH] = {};
 #pragma unroll 4
-    for (int i = 0; i < HD / 16; ++i) {
-      const int c = i * 4 + g;
+    for (int i = 0; i < HD / 4 / GROUPS; ++i) {
+      const int c = i * GROUPS + g;
       const float4 kv = *reinterpret_cast<const float4*>(k + at(r, c));
 #pragma unroll
       for (int h = 0; h < CH; ++h) {
@@ -120,16 +123,16 @@ struct GenericCore {
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
       if (h >= heads) continue;
-      s[h] += __shfl_xor_sync(0xffffffffu, s[h], 8);
-      s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
+#pragma unroll
+      for (int d = TT; d < 32; d <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], d);
       s[h] = r < n ? s[h] * scale : kNegInf;
       float top = s[h];
 #pragma unroll
-      for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      for (int d = TT / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       const float now = fmaxf(m[h], top);
       const float base = now == kNegInf ? 0.f : now;  // nothing but -inf so far: every weight is 0
-      const float pr = exp2f(s[h] - base);
-      const float keep = exp2f(m[h] - base);
+      const float pr = pow2(s[h] - base);
+      const float keep = pow2(m[h] - base);
       m[h] = now;
       l[h] = fmaf(l[h], keep, pr);  // this lane's token; the tokens are summed in put
 #pragma unroll
@@ -163,7 +166,7 @@ struct GenericCore {
       if (h / COMB != part) continue;
       float sum = l[h];
 #pragma unroll
-      for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      for (int d = TT / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == 0) stat[h % COMB] = make_float2(m[h], sum);
 #pragma unroll
       for (int e = 0; e < VPL; ++e) comb[(h % COMB) * (HD + 4) + lane * VPL + e] = o[h][e];
@@ -197,6 +200,7 @@ cudaError_t by_width(const AttnDesc& p, void* ws, cudaStream_t s) {
 CoreShape generic_attention_shape(const AttnDesc& p) {
   const int hd = p.cache.head_dim <= 64 ? 64 : (p.cache.head_dim <= 128 ? 128 : 256);
   CoreShape c = shape_of<GenericCore<float, 64, 8, true>>();
+  c.TT = hd <= 64 ? 16 : 8;
   c.HD = hd;
   c.CH = p.group == 1 ? 1 : 8;
   c.CTAS = hd <= 128 ? 2 : 1;

@@ -49,18 +49,34 @@ struct MmaCore {
   // ldmatrix block fall on different banks.
   static __device__ __forceinline__ uint32_t at(int r, int c) { return r * (HD * 2) + ((c ^ (r & 7)) << 4); }
 
-  __device__ __forceinline__ void load(const AttnDesc& p, uint8_t* stage, long long off) const {
-    const int lane = threadIdx.x & 31;
+  __device__ __forceinline__ void load(const AttnDesc& p, uint8_t* stage, long long off, int n) const {
+    constexpr int ROWS = 32 / (HD / 8);  // rows that one copy of the warp covers
+    const int lane = threadIdx.x & 31, r0 = lane / (HD / 8), c = lane % (HD / 8);
     const T* kg = static_cast<const T*>(p.cache.k);
     const T* vg = static_cast<const T*>(p.cache.v);
+    if (c * 8 >= p.cache.head_dim && p.whole_tiles) return;
+    if (p.whole_tiles) {
+      long long src = (off < 0 ? 0 : off + r0 * p.cache.token_stride) + c * 8;
+      const long long step = off < 0 ? 0 : ROWS * p.cache.token_stride;
+      if (off < 0) n = 0;
 #pragma unroll
-    for (int i = 0; i < TT * HD / 8 / 32; ++i) {
-      const int e = i * 32 + lane, r = e / (HD / 8), c = e % (HD / 8);
-      const long long row = __shfl_sync(0xffffffffu, off, r);
-      if (c * 8 < p.cache.head_dim) {
-        const long long src = row < 0 ? 0 : row + c * 8;
-        cp_async16_zfill(stage + at(r, c), kg + src, row < 0 ? 0 : 16);
-        cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, row < 0 ? 0 : 16);
+      for (int i = 0; i < TT / ROWS; ++i) {
+        const int r = i * ROWS + r0;
+        const uint32_t bytes = r < n ? 16 : 0;
+        cp_async16_zfill(stage + at(r, c), kg + src, bytes);
+        cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, bytes);
+        src += step;
+      }
+    } else {
+#pragma unroll 2
+      for (int i = 0; i < TT / ROWS; ++i) {
+        const int r = i * ROWS + r0;
+        const long long row = __shfl_sync(0xffffffffu, off, r);
+        if (c * 8 < p.cache.head_dim) {
+          const long long src = row < 0 ? 0 : row + c * 8;
+          cp_async16_zfill(stage + at(r, c), kg + src, row < 0 ? 0 : 16);
+          cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, row < 0 ? 0 : 16);
+        }
       }
     }
   }
@@ -136,10 +152,10 @@ struct MmaCore {
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float now = fmaxf(m[n][e], top);
         const float base = now == kNegInf ? 0.f : now;  // nothing but -inf so far: every weight is 0
-        keep[e] = exp2f(m[n][e] - base);
+        keep[e] = pow2(m[n][e] - base);
         m[n][e] = now;
-        x[e] = exp2f(x[e] - base);
-        x[e + 2] = exp2f(x[e + 2] - base);
+        x[e] = pow2(x[e] - base);
+        x[e + 2] = pow2(x[e + 2] - base);
         l[n][e] = fmaf(l[n][e], keep[e], x[e] + x[e + 2]);  // this lane's tokens; summed over lanes in put
       }
       split_hi_lo_bf16x2(x[0], x[1], hi[n][0], lo[n][0]);
