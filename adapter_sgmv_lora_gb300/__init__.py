@@ -193,6 +193,9 @@ def _check(rc: int, what: str):
 def _stream_handle(stream) -> Optional[int]:
     import torch
     if stream is None:
+        # The raw handle: building a Stream object costs more than a small call's kernel.
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -772,11 +775,12 @@ def lora_paged_attention(problem: AttentionProblem, workspace, stream=None) -> N
 
 def lora_kv_copy_pages(caches: KVCaches, src, dst, stream=None) -> None:
     """Copy pages src[i] -> dst[i] (host integers) in every layer's K and V."""
-    s = np.ascontiguousarray(src, dtype=np.int32)
-    d = np.ascontiguousarray(dst, dtype=np.int32)
+    s = np.asarray(src, dtype=np.int32)
+    d = np.asarray(dst, dtype=np.int32)
     if s.ndim != 1 or s.shape != d.shape:
         raise ValueError("src and dst must be 1-D and the same length")
-    _check(lib().lora_kv_copy_pages(caches._ref, len(caches.layers), s.ctypes.data, d.ctypes.data, s.size,
+    # As bytes: copying the list is cheaper than asking an array for its address.
+    _check(lib().lora_kv_copy_pages(caches._ref, len(caches.layers), s.tobytes(), d.tobytes(), s.size,
                                     _stream_handle(stream)), "lora_kv_copy_pages")
 
 

@@ -17,12 +17,14 @@ namespace {
 
 constexpr int kMaxTensors = 128;  // K and V of 64 layers a launch
 constexpr int kMaxCopies = 1024;  // pages a launch
+constexpr int kFewCopies = 32;    // a short list goes in a small launch parameter
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;        // units in flight per thread
 
+template <int COPIES>
 struct CopyTable {
   void* tensor[kMaxTensors];
-  int2 page[kMaxCopies];  // source, destination
+  int2 page[COPIES];  // source, destination
 };
 
 struct PageShape {  // in units of the copy
@@ -33,8 +35,8 @@ struct PageShape {  // in units of the copy
 // grid.x: chunks of one page; grid.y: tensors; grid.z: pages.  DENSE: the page
 // is one run.  I: the index type within a page (32 bits unless the page has
 // more units).
-template <typename U, bool DENSE, typename I>
-__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ CopyTable table,
+template <typename U, bool DENSE, typename I, int COPIES>
+__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ CopyTable<COPIES> table,
                                                               const __grid_constant__ PageShape g) {
   const int2 page = table.page[blockIdx.z];
   U* base = static_cast<U*>(table.tensor[blockIdx.y]);
@@ -62,19 +64,33 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
     if (first + i * kThreads < total) dst[at[i]] = v[i];
 }
 
-template <typename U>
-cudaError_t run(const CopyTable& t, const PageShape& g, int tensors, int pages, cudaStream_t s) {
+template <typename U, int COPIES>
+cudaError_t run(const CopyTable<COPIES>& t, const PageShape& g, int tensors, int pages, cudaStream_t s) {
   const long long total = g.outer * g.mid * g.run, chunk = (long long)kThreads * kUnroll;
   const dim3 grid((unsigned)((total + chunk - 1) / chunk), tensors, pages);
-  const bool dense = g.outer * g.mid == 1, wide = total > (1LL << 31);
-  if (wide) {
-    if (dense) copy_pages_kernel<U, true, long long><<<grid, kThreads, 0, s>>>(t, g);
-    else copy_pages_kernel<U, false, long long><<<grid, kThreads, 0, s>>>(t, g);
-  } else {
-    if (dense) copy_pages_kernel<U, true, unsigned><<<grid, kThreads, 0, s>>>(t, g);
-    else copy_pages_kernel<U, false, unsigned><<<grid, kThreads, 0, s>>>(t, g);
-  }
+  const bool dense = g.outer * g.mid == 1;
+  if (total > (1LL << 31)) copy_pages_kernel<U, false, long long, COPIES><<<grid, kThreads, 0, s>>>(t, g);
+  else if (dense) copy_pages_kernel<U, true, unsigned, COPIES><<<grid, kThreads, 0, s>>>(t, g);
+  else copy_pages_kernel<U, false, unsigned, COPIES><<<grid, kThreads, 0, s>>>(t, g);
   return noted(cudaGetLastError(), LORA_PATH_PAGES);
+}
+
+// One launch: np copies in nc layers.
+template <int COPIES>
+cudaError_t launch_table(const PageShape& g, int unit, const lora_kv_cache_t* caches, int nc, const int* src,
+                         const int* dst, int np, cudaStream_t s) {
+  CopyTable<COPIES> t;
+  for (int i = 0; i < nc; ++i) {
+    t.tensor[2 * i] = caches[i].k;
+    t.tensor[2 * i + 1] = caches[i].v;
+  }
+  for (int i = 0; i < np; ++i) t.page[i] = make_int2(src[i], dst[i]);
+  switch (unit) {
+    case 16: return run<uint4>(t, g, 2 * nc, np, s);
+    case 8: return run<uint2>(t, g, 2 * nc, np, s);
+    case 4: return run<unsigned>(t, g, 2 * nc, np, s);
+    default: return run<unsigned short>(t, g, 2 * nc, np, s);
+  }
 }
 
 }  // namespace
@@ -109,16 +125,9 @@ cudaError_t launch_copy_pages(const CacheDesc& c, int dtype, const lora_kv_cache
     const int nc = std::min(num_caches - c0, kMaxTensors / 2);
     for (int p0 = 0; p0 < n; p0 += kMaxCopies) {
       const int np = std::min(n - p0, kMaxCopies);
-      CopyTable t;
-      for (int i = 0; i < nc; ++i) {
-        t.tensor[2 * i] = caches[c0 + i].k;
-        t.tensor[2 * i + 1] = caches[c0 + i].v;
-      }
-      for (int i = 0; i < np; ++i) t.page[i] = make_int2(src[p0 + i], dst[p0 + i]);
-      cudaError_t e = unit >= 16 ? run<uint4>(t, g, 2 * nc, np, s)
-                      : unit == 8 ? run<uint2>(t, g, 2 * nc, np, s)
-                      : unit == 4 ? run<unsigned>(t, g, 2 * nc, np, s)
-                                  : run<unsigned short>(t, g, 2 * nc, np, s);
+      const cudaError_t e =
+          np <= kFewCopies ? launch_table<kFewCopies>(g, (int)unit, caches + c0, nc, src + p0, dst + p0, np, s)
+                           : launch_table<kMaxCopies>(g, (int)unit, caches + c0, nc, src + p0, dst + p0, np, s);
       if (e != cudaSuccess) return e;
     }
   }
