@@ -14,6 +14,11 @@
 // (256 ragged contexts: 25 streams against 4, 194 us against 151).  Every CTA
 // works the cut out from the lengths alone.
 //
+// Where every stream is short (kSoloTiles at most) and there are more streams
+// than CTAs, the pieces go to warps instead and a stream to the one whose piece
+// holds its first tile: no stream is shared, no warp waits for another (4720
+// streams of one or two tiles: 47 us before, SOLO_US after, cold).
+//
 // Within a CTA the warps take the tiles of a piece in turn, each through its
 // own ring of asynchronous copies; a ring runs ahead across the ends of
 // streams, so memory stays busy while results are put together.  Each warp
@@ -124,7 +129,10 @@ struct Piece {
   Line line;
   long long lo, hi, origin;
   int seq;
+  bool solo;  // pieces are for warps, streams are whole
 };
+
+constexpr int kSoloTiles = 8;
 
 // Sum over the warp of values below 2^32 / of any size.
 __device__ __forceinline__ long long warp_sum(unsigned v) {
@@ -173,6 +181,7 @@ template <class Core>
 __device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_units) {
   constexpr int PER = 8, C = Core::STREAM_COST;
   const int lane = threadIdx.x & 31;
+  int longest = 0;  // places of the longest stream
   const int streams = p.cache.num_kv_heads * p.chunks;  // per sequence
   int n[PER];  // places of one stream of each sequence
   bool bad = false;
@@ -185,6 +194,7 @@ __device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_
       const int tiles = b < p.num_seqs ? tiles_of<Core::TT>(p, p.lengths[b]) : 0;
       bad |= tiles == 0 && b < p.num_seqs;
       n[i] = tiles > 0 ? tiles + C : 0;
+      longest = max(longest, n[i]);
       tiles_sum += tiles;
       live += tiles > 0;
     }
@@ -207,7 +217,14 @@ __device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_
   if (u == 0 && bad) atomicOr(p.status, LORA_DEV_BAD_LENGTH);
   Piece r;
   const long long one = all_tiles + C * all_live, total = one * streams;
-  const long long want = (all_tiles * streams + Core::W - 1) / Core::W;  // pieces with a tile for every warp
+  long long want = (all_tiles * streams + Core::W - 1) / Core::W;  // pieces with a tile for every warp
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  r.solo = longest <= kSoloTiles + C && all_live * streams > max_units;
+  if (r.solo) {
+    want = all_live * streams;  // a stream for every warp
+    max_units *= Core::W;
+    u = u * Core::W + (threadIdx.x >> 5);
+  }
   r.line.cut(total, (int)(want < 1 ? 1 : (want < max_units ? want : max_units)));
   r.lo = r.hi = r.origin = 0;
   r.seq = 0;
@@ -244,11 +261,11 @@ template <class Core>
 struct Segments {
   long long room;  // places of the piece from this stream's first tile on
   int seq, stream, len, n, t0, t1;
-  bool valid;
+  bool valid, solo;
 
   __device__ __forceinline__ void clip() {
-    t1 = n <= room ? n : (int)room;
-    valid = t1 > t0;
+    t1 = n <= room || solo ? n : (int)room;
+    valid = room > 0 && t1 > t0;
   }
   __device__ __forceinline__ void first(const AttnDesc& p, const Piece& r) {
     valid = r.lo < r.hi;
@@ -262,7 +279,9 @@ struct Segments {
     const long long tile0 = r.origin + (long long)stream * places + Core::STREAM_COST;  // place of the first tile
     t0 = r.lo > tile0 ? (int)(r.lo - tile0) : 0;
     room = r.hi - tile0;
-    clip();
+    solo = r.solo;
+    if (solo && t0 > 0) next(p);  // the stream is the piece's before
+    else clip();
   }
   __device__ __forceinline__ void next(const AttnDesc& p) {
     room -= n + Core::STREAM_COST;
@@ -282,18 +301,20 @@ struct Segments {
   }
 };
 
-// One warp's walk over the tiles it loads, with the tile's page (or its lane's
-// token's, where a tile may cross pages) looked up ahead of the load: the
-// block-table read is in flight meanwhile.
+// One warp's walk over the tiles it loads: rank, rank + step, ... of each
+// segment.  The block-table reads of a tile are made ahead of its load and are
+// in flight meanwhile.  Where pages hold whole grains of GRAIN tokens lane i
+// looks up grain i of the tile, else token i.
 template <class Core>
 struct TileCursor {
+  static constexpr int GRAINS = Core::TT / Core::GRAIN;
   Segments<Core> seg;
   int tile;
   int page, slot;  // slot: token within the page; below 0: no token
 
   __device__ __forceinline__ void look_up(const AttnDesc& p) {
-    int j = tile * Core::TT;
-    if (!p.whole_tiles) j += (int)(threadIdx.x & (Core::TT - 1));
+    const int j = tile * Core::TT + (int)(p.whole_grains ? (threadIdx.x & (GRAINS - 1)) * Core::GRAIN
+                                                         : threadIdx.x & (Core::TT - 1));
     page = 0;
     slot = -1;
     if (j < seg.len) {
@@ -302,30 +323,29 @@ struct TileCursor {
       page = p.tables[seg.seq * p.table_stride + i];
     }
   }
-  __device__ __forceinline__ void settle(const AttnDesc& p, int warp) {
+  __device__ __forceinline__ void settle(const AttnDesc& p, int rank) {
     while (seg.valid && tile >= seg.t1) {
       seg.next(p);
-      tile = warp;
+      tile = rank;
     }
     if (seg.valid) look_up(p);
   }
-  __device__ __forceinline__ void first(const AttnDesc& p, const Segments<Core>& sg, int warp) {
+  __device__ __forceinline__ void first(const AttnDesc& p, const Segments<Core>& sg, int rank) {
     seg = sg;
     if (!seg.valid) return;
-    tile = seg.t0 + warp;
-    settle(p, warp);
+    tile = seg.t0 + rank;
+    settle(p, rank);
   }
-  __device__ __forceinline__ void next(const AttnDesc& p, int warp) {
+  __device__ __forceinline__ void next(const AttnDesc& p, int rank, int step) {
     if (!seg.valid) return;
-    tile += Core::W;
-    settle(p, warp);
+    tile += step;
+    settle(p, rank);
   }
-  // Element offset in the cache of the tile's first token, or of this lane's
-  // where tiles may cross pages.  -1: none, or its page is not one of the
-  // cache's (*bad, the same on every lane).
+  // Element offset in the cache of this lane's grain or token.  -1: none, or
+  // its page is not one of the cache's (*bad: some lane's is not).
   __device__ __forceinline__ long long offset(const AttnDesc& p, bool* bad) const {
     const bool off_cache = slot >= 0 && (unsigned)page >= (unsigned)p.cache.num_pages;
-    *bad = p.whole_tiles ? off_cache : __any_sync(0xffffffffu, off_cache);
+    *bad = __any_sync(0xffffffffu, off_cache);
     if (slot < 0 || off_cache) return -1;
     return page * p.cache.page_stride + slot * p.cache.token_stride + kv_head_of(p, seg.stream) * p.cache.head_stride;
   }
@@ -338,7 +358,8 @@ struct TileCursor {
 //   width), CH (query heads a stream), COMB (heads joined in shared memory at
 //   a time, CH of them in CH / COMB parts), STAGES, STAGE_BYTES (K and V of a
 //   tile), EXTRA_BYTES (its own shared memory per CTA), STREAM_COST (places
-//   of the line that stand for a stream's fixed cost)
+//   of the line that stand for a stream's fixed cost), GRAIN (tokens that a
+//   load takes from one page where pages allow it)
 //   Core(p, extra)            before anything else, all threads
 //   load(p, stage, off, n)    this warp's copies of one tile into a stage:
 //                             off as TileCursor::offset gives it, n tokens
@@ -346,6 +367,7 @@ struct TileCursor {
 //                             thread's share, into registers
 //   pass_on()                 puts that share into shared memory
 //   begin(p, heads)           new stream: its queries are in shared memory
+//   begin_solo(p, seq, head0, heads)  new stream of a warp on its own
 //   tile(p, stage, n)         one tile, its first n tokens
 //   put(part, o, s)           this warp's O [COMB][HD + 4] and (m, l) [COMB] of part
 template <class Core>
@@ -365,12 +387,21 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   const Piece piece = locate_piece<Core>(p, u, gridDim.x);
   Segments<Core> seg;
   seg.first(p, piece);
-  if (!seg.valid) return;  // the whole CTA
+  if (!seg.valid) return;  // the whole CTA, or a warp on its own
+  // The team that works on a segment: the CTA's warps, or one.
+  const bool solo = piece.solo;
+  const int team = solo ? 1 : W, rank = solo ? 0 : warp, leader = solo ? warp : 0;
+  const int tid = solo ? lane : threadIdx.x;
+  auto team_sync = [&] {
+    if (solo) __syncwarp();
+    else __syncthreads();
+  };
+  uint8_t* my_ring = ring + warp * STAGES * Core::STAGE_BYTES;
   // Columns past head_dim are never loaded and read as zero.
   if (p.cache.head_dim < HD) {
-    for (int i = threadIdx.x; i < W * STAGES * Core::STAGE_BYTES / 16; i += W * 32)
-      reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    for (int i = lane; i < STAGES * Core::STAGE_BYTES / 16; i += 32)
+      reinterpret_cast<uint4*>(my_ring)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
   }
   // The next segment's queries travel through registers (each thread a share)
   // into the core's shared buffer while the present segment is worked on.
@@ -382,8 +413,7 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   };
   Core core(p, extra);
   int head0, heads = heads_of(seg, &head0);
-  core.fetch(p, seg.seq, head0, heads);
-  uint8_t* my_ring = ring + warp * STAGES * Core::STAGE_BYTES;
+  if (!solo) core.fetch(p, seg.seq, head0, heads);
   TileCursor<Core> cur;
   unsigned bad_stages = 0;
   auto load = [&](int stage, const TileCursor<Core>& c) {
@@ -398,41 +428,44 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   {
     // The first tiles' block-table reads all go out before any is waited for.
     TileCursor<Core> ahead[STAGES];
-    ahead[0].first(p, seg, warp);
+    ahead[0].first(p, seg, rank);
 #pragma unroll
     for (int s = 1; s < STAGES; ++s) {
       ahead[s] = ahead[s - 1];
-      ahead[s].next(p, warp);
+      ahead[s].next(p, rank, team);
     }
     cur = ahead[STAGES - 1];
-    cur.next(p, warp);
+    cur.next(p, rank, team);
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) load(s, ahead[s]);
   }
 
-  core.pass_on();
-  __syncthreads();
+  if (!solo) {
+    core.pass_on();
+    __syncthreads();
+  }
   int stage = 0;
 #pragma unroll 1
   while (true) {
-    core.begin(p, heads);
+    if (solo) core.begin_solo(p, seg.seq, head0, heads);
+    else core.begin(p, heads);
     Segments<Core> after = seg;
     after.next(p);
     int after_head0 = 0, after_heads = 0;
     if (after.valid) {
       after_heads = heads_of(after, &after_head0);
-      core.fetch(p, after.seq, after_head0, after_heads);
+      if (!solo) core.fetch(p, after.seq, after_head0, after_heads);
     }
     bool bad = false;
 #pragma unroll 1
-    for (int t = seg.t0 + warp; t < seg.t1; t += W) {
+    for (int t = seg.t0 + rank; t < seg.t1; t += team) {
       cp_async_wait<STAGES - 1>();
       __syncwarp();
       bad |= (bad_stages >> stage) & 1;
       core.tile(p, my_ring + stage * Core::STAGE_BYTES, min(TT, seg.len - t * TT));
       __syncwarp();
       load(stage, cur);
-      cur.next(p, warp);
+      cur.next(p, rank, team);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     // Join the warps.  A sum of -1 marks a page outside the cache.
@@ -442,19 +475,20 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
     for (int part = 0; part < CH / COMB; ++part) {
       const int part_heads = min(COMB, heads - part * COMB);
       if (part_heads <= 0) break;
-      if (part > 0) __syncthreads();
+      if (part > 0) team_sync();
       core.put(part, comb + warp * COMB * PITCH, stat + warp * COMB);
       __syncwarp();
       if (bad && lane < COMB) stat[warp * COMB + lane].y = -1.f;
-      __syncthreads();
-      for (int i = threadIdx.x; i < part_heads * (HD / 4); i += W * 32) {
+      team_sync();
+      for (int i = tid; i < part_heads * (HD / 4); i += team * 32) {
         const int h = i / (HD / 4), d = (i - h * (HD / 4)) * 4;
         if (d >= p.cache.head_dim) continue;
         float m = kNegInf;
         bool any_bad = false;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float2 st = stat[w * COMB + h];
+          if (w >= team) break;
+          const float2 st = stat[(leader + w) * COMB + h];
           m = fmaxf(m, st.x);
           any_bad |= st.y < 0.f;
         }
@@ -462,9 +496,10 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float2 st = stat[w * COMB + h];
+          if (w >= team) break;
+          const float2 st = stat[(leader + w) * COMB + h];
           const float f = weight_of(st.x, m);
-          const float4 v = *reinterpret_cast<const float4*>(comb + (w * COMB + h) * PITCH + d);
+          const float4 v = *reinterpret_cast<const float4*>(comb + ((leader + w) * COMB + h) * PITCH + d);
           l = fmaf(st.y, f, l);
           o.x = fmaf(v.x, f, o.x);
           o.y = fmaf(v.y, f, o.y);
@@ -486,8 +521,8 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
       }
     }
     if (!after.valid) break;
-    core.pass_on();
-    __syncthreads();  // the join's buffer is free, the queries are there
+    if (!solo) core.pass_on();
+    team_sync();  // the join's buffer is free, the queries are there
     seg = after;
     head0 = after_head0;
     heads = after_heads;
@@ -517,7 +552,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
     int4 split = make_int4(0, 0, 0, 0);
     Segments<Core> sg;
     sg.first(p, piece);
-    if (sg.valid && sg.t0 > 0) {
+    if (sg.valid && sg.t0 > 0) {  // never where streams are whole
       const long long begin = piece.lo - sg.t0, end = begin + sg.n;  // places of the stream's tiles
       if (piece.line.start(u - 1) <= begin)
         split = make_int4(sg.seq, sg.stream, piece.line.first_from(end) - u + 1, 0);
@@ -660,7 +695,7 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
   while ((1LL << log) < p.cache.page_size) ++log;
   p.page_shift = 31 + log;
   p.page_magic = (unsigned)(((1ULL << p.page_shift) + p.cache.page_size - 1) / p.cache.page_size);
-  p.whole_tiles = p.cache.page_size % Core::TT == 0;
+  p.whole_grains = p.cache.page_size % Core::GRAIN == 0;
   const int units = units_of(c, p, std::min(device_sm_count(), kMaxSmsForWorkspace));
   const WorkspaceParts w = workspace_parts(c, units);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

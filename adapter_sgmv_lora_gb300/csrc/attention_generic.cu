@@ -18,16 +18,17 @@ template <typename T_, int HD_, int CH_, bool ASYNC>
 struct GenericCore {
   using T = T_;
   // 16 tokens where a tile of them is small: the fixed steps of a tile weigh less.
-  static constexpr int TT = HD_ == 64 ? 16 : 8, GROUPS = 32 / TT, W = 4, HD = HD_, CH = CH_, COMB = CH_ < 4 ? CH_ : 4;
+  static constexpr int TT = HD_ == 64 ? 16 : 8, GRAIN = TT, GROUPS = 32 / TT, W = 4, HD = HD_, CH = CH_, COMB = CH_ < 4 ? CH_ : 4;
   static constexpr int STAGE_BYTES = 2 * TT * HD * 4;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = CH == 8 && HD > 64 ? 2 : 3;
   static constexpr int CTAS = HD <= 128 ? 2 : 1;
   static constexpr int VPL = HD / 32;  // output columns per lane
   static constexpr int STREAM_COST = 6;
-  static constexpr int EXTRA_BYTES = (CH * HD + W * TT * CH) * 4;
+  static constexpr int EXTRA_BYTES = W * (CH * HD + TT * CH) * 4;
   static_assert(CH <= 8, "");
 
-  float* q;  // [CH][HD], this CTA's queries
+  float* shared;
+  float* q;  // [CH][HD]: the CTA's queries, or this warp's where it is on its own
   float* prob;  // [TT][CH], this warp's
   float scale;
   int heads;
@@ -35,8 +36,9 @@ struct GenericCore {
   float next_q[(CH * HD + W * 32 - 1) / (W * 32)];
 
   __device__ __forceinline__ GenericCore(const AttnDesc& p, uint8_t* extra)
-      : q(reinterpret_cast<float*>(extra)),
-        prob(q + CH * HD + (threadIdx.x >> 5) * TT * CH),
+      : shared(reinterpret_cast<float*>(extra)),
+        q(shared),
+        prob(q + W * CH * HD + (threadIdx.x >> 5) * TT * CH),
         scale(p.scale * kLog2e) {}
 
   static __device__ __forceinline__ int at(int r, int chunk) { return r * HD + ((chunk ^ (r & 7)) << 2); }
@@ -48,7 +50,7 @@ struct GenericCore {
     const T* kg = static_cast<const T*>(p.cache.k);
     const T* vg = static_cast<const T*>(p.cache.v);
     // Offset of each row (lane r knows row r's), -1: none.
-    if (p.whole_tiles) off = off < 0 || (lane & (TT - 1)) >= n ? -1 : off + (lane & (TT - 1)) * p.cache.token_stride;
+    if (p.whole_grains) off = off < 0 || (lane & (TT - 1)) >= n ? -1 : off + (lane & (TT - 1)) * p.cache.token_stride;
     if constexpr (ASYNC) {
 #pragma unroll
       for (int i = 0; i < TT * HD / 4 / 32; ++i) {
@@ -87,6 +89,22 @@ struct GenericCore {
 #pragma unroll
     for (int i = 0; i < Q_PER_THREAD; ++i)
       if (i * W * 32 + threadIdx.x < CH * HD) q[i * W * 32 + threadIdx.x] = next_q[i];
+  }
+
+  __device__ __forceinline__ void begin_solo(const AttnDesc& p, int seq, int head0, int heads_) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    q = shared + warp * CH * HD;
+    const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride + head0 * p.q.head_stride;
+    for (int h = 0; h < heads_; ++h) {  // rows of heads that are not there are not read
+      float v[HD / 32];
+#pragma unroll
+      for (int i = 0; i < HD / 32; ++i)
+        v[i] = i * 32 + lane < p.cache.head_dim ? to_f(src[h * p.q.head_stride + i * 32 + lane]) : 0.f;
+#pragma unroll
+      for (int i = 0; i < HD / 32; ++i) q[h * HD + i * 32 + lane] = v[i];
+    }
+    __syncwarp();
+    begin(p, heads_);
   }
 
   __device__ __forceinline__ void begin(const AttnDesc&, int heads_) {

@@ -17,6 +17,8 @@
 // TFLOP/s, a few percent of what the instruction reaches, so the 128-row
 // tcgen05 tiles would buy nothing here and cost the softmax its place in
 // registers.  What bounds the kernel is memory.
+#include <type_traits>
+
 #include "attention.cuh"
 
 namespace lora {
@@ -26,9 +28,12 @@ namespace {
 template <int HD_, int NT>
 struct MmaCore {
   using T = __nv_bfloat16;
-  static constexpr int TT = 16, W = 4, HD = HD_, CH = 8 * NT, COMB = 4;
+  // A stage is 8 KB (4 KB for the narrowest heads): narrow heads take two
+  // grains of 16 tokens a tile, so the fixed steps of a tile weigh the same.
+  static constexpr int GRAIN = 16, GRAINS = HD_ <= 64 ? 2 : 1, TT = GRAIN * GRAINS;
+  static constexpr int W = 4, HD = HD_, CH = 8 * NT, COMB = 4;
   static constexpr int STAGE_BYTES = 2 * TT * HD * 2;
-  static constexpr int STAGES = HD == 64 ? 6 : 3;
+  static constexpr int STAGES = HD == 32 ? 6 : 3;
   static constexpr int CTAS = HD <= 128 ? 2 : 1;
   static constexpr int STREAM_COST = 6;
   static constexpr int EXTRA_BYTES = CH * HD * 2;
@@ -47,25 +52,32 @@ struct MmaCore {
 
   // Byte offset of 16-byte chunk c of row r: swizzled, so the 8 rows of an
   // ldmatrix block fall on different banks.
-  static __device__ __forceinline__ uint32_t at(int r, int c) { return r * (HD * 2) + ((c ^ (r & 7)) << 4); }
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    return r * (HD * 2) + ((c ^ (HD >= 64 ? r & 7 : (r >> 1) & 3)) << 4);
+  }
 
   __device__ __forceinline__ void load(const AttnDesc& p, uint8_t* stage, long long off, int n) const {
     constexpr int ROWS = 32 / (HD / 8);  // rows that one copy of the warp covers
     const int lane = threadIdx.x & 31, r0 = lane / (HD / 8), c = lane % (HD / 8);
     const T* kg = static_cast<const T*>(p.cache.k);
     const T* vg = static_cast<const T*>(p.cache.v);
-    if (c * 8 >= p.cache.head_dim && p.whole_tiles) return;
-    if (p.whole_tiles) {
-      long long src = (off < 0 ? 0 : off + r0 * p.cache.token_stride) + c * 8;
-      const long long step = off < 0 ? 0 : ROWS * p.cache.token_stride;
-      if (off < 0) n = 0;
+    if (p.whole_grains) {
 #pragma unroll
-      for (int i = 0; i < TT / ROWS; ++i) {
-        const int r = i * ROWS + r0;
-        const uint32_t bytes = r < n ? 16 : 0;
-        cp_async16_zfill(stage + at(r, c), kg + src, bytes);
-        cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, bytes);
-        src += step;
+      for (int j = 0; j < GRAINS; ++j) {
+        const long long first = __shfl_sync(0xffffffffu, off, j);
+        if (c * 8 < p.cache.head_dim) {
+          long long src = (first < 0 ? 0 : first + r0 * p.cache.token_stride) + c * 8;
+          const long long step = first < 0 ? 0 : ROWS * p.cache.token_stride;
+          const int live = first < 0 ? 0 : n;
+#pragma unroll
+          for (int i = 0; i < GRAIN / ROWS; ++i) {
+            const int r = j * GRAIN + i * ROWS + r0;
+            const uint32_t bytes = r < live ? 16 : 0;
+            cp_async16_zfill(stage + at(r, c), kg + src, bytes);
+            cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, bytes);
+            src += step;
+          }
+        }
       }
     } else {
 #pragma unroll 2
@@ -83,7 +95,6 @@ struct MmaCore {
 
   // Queries in shared memory: [CH][HD], 16-byte chunks swizzled by the head.
   static constexpr int Q_CHUNKS = CH * HD / 8, Q_PER_THREAD = (Q_CHUNKS + W * 32 - 1) / (W * 32);
-  static __device__ __forceinline__ uint32_t q_at(int h, int c) { return h * (HD * 2) + ((c ^ (h & 7)) << 4); }
 
   __device__ __forceinline__ void fetch(const AttnDesc& p, int seq, int head0, int heads) {
     const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride + head0 * p.q.head_stride;
@@ -100,20 +111,13 @@ struct MmaCore {
 #pragma unroll
     for (int i = 0; i < Q_PER_THREAD; ++i) {
       const int e = i * W * 32 + threadIdx.x, h = e / (HD / 8), c = e % (HD / 8);
-      if (Q_CHUNKS % (W * 32) == 0 || e < Q_CHUNKS) *reinterpret_cast<uint4*>(q_shared + q_at(h, c)) = next_q[i];
+      if (Q_CHUNKS % (W * 32) == 0 || e < Q_CHUNKS) *reinterpret_cast<uint4*>(q_shared + at(h, c)) = next_q[i];
     }
   }
 
-  __device__ __forceinline__ void begin(const AttnDesc&, int) {
-    const int lane = threadIdx.x & 31;
-    // Two k steps of 8 heads per load: blocks (chunk 2 k, 2 k + 1, 2 k + 2, 2 k + 3).
-    const uint32_t qb = smem_addr(q_shared);
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int k = 0; k < KT; k += 2)
-        ldsm_x4(qb + q_at(n * 8 + (lane & 7), 2 * k + (lane >> 3)), q[k][n][0], q[k][n][1], q[k + 1][n][0],
-                q[k + 1][n][1]);
 #pragma unroll
       for (int k = 0; k < KT; ++k)
 #pragma unroll
@@ -123,47 +127,92 @@ struct MmaCore {
     }
   }
 
+  __device__ __forceinline__ void begin_solo(const AttnDesc& p, int seq, int head0, int heads) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const T* src = static_cast<const T*>(p.q.data) + seq * p.q.row_stride + head0 * p.q.head_stride;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = n * 8 + g, d = k * 16 + e * 8 + t * 2;
+          q[k][n][e] = h < heads && d < p.cache.head_dim
+                           ? *reinterpret_cast<const uint32_t*>(src + h * p.q.head_stride + d)
+                           : 0u;
+        }
+    clear();
+  }
+
+  __device__ __forceinline__ void begin(const AttnDesc&, int) {
+    const int lane = threadIdx.x & 31;
+    // Two k steps of 8 heads per load: blocks (chunk 2 k, 2 k + 1, 2 k + 2, 2 k + 3).
+    const uint32_t qb = smem_addr(q_shared);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < KT; k += 2)
+        ldsm_x4(qb + at(n * 8 + (lane & 7), 2 * k + (lane >> 3)), q[k][n][0], q[k][n][1], q[k + 1][n][0],
+                q[k + 1][n][1]);
+    clear();
+  }
+
   __device__ __forceinline__ void tile(const AttnDesc& p, const uint8_t* stage, int n_tokens) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
     const uint32_t kb = smem_addr(stage), vb = kb + TT * HD * 2;
-    float s[NT][2][4] = {};  // two chains of accumulation, summed below
+    // Scores: a grain's products in two chains (one where there are two
+    // grains), summed below.
+    constexpr int CHAINS = GRAINS == 1 ? 2 : 1;
+    float s[GRAINS][NT][CHAINS][4] = {};
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
-      uint32_t a[4];
-      ldsm_x4(kb + at(lane & 15, 2 * k + (lane >> 4)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma_bf16_16816(s[n][k & 1], a, q[k][n][0], q[k][n][1]);
+      for (int j = 0; j < GRAINS; ++j) {
+        uint32_t a[4];
+        ldsm_x4(kb + at(j * GRAIN + (lane & 15), 2 * k + (lane >> 4)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_bf16_16816(s[j][n][k % CHAINS], a, q[k][n][0], q[k][n][1]);
+      }
     }
-    const bool live0 = g < n_tokens, live1 = g + 8 < n_tokens;
-    uint32_t hi[NT][2], lo[NT][2];
+    uint32_t hi[GRAINS][NT][2], lo[GRAINS][NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float x[4];
+      float x[GRAINS][4], keep[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = (s[n][0][e] + s[n][1][e]) * scale;
-        if (!(e < 2 ? live0 : live1)) x[e] = kNegInf;
-      }
-      float keep[2];
+      for (int j = 0; j < GRAINS; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[j][e] = (CHAINS == 2 ? s[j][n][0][e] + s[j][n][CHAINS - 1][e] : s[j][n][0][e]) * scale;
+          if (j * GRAIN + g + (e < 2 ? 0 : 8) >= n_tokens) x[j][e] = kNegInf;
+        }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float top = fmaxf(x[e], x[e + 2]);
+        float top = fmaxf(x[0][e], x[0][e + 2]);
+        if (GRAINS == 2) top = fmaxf(top, fmaxf(x[GRAINS - 1][e], x[GRAINS - 1][e + 2]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float now = fmaxf(m[n][e], top);
         const float base = now == kNegInf ? 0.f : now;  // nothing but -inf so far: every weight is 0
         keep[e] = pow2(m[n][e] - base);
         m[n][e] = now;
-        x[e] = pow2(x[e] - base);
-        x[e + 2] = pow2(x[e + 2] - base);
-        l[n][e] = fmaf(l[n][e], keep[e], x[e] + x[e + 2]);  // this lane's tokens; summed over lanes in put
-      }
-      split_hi_lo_bf16x2(x[0], x[1], hi[n][0], lo[n][0]);
-      split_hi_lo_bf16x2(x[2], x[3], hi[n][1], lo[n][1]);
+        float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        hi[n][e] = transpose_8x8(hi[n][e]);
-        lo[n][e] = transpose_8x8(lo[n][e]);
+        for (int j = 0; j < GRAINS; ++j) {
+          x[j][e] = pow2(x[j][e] - base);
+          x[j][e + 2] = pow2(x[j][e + 2] - base);
+          sum += x[j][e] + x[j][e + 2];
+        }
+        l[n][e] = fmaf(l[n][e], keep[e], sum);  // this lane's tokens; summed over lanes in put
+      }
+#pragma unroll
+      for (int j = 0; j < GRAINS; ++j) {
+        split_hi_lo_bf16x2(x[j][0], x[j][1], hi[j][n][0], lo[j][n][0]);
+        split_hi_lo_bf16x2(x[j][2], x[j][3], hi[j][n][1], lo[j][n][1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          hi[j][n][e] = transpose_8x8(hi[j][n][e]);
+          lo[j][n][e] = transpose_8x8(lo[j][n][e]);
+        }
       }
       if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
 #pragma unroll
@@ -177,12 +226,16 @@ struct MmaCore {
     }
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
-      uint32_t a[4];
-      ldsm_x4_trans(vb + at((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma_bf16_16816(o[k][n], a, hi[n][0], hi[n][1]);
-        mma_bf16_16816(o[k][n], a, lo[n][0], lo[n][1]);
+      for (int j = 0; j < GRAINS; ++j) {
+        uint32_t a[4];
+        ldsm_x4_trans(vb + at(j * GRAIN + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), a[0], a[1],
+                      a[2], a[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_bf16_16816(o[k][n], a, hi[j][n][0], hi[j][n][1]);
+          mma_bf16_16816(o[k][n], a, lo[j][n][0], lo[j][n][1]);
+        }
       }
     }
   }
@@ -208,12 +261,6 @@ struct MmaCore {
   }
 };
 
-template <int HD>
-cudaError_t by_group(const AttnDesc& p, void* ws, cudaStream_t s) {
-  if (p.group <= 8) return launch_core<MmaCore<HD, 1>>(p, ws, s, LORA_PATH_MMA_ATTENTION);
-  return launch_core<MmaCore<HD, 2>>(p, ws, s, LORA_PATH_MMA_ATTENTION);
-}
-
 }  // namespace
 
 bool mma_attention_ok(const AttnDesc& p) {
@@ -224,17 +271,30 @@ bool mma_attention_ok(const AttnDesc& p) {
          c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && p.q.row_stride % 8 == 0 && p.q.head_stride % 8 == 0;
 }
 
-CoreShape mma_attention_shape(const AttnDesc& p) {
+// f(a core's type) for the head width and group of p.
+template <class F>
+auto with_core(const AttnDesc& p, F f) {
   const int hd = p.cache.head_dim;
-  if (p.group <= 8)
-    return hd <= 64 ? shape_of<MmaCore<64, 1>>() : (hd <= 128 ? shape_of<MmaCore<128, 1>>() : shape_of<MmaCore<256, 1>>());
-  return hd <= 64 ? shape_of<MmaCore<64, 2>>() : (hd <= 128 ? shape_of<MmaCore<128, 2>>() : shape_of<MmaCore<256, 2>>());
+  if (p.group <= 8) {
+    if (hd <= 32) return f((MmaCore<32, 1>*)nullptr);
+    if (hd <= 64) return f((MmaCore<64, 1>*)nullptr);
+    if (hd <= 128) return f((MmaCore<128, 1>*)nullptr);
+    return f((MmaCore<256, 1>*)nullptr);
+  }
+  if (hd <= 32) return f((MmaCore<32, 2>*)nullptr);
+  if (hd <= 64) return f((MmaCore<64, 2>*)nullptr);
+  if (hd <= 128) return f((MmaCore<128, 2>*)nullptr);
+  return f((MmaCore<256, 2>*)nullptr);
+}
+
+CoreShape mma_attention_shape(const AttnDesc& p) {
+  return with_core(p, [](auto* core) { return shape_of<std::remove_pointer_t<decltype(core)>>(); });
 }
 
 cudaError_t launch_attention_mma(const AttnDesc& p, void* workspace, cudaStream_t s) {
-  if (p.cache.head_dim <= 64) return by_group<64>(p, workspace, s);
-  if (p.cache.head_dim <= 128) return by_group<128>(p, workspace, s);
-  return by_group<256>(p, workspace, s);
+  return with_core(p, [&](auto* core) {
+    return launch_core<std::remove_pointer_t<decltype(core)>>(p, workspace, s, LORA_PATH_MMA_ATTENTION);
+  });
 }
 
 // The workspace is sized for either core, so that it depends on shapes only

@@ -231,12 +231,12 @@ struct AttnDesc {
   unsigned* status;
   // Filled in by the launcher: heads of a group are taken CH at a time
   // (chunks per key/value head); token / page_size is
-  // token * page_magic >> page_shift for tokens below 2^31; whole_tiles: no
-  // tile of tokens crosses a page's end; and the workspace's two parts.
+  // token * page_magic >> page_shift for tokens below 2^31; whole_grains: no
+  // grain of tokens crosses a page's end; and the workspace's two parts.
   int chunks;
   unsigned page_magic;
   int page_shift;
-  bool whole_tiles;
+  bool whole_grains;
   float2* stats;   // [2 * units, CH] running maximum and sum of a partial result
   float* partial;  // [2 * units, CH, HD] its unnormalised output
 };
