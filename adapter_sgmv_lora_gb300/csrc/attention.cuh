@@ -17,7 +17,7 @@
 // Where every stream is short (kSoloTiles at most) and there are more streams
 // than CTAs, the pieces go to warps instead and a stream to the one whose piece
 // holds its first tile: no stream is shared, no warp waits for another (4720
-// streams of one or two tiles: 47 us before, SOLO_US after, cold).
+// streams of one or two tiles: 47 us before, 33 after, cold).
 //
 // Within a CTA the warps take the tiles of a piece in turn, each through its
 // own ring of asynchronous copies; a ring runs ahead across the ends of
