@@ -426,18 +426,12 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
     cp_async_commit();
   };
   {
-    // The first tiles' block-table reads all go out before any is waited for.
-    TileCursor<Core> ahead[STAGES];
-    ahead[0].first(p, seg, rank);
-#pragma unroll
-    for (int s = 1; s < STAGES; ++s) {
-      ahead[s] = ahead[s - 1];
-      ahead[s].next(p, rank, team);
+    cur.first(p, seg, rank);
+#pragma unroll 1
+    for (int s = 0; s < STAGES; ++s) {
+      load(s, cur);
+      cur.next(p, rank, team);
     }
-    cur = ahead[STAGES - 1];
-    cur.next(p, rank, team);
-#pragma unroll
-    for (int s = 0; s < STAGES; ++s) load(s, ahead[s]);
   }
 
   if (!solo) {
