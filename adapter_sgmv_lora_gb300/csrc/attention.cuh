@@ -105,31 +105,54 @@ __device__ __forceinline__ long long divide(long long a, int b) {  // a >= 0, b 
 
 // The line.  A stream takes C places that stand for what a CTA spends on any
 // stream it touches (joining its warps, starting the next), then one place a
-// tile.  units pieces share the line's `total` places evenly.
+// tile.  The line is cut into `pieces` even parts.  Where those are long each
+// gives its last eighth up in kSpare spare units, which go to the CTAs that
+// are done first (attention_kernel): unit (kSpare + 1) u is the head of piece
+// u, the kSpare units after it its spares.  Else a piece is one unit.
+constexpr int kSpare = 2;
+constexpr int kSparePlaces = 192;  // places of a piece that gives spares
+
 struct Line {
-  long long total, base;  // piece u: base places, the first `rest` pieces one more
-  int units, rest;
-  __device__ __forceinline__ void cut(long long total_, int units_) {
+  long long total, base, head, spare;  // piece u: base places, the first `rest` pieces one more
+  int pieces, rest;
+  bool spares;
+  __device__ __forceinline__ void cut(long long total_, int pieces_, bool may_spare) {
     total = total_;
-    units = units_;
-    base = divide(total, units);
-    rest = (int)(total - base * units);
+    pieces = pieces_;
+    base = divide(total, pieces);
+    rest = (int)(total - base * pieces);
+    spares = may_spare && base >= kSparePlaces;
+    spare = base >> 4;
+    head = base - kSpare * spare;
   }
-  __device__ __forceinline__ long long start(int u) const { return u * base + min(u, rest); }
-  // First piece that starts at or after a place > 0.
+  __device__ __forceinline__ int units() const { return spares ? pieces * (kSpare + 1) : pieces; }
+  __device__ __forceinline__ long long piece_start(int u) const { return u * base + min(u, rest); }
+  __device__ __forceinline__ long long start(int v) const {
+    if (!spares) return piece_start(v);
+    const int u = v / (kSpare + 1), i = v - u * (kSpare + 1);
+    return piece_start(u) + (i == 0 ? 0 : head + (i - 1) * spare);
+  }
+  // First unit that starts at or after a place > 0.
   __device__ __forceinline__ int first_from(long long place) const {
     const long long wide = rest * (base + 1);
-    return place <= wide ? (int)((place + base) / (base + 1)) : rest + (int)((place - wide + base - 1) / base);
+    const int u = place <= wide ? (int)((place + base) / (base + 1)) : rest + (int)((place - wide + base - 1) / base);
+    if (!spares) return u;
+    const long long in = place - piece_start(u - 1);  // > 0: within piece u - 1 or at its end
+    const int i = in <= head ? 1 : 1 + (int)((in - head + spare - 1) / spare);
+    return i > kSpare ? u * (kSpare + 1) : (u - 1) * (kSpare + 1) + i;
+  }
+  // The unit that block b starts with; blocks past the pieces have the spares.
+  __device__ __forceinline__ int unit_of(int b) const {
+    if (!spares) return b;
+    return b < pieces ? b * (kSpare + 1) : (b - pieces) / kSpare * (kSpare + 1) + 1 + (b - pieces) % kSpare;
   }
 };
 
-// One piece of the line, [lo, hi), and the sequence that place lo belongs to
-// (whose first place is number origin).
+// One unit's part of the line, [lo, hi), and the sequence that place lo
+// belongs to (whose first place is number origin).
 struct Piece {
-  Line line;
   long long lo, hi, origin;
   int seq;
-  bool solo;  // pieces are for warps, streams are whole
 };
 
 constexpr int kSoloTiles = 8;
@@ -175,80 +198,104 @@ __device__ __forceinline__ bool find_place(const int (&n)[PER], I mine, I before
   return true;
 }
 
-// Executed by one full warp (every lane gets the result).  Lane i counts the
-// sequences [8 i, 8 i + 8) of each 256, so up to 256 of them are read once.
+// What one lane counts of sequences [from + 8 lane, from + 8 lane + 8): the
+// places of one stream of each.
 template <class Core>
-__device__ __forceinline__ Piece locate_piece(const AttnDesc& p, int u, int max_units) {
-  constexpr int PER = 8, C = Core::STREAM_COST;
-  const int lane = threadIdx.x & 31;
-  int longest = 0;  // places of the longest stream
-  const int streams = p.cache.num_kv_heads * p.chunks;  // per sequence
-  int n[PER];  // places of one stream of each sequence
-  bool bad = false;
-  unsigned tiles_sum = 0, live = 0;  // of one reading
-  auto read = [&](int from) {
-    tiles_sum = live = 0;
+struct Count {
+  static constexpr int PER = 8, C = Core::STREAM_COST;
+  int n[PER];
+  unsigned tiles, live;
+  int longest;
+  bool bad;
+  __device__ __forceinline__ void read(const AttnDesc& p, int from) {
+    tiles = live = 0;
+    longest = 0;
+    bad = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int b = from + lane * PER + i;
-      const int tiles = b < p.num_seqs ? tiles_of<Core::TT>(p, p.lengths[b]) : 0;
-      bad |= tiles == 0 && b < p.num_seqs;
-      n[i] = tiles > 0 ? tiles + C : 0;
+      const int b = from + (int)(threadIdx.x & 31) * PER + i;
+      const int t = b < p.num_seqs ? tiles_of<Core::TT>(p, p.lengths[b]) : 0;
+      bad |= t == 0 && b < p.num_seqs;
+      n[i] = t > 0 ? t + C : 0;
       longest = max(longest, n[i]);
-      tiles_sum += tiles;
-      live += tiles > 0;
+      tiles += t;
+      live += t > 0;
     }
-  };
-  read(0);
-  const bool once = p.num_seqs <= 32 * PER;
-  long long all_tiles = 0, all_live = 0;
-  if (once) {
-    all_tiles = warp_sum(tiles_sum);
-    all_live = __reduce_add_sync(0xffffffffu, live);
-  } else {
-    for (int from = 0; from < p.num_seqs; from += 32 * PER) {
-      if (from > 0) read(from);
-      all_tiles += tiles_sum;
-      all_live += live;
+  }
+  __device__ __forceinline__ long long places() const { return (long long)tiles + C * live; }
+};
+
+// How the whole call is shared out; every warp works it out from the lengths.
+// Executed by one full warp (every lane gets the results), as is locate.
+template <class Core>
+struct Plan {
+  static constexpr int CHUNK = 32 * Count<Core>::PER;
+  Line line;
+  bool solo;   // units are for warps, streams are whole
+  bool small;  // one count covers the sequences, and places fit 32 bits
+
+  // c: the count of the first sequences.
+  __device__ __forceinline__ void make(const AttnDesc& p, const Count<Core>& c, bool report) {
+    const int streams = p.cache.num_kv_heads * p.chunks;  // per sequence
+    const bool once = p.num_seqs <= CHUNK;
+    long long tiles, live;
+    int longest = c.longest;
+    bool bad = c.bad;
+    if (once) {
+      tiles = warp_sum(c.tiles);
+      live = __reduce_add_sync(0xffffffffu, c.live);
+    } else {
+      tiles = c.tiles;
+      live = c.live;
+      for (int from = CHUNK; from < p.num_seqs; from += CHUNK) {
+        Count<Core> more;
+        more.read(p, from);
+        tiles += more.tiles;
+        live += more.live;
+        longest = max(longest, more.longest);
+        bad |= more.bad;
+      }
+      tiles = warp_sum(tiles);
+      live = warp_sum(live);
     }
-    all_tiles = warp_sum(all_tiles);
-    all_live = warp_sum(all_live);
+    if (report && bad) atomicOr(p.status, LORA_DEV_BAD_LENGTH);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const long long one = tiles + Core::STREAM_COST * live;
+    solo = longest <= kSoloTiles + Core::STREAM_COST && live * streams > p.pieces;
+    // Pieces with a tile for every warp; on their own, a stream for every warp.
+    const long long want = solo ? live * streams : (tiles * streams + Core::W - 1) / Core::W;
+    const long long most = solo ? (long long)p.pieces * Core::W : p.pieces;
+    line.cut(one * streams, (int)(want < 1 ? 1 : (want < most ? want : most)), !solo && p.spares);
+    small = once && one < INT_MAX;
   }
-  if (u == 0 && bad) atomicOr(p.status, LORA_DEV_BAD_LENGTH);
-  Piece r;
-  const long long one = all_tiles + C * all_live, total = one * streams;
-  long long want = (all_tiles * streams + Core::W - 1) / Core::W;  // pieces with a tile for every warp
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  r.solo = longest <= kSoloTiles + C && all_live * streams > max_units;
-  if (r.solo) {
-    want = all_live * streams;  // a stream for every warp
-    max_units *= Core::W;
-    u = u * Core::W + (threadIdx.x >> 5);
-  }
-  r.line.cut(total, (int)(want < 1 ? 1 : (want < max_units ? want : max_units)));
-  r.lo = r.hi = r.origin = 0;
-  r.seq = 0;
-  if (u >= r.line.units || total == 0) return r;
-  r.lo = r.line.start(u);
-  r.hi = r.line.start(u + 1);
-  // The sequence whose one-stream places contain lo / streams.
-  const long long place = divide(r.lo, streams);
-  if (once && one < INT_MAX) {
-    unsigned first = 0;
-    find_place<unsigned>(n, tiles_sum + C * live, 0u, (unsigned)place, lane * PER, &r.seq, &first);
-    r.origin = (long long)first * streams;
+
+  // Unit v's part.  c: the count of the first sequences.
+  __device__ __forceinline__ Piece locate(const AttnDesc& p, Count<Core> c, int v) const {
+    const int streams = p.cache.num_kv_heads * p.chunks, lane = threadIdx.x & 31;
+    Piece r;
+    r.lo = r.hi = r.origin = 0;
+    r.seq = 0;
+    if (v >= line.units() || line.total == 0) return r;
+    r.lo = line.start(v);
+    r.hi = line.start(v + 1);
+    // The sequence whose one-stream places contain lo / streams.
+    const long long place = divide(r.lo, streams);
+    if (small) {
+      unsigned first = 0;
+      find_place<unsigned>(c.n, (unsigned)c.places(), 0u, (unsigned)place, lane * Count<Core>::PER, &r.seq, &first);
+      r.origin = (long long)first * streams;
+      return r;
+    }
+    long long before = 0, first = 0;
+    for (int from = 0; from < p.num_seqs; from += CHUNK) {
+      if (from > 0) c.read(p, from);
+      if (find_place<long long>(c.n, c.places(), before, place, from + lane * Count<Core>::PER, &r.seq, &first)) break;
+      before += warp_sum(c.places());
+    }
+    r.origin = first * streams;
     return r;
   }
-  long long before = 0, first = 0;
-  for (int from = 0; from < p.num_seqs; from += 32 * PER) {
-    read(from);
-    const long long mine = (long long)tiles_sum + C * live;
-    if (find_place<long long>(n, mine, before, place, from + lane * PER, &r.seq, &first)) break;
-    before += warp_sum(mine);
-  }
-  r.origin = first * streams;
-  return r;
-}
+};
 
 // Key/value head of a stream.
 __device__ __forceinline__ int kv_head_of(const AttnDesc& p, int stream) {
@@ -267,7 +314,7 @@ struct Segments {
     t1 = n <= room || solo ? n : (int)room;
     valid = room > 0 && t1 > t0;
   }
-  __device__ __forceinline__ void first(const AttnDesc& p, const Piece& r) {
+  __device__ __forceinline__ void first(const AttnDesc& p, const Piece& r, bool solo_) {
     valid = r.lo < r.hi;
     if (!valid) return;
     seq = r.seq;
@@ -279,7 +326,7 @@ struct Segments {
     const long long tile0 = r.origin + (long long)stream * places + Core::STREAM_COST;  // place of the first tile
     t0 = r.lo > tile0 ? (int)(r.lo - tile0) : 0;
     room = r.hi - tile0;
-    solo = r.solo;
+    solo = solo_;
     if (solo && t0 > 0) next(p);  // the stream is the piece's before
     else clip();
   }
@@ -301,6 +348,17 @@ struct Segments {
   }
 };
 
+// A unit that starts inside a stream whose beginning lies in the unit before
+// it stands for that stream in the join: {sequence, stream, units that share
+// it}; others {0, 0, 0}.
+template <class Core>
+__device__ __forceinline__ int4 split_of(const Line& line, const Piece& piece, const Segments<Core>& first, int v) {
+  if (!first.valid || first.t0 == 0) return make_int4(0, 0, 0, 0);  // so where streams are whole
+  const long long begin = piece.lo - first.t0, end = begin + first.n;  // places of the stream's tiles
+  if (line.start(v - 1) > begin) return make_int4(0, 0, 0, 0);
+  return make_int4(first.seq, first.stream, line.first_from(end) - v + 1, 0);
+}
+
 // One warp's walk over the tiles it loads: rank, rank + step, ... of each
 // segment.  The block-table reads of a tile are made ahead of its load and are
 // in flight meanwhile.  Where pages hold whole grains of GRAIN tokens lane i
@@ -309,6 +367,8 @@ template <class Core>
 struct TileCursor {
   static constexpr int GRAINS = Core::TT / Core::GRAIN;
   Segments<Core> seg;
+  Segments<Core> entry;  // the first segment of the unit after seg's, once it is known
+  bool has_entry;
   int tile;
   int page, slot;  // slot: token within the page; below 0: no token
 
@@ -326,18 +386,20 @@ struct TileCursor {
   __device__ __forceinline__ void settle(const AttnDesc& p, int rank) {
     while (seg.valid && tile >= seg.t1) {
       seg.next(p);
-      tile = rank;
+      if (!seg.valid && has_entry) {
+        seg = entry;
+        has_entry = false;
+      }
+      tile = seg.t0 + rank;
     }
     if (seg.valid) look_up(p);
   }
-  __device__ __forceinline__ void first(const AttnDesc& p, const Segments<Core>& sg, int rank) {
+  __device__ __forceinline__ void enter(const AttnDesc& p, const Segments<Core>& sg, int rank) {
     seg = sg;
-    if (!seg.valid) return;
     tile = seg.t0 + rank;
     settle(p, rank);
   }
   __device__ __forceinline__ void next(const AttnDesc& p, int rank, int step) {
-    if (!seg.valid) return;
     tile += step;
     settle(p, rank);
   }
@@ -352,6 +414,37 @@ struct TileCursor {
   // Tokens of the tile.
   __device__ __forceinline__ int tokens() const { return min(Core::TT, seg.len - tile * Core::TT); }
 };
+
+// Waits for the oldest of `pending` groups of asynchronous copies.
+template <int N>
+__device__ __forceinline__ void wait_oldest(int pending) {
+  if constexpr (N == 1) {
+    cp_async_wait<0>();
+  } else {
+    if (pending >= N) cp_async_wait<N - 1>();
+    else wait_oldest<N - 1>(pending);
+  }
+}
+
+// A CTA that is done takes over a block of the grid that has not started
+// (cluster launch control): the hardware hands each block out once, so spare
+// units go to whoever is free and nothing in memory has to start at zero.  A
+// unit's partial result has its place whoever computes it, so results do not
+// depend on who does.
+__device__ __forceinline__ void ask_for_block(uint4* answer, uint64_t* bar) {
+  fence_proxy_async_smem();  // the earlier answer's reads come before this write
+  mbar_arrive_expect_tx(bar, 16);
+  launch_control_try_cancel(answer, bar);
+}
+
+// The block taken over, or -1: none is left (or the wait ran out).
+__device__ __forceinline__ int answered_block(const uint4* answer, uint64_t* bar, uint32_t parity, unsigned* status) {
+  if (!mbar_wait(bar, parity) && !mbar_wait(bar, parity)) {
+    atomicOr(status, LORA_DEV_TIMEOUT);
+    return -1;
+  }
+  return launch_control_block(answer);
+}
 
 // The frame.  Core gives:
 //   T, TT (tokens a tile), W (warps), CTAS (resident per SM), HD (padded head
@@ -377,19 +470,31 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   constexpr int COMB = Core::COMB;
   constexpr int PITCH = HD + 4;  // floats per head of the join buffer: its columns fall on different banks
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) uint4 s_answer[2];
+  __shared__ uint64_t s_asked[2];
   uint8_t* ring = smem;
   float* comb = reinterpret_cast<float*>(smem + W * STAGES * Core::STAGE_BYTES);
   float2* stat = reinterpret_cast<float2*>(comb + W * COMB * PITCH);
   uint8_t* extra = reinterpret_cast<uint8_t*>(stat + W * COMB);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
 
-  const Piece piece = locate_piece<Core>(p, u, gridDim.x);
+  Count<Core> count;
+  count.read(p, 0);
+  Plan<Core> plan;
+  plan.make(p, count, blockIdx.x == 0);
+  const bool solo = plan.solo;
+  int unit = plan.line.unit_of(solo ? blockIdx.x * W + warp : blockIdx.x);
   Segments<Core> seg;
-  seg.first(p, piece);
+  {
+    const Piece piece = plan.locate(p, count, unit);
+    seg.first(p, piece, solo);
+    if (p.spares && threadIdx.x == 0)
+      p.splits[solo ? blockIdx.x : unit] =
+          solo ? make_int4(0, 0, 0, 0) : split_of<Core>(plan.line, piece, seg, unit);
+  }
   if (!seg.valid) return;  // the whole CTA, or a warp on its own
   // The team that works on a segment: the CTA's warps, or one.
-  const bool solo = piece.solo;
   const int team = solo ? 1 : W, rank = solo ? 0 : warp, leader = solo ? warp : 0;
   const int tid = solo ? lane : threadIdx.x;
   auto team_sync = [&] {
@@ -414,37 +519,66 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   Core core(p, extra);
   int head0, heads = heads_of(seg, &head0);
   if (!solo) core.fetch(p, seg.seq, head0, heads);
-  TileCursor<Core> cur;
-  unsigned bad_stages = 0;
-  auto load = [&](int stage, const TileCursor<Core>& c) {
-    if (c.seg.valid) {
-      bool bad;
-      const long long off = c.offset(p, &bad);
-      bad_stages = (bad_stages & ~(1u << stage)) | ((unsigned)bad << stage);
-      core.load(p, my_ring + stage * Core::STAGE_BYTES, off, c.tokens());
-    }
-    cp_async_commit();
-  };
-  {
-    cur.first(p, seg, rank);
-#pragma unroll 1
-    for (int s = 0; s < STAGES; ++s) {
-      load(s, cur);
-      cur.next(p, rank, team);
-    }
+  if (plan.line.spares && threadIdx.x == 0) {
+    mbar_init(&s_asked[0], 1);
+    mbar_init(&s_asked[1], 1);
+    fence_mbar_init();
+    ask_for_block(&s_answer[0], &s_asked[0]);
   }
+
+  // The ring: `pending` tiles are loaded or on their way, the oldest in stage
+  // `stage`, the next to load goes to stage `fill`.
+  TileCursor<Core> cur;
+  cur.has_entry = false;
+  cur.enter(p, seg, rank);
+  unsigned bad_stages = 0;
+  int stage = 0, fill = 0, pending = 0;
+  auto load = [&] {
+    bool bad;
+    const long long off = cur.offset(p, &bad);
+    bad_stages = (bad_stages & ~(1u << fill)) | ((unsigned)bad << fill);
+    core.load(p, my_ring + fill * Core::STAGE_BYTES, off, cur.tokens());
+    cp_async_commit();
+    ++pending;
+    fill = fill + 1 == STAGES ? 0 : fill + 1;
+    cur.next(p, rank, team);
+  };
+#pragma unroll 1
+  while (pending < STAGES && cur.seg.valid) load();
 
   if (!solo) {
     core.pass_on();
     __syncthreads();
   }
-  int stage = 0;
+  int asked = 0;  // requests for spare units answered so far
 #pragma unroll 1
   while (true) {
     if (solo) core.begin_solo(p, seg.seq, head0, heads);
     else core.begin(p, heads);
     Segments<Core> after = seg;
     after.next(p);
+    int after_unit = unit;
+    if (!after.valid && plan.line.spares && asked >= 0) {
+      // This unit ends here: on to a spare one, if one is left.
+      const int block = answered_block(&s_answer[asked & 1], &s_asked[asked & 1], (asked >> 1) & 1, p.status);
+      if (block < 0) {
+        asked = -1;
+      } else {
+        after_unit = plan.line.unit_of(block);
+        count.read(p, 0);
+        const Piece piece = plan.locate(p, count, after_unit);
+        after.first(p, piece, false);
+        if (threadIdx.x == 0) p.splits[after_unit] = split_of<Core>(plan.line, piece, after, after_unit);
+        if (cur.seg.valid) {
+          cur.entry = after;
+          cur.has_entry = true;
+        } else {
+          cur.enter(p, after, rank);
+#pragma unroll 1
+          while (pending < STAGES && cur.seg.valid) load();
+        }
+      }
+    }
     int after_head0 = 0, after_heads = 0;
     if (after.valid) {
       after_heads = heads_of(after, &after_head0);
@@ -453,18 +587,18 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
     bool bad = false;
 #pragma unroll 1
     for (int t = seg.t0 + rank; t < seg.t1; t += team) {
-      cp_async_wait<STAGES - 1>();
+      wait_oldest<STAGES>(pending);
       __syncwarp();
       bad |= (bad_stages >> stage) & 1;
       core.tile(p, my_ring + stage * Core::STAGE_BYTES, min(TT, seg.len - t * TT));
       __syncwarp();
-      load(stage, cur);
-      cur.next(p, rank, team);
+      --pending;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
+      if (cur.seg.valid) load();
     }
     // Join the warps.  A sum of -1 marks a page outside the cache.
     const bool whole = seg.t0 == 0 && seg.t1 == seg.n;
-    const long long slot = 2 * u + (seg.t0 == 0 ? 1 : 0);  // of the workspace
+    const long long slot = 2 * (long long)unit + (seg.t0 == 0 ? 1 : 0);  // of the workspace
 #pragma unroll 1
     for (int part = 0; part < CH / COMB; ++part) {
       const int part_heads = min(COMB, heads - part * COMB);
@@ -517,11 +651,15 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
     if (!after.valid) break;
     if (!solo) core.pass_on();
     team_sync();  // the join's buffer is free, the queries are there
+    if (after_unit != unit) {
+      unit = after_unit;
+      ++asked;  // every warp has the last answer, the buffer before it is free
+      if (threadIdx.x == 0) ask_for_block(&s_answer[asked & 1], &s_asked[asked & 1]);
+    }
     seg = after;
     head0 = after_head0;
     heads = after_heads;
   }
-  cp_async_wait<0>();
 }
 
 // Joins the partial results of the streams that several units share.  Block
@@ -529,8 +667,11 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
 // the h-th query head of it; its warps share the partial results out and are
 // joined in warp order.  Partial 0 is the end of unit u - 1, partial i the
 // beginning of unit u - 1 + i.  Which stream that is follows from the lengths
-// alone, so it is found while the units still run; after them the statistics
-// and the outputs are one round trip to memory.
+// alone, so for small calls it is found while the units still run: after them
+// the statistics and the outputs are one round trip to memory.  Calls that can
+// be large have thousands of these blocks, most with nothing to join and none
+// resident before the units are done: there the units leave the answer in
+// memory.
 constexpr int kJoinWarps = 4, kJoinBatch = 8;
 
 template <class Core>
@@ -541,21 +682,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
   __shared__ float s_o[kJoinWarps][HD];
   __shared__ float s_l[kJoinWarps];
   const int u = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    const Piece piece = locate_piece<Core>(p, u, gridDim.x);
-    int4 split = make_int4(0, 0, 0, 0);
-    Segments<Core> sg;
-    sg.first(p, piece);
-    if (sg.valid && sg.t0 > 0) {  // never where streams are whole
-      const long long begin = piece.lo - sg.t0, end = begin + sg.n;  // places of the stream's tiles
-      if (piece.line.start(u - 1) <= begin)
-        split = make_int4(sg.seq, sg.stream, piece.line.first_from(end) - u + 1, 0);
+  int4 split;
+  if (p.spares) {
+    pdl_wait();
+    split = p.splits[u];
+  } else {
+    if (warp == 0) {
+      Count<Core> count;
+      count.read(p, 0);
+      Plan<Core> plan;
+      plan.make(p, count, false);
+      const Piece piece = plan.locate(p, count, u);
+      Segments<Core> sg;
+      sg.first(p, piece, plan.solo);
+      split = split_of<Core>(plan.line, piece, sg, u);
+      if (lane == 0) s_split = split;
     }
-    if (lane == 0) s_split = split;
+    __syncthreads();
+    pdl_wait();  // every block: the grid must not be over before the units are
+    split = s_split;
   }
-  __syncthreads();
-  pdl_wait();  // every block: the grid must not be over before the units are
-  const int4 split = s_split;
   const int kv_head = split.y / p.chunks;
   const int in_group = (split.y - kv_head * p.chunks) * CH;
   if (split.z == 0 || h >= p.group - in_group) return;
@@ -629,37 +775,63 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
 
 // What a core's launch needs; the same numbers size the workspace.
 struct CoreShape {
-  int TT, W, HD, CH, CTAS;
+  int TT, W, HD, CH, CTAS, COST;
 };
 
 inline int chunks_of(const CoreShape& c, const AttnDesc& p) { return (p.group + c.CH - 1) / c.CH; }
 
-// CTAs of a launch: what fits on the GPU at once, or less when the longest
-// sequences the block tables allow would not give every warp a tile.
-inline int units_of(const CoreShape& c, const AttnDesc& p, int sms) {
-  const long long tiles = std::max(1, p.max_len / c.TT + (p.max_len % c.TT != 0));
-  const long long streams = (long long)p.num_seqs * p.cache.num_kv_heads * chunks_of(c, p);
-  const long long most = (long long)c.CTAS * std::max(sms, 1);
-  if (streams >= most * c.W) return (int)most;
-  return (int)std::max(1LL, std::min(most, (tiles * streams + c.W - 1) / c.W));
+// Streams of a call, and places of its line at most (both saturating): every
+// sequence as long as the block tables allow.
+inline long long streams_of(const CoreShape& c, const AttnDesc& p) {
+  return (long long)p.num_seqs * std::min<long long>((long long)p.cache.num_kv_heads * chunks_of(c, p), INT_MAX);
 }
+inline long long most_tiles(const CoreShape& c, const AttnDesc& p) {
+  return std::max(1, p.max_len / c.TT + (p.max_len % c.TT != 0));
+}
+inline long long most_places(const CoreShape& c, const AttnDesc& p) {
+  return std::min(streams_of(c, p), (long long)INT_MAX) * (most_tiles(c, p) + c.COST);
+}
+
+// Pieces the line is cut into at most: what fits on the GPU at once, or less
+// when the longest sequences would not give every warp a tile.  *spares:
+// whether pieces can be long enough to give spare units, and streams are not
+// shared by more than eight pieces (where they are, joining the extra parts
+// costs more than evenness brings: one context of 131071 tokens 97.3 us with
+// spares, 93.9 without; 256 ragged contexts 191.7 and 197.9).
+inline int pieces_of(const CoreShape& c, const AttnDesc& p, int sms, bool* spares) {
+  const long long most = (long long)c.CTAS * std::max(sms, 1), streams = streams_of(c, p);
+  *spares = most_places(c, p) / most >= kSparePlaces && streams * 8 >= most;
+  if (streams >= most * c.W) return (int)most;
+  return (int)std::max(1LL, std::min(most, (most_tiles(c, p) * streams + c.W - 1) / c.W));
+}
+inline int grid_of(int pieces, bool spares) { return spares ? pieces * (kSpare + 1) : pieces; }
 
 inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct WorkspaceParts {
-  size_t partial, bytes;  // offset of the outputs (the statistics come first), and the whole
+  size_t stats, partial, bytes;  // offsets (the splits come first), and the whole
 };
 
 inline WorkspaceParts workspace_parts(const CoreShape& c, int units) {
   WorkspaceParts w;
-  w.partial = round256((size_t)2 * units * c.CH * sizeof(float2));
+  w.stats = round256((size_t)units * sizeof(int4));
+  w.partial = w.stats + round256((size_t)2 * units * c.CH * sizeof(float2));
   w.bytes = w.partial + round256((size_t)2 * units * c.CH * c.HD * sizeof(float));
   return w;
 }
 
+// Enough on any GPU: one with fewer SMs cuts fewer pieces, but they may be
+// long enough to give spares where those of a larger one are not.
+inline size_t workspace_bytes_of(const CoreShape& c, const AttnDesc& p) {
+  bool spares = false;
+  const int pieces = pieces_of(c, p, kMaxSmsForWorkspace, &spares);
+  const long long long_pieces = std::min<long long>(pieces, most_places(c, p) / kSparePlaces);
+  return workspace_parts(c, std::max(pieces, grid_of((int)long_pieces, true))).bytes;
+}
+
 template <class Core>
 constexpr CoreShape shape_of() {
-  return {Core::TT, Core::W, Core::HD, Core::CH, Core::CTAS};
+  return {Core::TT, Core::W, Core::HD, Core::CH, Core::CTAS, Core::STREAM_COST};
 }
 
 // Raises the kernel's shared-memory limit, once per device.
@@ -690,10 +862,12 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
   p.page_shift = 31 + log;
   p.page_magic = (unsigned)(((1ULL << p.page_shift) + p.cache.page_size - 1) / p.cache.page_size);
   p.whole_grains = p.cache.page_size % Core::GRAIN == 0;
-  const int units = units_of(c, p, std::min(device_sm_count(), kMaxSmsForWorkspace));
+  p.pieces = pieces_of(c, p, std::min(device_sm_count(), kMaxSmsForWorkspace), &p.spares);
+  const int units = grid_of(p.pieces, p.spares);
   const WorkspaceParts w = workspace_parts(c, units);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.stats = reinterpret_cast<float2*>(ws);
+  p.splits = reinterpret_cast<int4*>(ws);
+  p.stats = reinterpret_cast<float2*>(ws + w.stats);
   p.partial = reinterpret_cast<float*>(ws + w.partial);
   cudaError_t e = allow_smem<Core>((int)smem);
   if (e != cudaSuccess) return e;

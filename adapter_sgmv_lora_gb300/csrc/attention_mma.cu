@@ -300,12 +300,8 @@ cudaError_t launch_attention_mma(const AttnDesc& p, void* workspace, cudaStream_
 // The workspace is sized for either core, so that it depends on shapes only
 // and not on which one the alignments allow.
 size_t attention_workspace_bytes(const AttnDesc& p) {
-  const CoreShape g = generic_attention_shape(p);
-  size_t bytes = workspace_parts(g, units_of(g, p, kMaxSmsForWorkspace)).bytes;
-  if (p.dtype == LORA_DTYPE_BF16) {
-    const CoreShape m = mma_attention_shape(p);
-    bytes = std::max(bytes, workspace_parts(m, units_of(m, p, kMaxSmsForWorkspace)).bytes);
-  }
+  size_t bytes = workspace_bytes_of(generic_attention_shape(p), p);
+  if (p.dtype == LORA_DTYPE_BF16) bytes = std::max(bytes, workspace_bytes_of(mma_attention_shape(p), p));
   return bytes;
 }
 

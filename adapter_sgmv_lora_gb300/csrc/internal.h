@@ -230,13 +230,17 @@ struct AttnDesc {
   float* lse;  // or nullptr
   unsigned* status;
   // Filled in by the launcher: heads of a group are taken CH at a time
-  // (chunks per key/value head); token / page_size is
+  // (chunks per key/value head); the work is cut into at most `pieces` parts,
+  // which may give spare units; token / page_size is
   // token * page_magic >> page_shift for tokens below 2^31; whole_grains: no
-  // grain of tokens crosses a page's end; and the workspace's two parts.
+  // grain of tokens crosses a page's end; and the workspace's three parts.
   int chunks;
+  int pieces;
+  bool spares;
   unsigned page_magic;
   int page_shift;
   bool whole_grains;
+  int4* splits;    // [units] streams that several units share (calls that may give spares)
   float2* stats;   // [2 * units, CH] running maximum and sum of a partial result
   float* partial;  // [2 * units, CH, HD] its unnormalised output
 };

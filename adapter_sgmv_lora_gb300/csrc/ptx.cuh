@@ -166,6 +166,31 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Cluster launch control: asks for a block of this grid that has not started
+// to be cancelled and handed to this CTA; the 16-byte answer completes on
+// `bar`.  After an answer that says no, nothing more may be asked.
+__device__ __forceinline__ void launch_control_try_cancel(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_addr(answer)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+// The x index of the block handed over, or -1.
+__device__ __forceinline__ int launch_control_block(const void* answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+      : "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return x;
+}
+
 // Two fp32 additions in one packed instruction (each lane rounds to nearest
 // like a scalar add).
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {

@@ -358,6 +358,25 @@ def test_attention(case):
     check_attention(a, out, lse, 1.0 / hd ** 0.5, rows=range(0, len(lens), max(1, len(lens) // 40)))
 
 
+@pytest.mark.parametrize("dtype,lens,H,Hk,hd,order,tile", [
+    (BF, [4000, 6500, 9000, 1, 0, 5555] * 8, 16, 8, 128, "token", 16),
+    (BF, [17000, 33, 9111, 20001] * 12, 16, 4, 64, "head", 32),
+    (F32, [2100, 7, 3333, 1500] * 20, 8, 8, 64, "token", 16),
+    (BF, [1000 + 7 * i for i in range(300)], 16, 2, 128, "token", 16),   # more lengths than one count covers
+])
+def test_attention_spare_units(dtype, lens, H, Hk, hd, order, tile):
+    """Calls long enough that CTAs which are done take over spare units: whole streams and shared ones; the
+    same bits every time, whoever computed what."""
+    a = make_attention(lens, H, Hk, hd, 16, dtype, order, seed=11)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert sum(-(-n // tile) for n in lens) * Hk >= 2 * sms * 192   # else no spares
+    out, lse = run_attention(a)
+    check_attention(a, out, lse, 1.0 / hd ** 0.5, rows=range(0, len(lens), max(1, len(lens) // 12)))
+    for _ in range(5):
+        again, lse2 = run_attention(a)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_attention_same_bits_and_other_stream():
     a = make_attention([700, 3, 0, 5000, 64], 16, 4, 128, 16, BF, "token", seed=3)
     out, lse = run_attention(a)
