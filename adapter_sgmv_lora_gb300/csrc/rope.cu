@@ -130,11 +130,19 @@ __global__ void __launch_bounds__(kGenericWarps * 32) rope_generic_kernel(const 
 //
 // A warp takes one token, or a share of its groups, and works the angles out
 // for itself: no block barrier.  Query, key and value heads are grouped apart,
-// so what a group needs is the same for the whole warp.  kRopeBatch groups
-// are loaded at a time (the first before the angles): 4 KB a warp in flight.
-// Products go two to an instruction (f32x2).
+// so what a group needs is the same for the whole warp.  Four or five groups
+// are loaded at a time (the first before the angles): 4 to 5 KB a warp in
+// flight.  Products go two to an instruction (f32x2).  What is larger than L2
+// anyway is read and written as streams (either alone gains nothing).
+//
+// Bounded by memory: 8192 bf16 tokens of 64 + 2 x 8 heads, 336 MB, take 58 us
+// (5.8 TB/s; a plain copy of as many bytes takes 58, too), 66.6 us without the
+// streams.  With norms (40 + 2 x 8 heads, 235 MB) 58 us: there the reductions'
+// latency shows.
 constexpr int kRopeWarps = 4;  // per block
-constexpr int kRopeBatch = 4;
+// Groups a batch; measured 5 / 4: 80 heads 57.3 / 60.9 us, 48 heads 39.4 / 39.4,
+// 56 heads with norms 60.9 / 57.9.
+constexpr int kRopeBatch = 5, kRopeNormBatch = 4;
 
 // Four chunk elements (two for fp32) as fp32, and back.
 template <typename T>
@@ -201,8 +209,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
     if (h >= (is_q ? p.H : p.Hk)) return;
     const uint4* row =
         reinterpret_cast<const uint4*>(static_cast<const T*>(in.data) + t * in.row_stride + h * in.head_stride);
-    if (has0) x[0] = row[c0];
-    if (has1) x[1] = row[c1];
+    if (has0) x[0] = BATCH > 1 ? __ldcs(row + c0) : row[c0];
+    if (has1) x[1] = BATCH > 1 ? __ldcs(row + c1) : row[c1];
   };
   uint4 x[BATCH][2] = {};
 #pragma unroll
@@ -290,8 +298,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
     if (h >= (is_q ? p.H : p.Hk)) return;
     auto store = [&](void* base, long long off) {
       uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(base) + off);
-      if (has0) dst[c0] = r[0];
-      if (has1) dst[c1] = r[1];
+      if (has0) {
+        if (BATCH > 1) __stcs(dst + c0, r[0]);
+        else dst[c0] = r[0];
+      }
+      if (has1) {
+        if (BATCH > 1) __stcs(dst + c1, r[1]);
+        else dst[c1] = r[1];
+      }
     };
     if (is_q) {
       store(p.q_out.data, t * p.q_out.row_stride + h * p.q_out.head_stride);
@@ -356,25 +370,23 @@ cudaError_t launch_rope(const RopeDesc& p, cudaStream_t s) {
   // tokens of 48 heads: 6.1 us against 8.2 by the long one, which is mostly
   // instructions not yet in any cache).
   const bool few = (long long)p.T * groups <= 32LL * sms;
-  const int shares = few ? groups : (groups + kRopeBatch - 1) / kRopeBatch;
+  const bool norm = p.q_weight || p.k_weight;
+  const int batch = norm ? kRopeNormBatch : kRopeBatch;
+  const int shares = few ? groups : (groups + batch - 1) / batch;
   const unsigned grid = (unsigned)(((long long)p.T * shares + kRopeWarps - 1) / kRopeWarps);
   auto run = [&](auto kernel) { kernel<<<grid, kRopeWarps * 32, 0, s>>>(p, lph_log2, shares); };
-  auto by_batch = [&](auto batch) {
-    constexpr int B = decltype(batch)::value;
-    if (p.q_weight || p.k_weight) {
-      if (bf && inter) run(rope_kernel<__nv_bfloat16, true, true, B>);
-      else if (bf) run(rope_kernel<__nv_bfloat16, false, true, B>);
-      else if (inter) run(rope_kernel<float, true, true, B>);
-      else run(rope_kernel<float, false, true, B>);
-    } else {
-      if (bf && inter) run(rope_kernel<__nv_bfloat16, true, false, B>);
-      else if (bf) run(rope_kernel<__nv_bfloat16, false, false, B>);
-      else if (inter) run(rope_kernel<float, true, false, B>);
-      else run(rope_kernel<float, false, false, B>);
-    }
+  auto by_kind = [&](auto norm_c, auto batch_c) {
+    constexpr bool N = decltype(norm_c)::value;
+    constexpr int B = decltype(batch_c)::value;
+    if (bf && inter) run(rope_kernel<__nv_bfloat16, true, N, B>);
+    else if (bf) run(rope_kernel<__nv_bfloat16, false, N, B>);
+    else if (inter) run(rope_kernel<float, true, N, B>);
+    else run(rope_kernel<float, false, N, B>);
   };
-  if (few) by_batch(std::integral_constant<int, 1>());
-  else by_batch(std::integral_constant<int, kRopeBatch>());
+  if (few && norm) by_kind(std::true_type(), std::integral_constant<int, 1>());
+  else if (few) by_kind(std::false_type(), std::integral_constant<int, 1>());
+  else if (norm) by_kind(std::true_type(), std::integral_constant<int, kRopeNormBatch>());
+  else by_kind(std::false_type(), std::integral_constant<int, kRopeBatch>());
   return noted(cudaGetLastError(), LORA_PATH_ROPE);
 }
 
