@@ -668,16 +668,19 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   }
 }
 
-// Joins the partial results of the streams that several units share.  Block
-// (u, h): the stream that unit u starts inside of and unit u - 1 begins, and
-// the h-th query head of it; its warps share the partial results out and are
-// joined in warp order.  Partial 0 is the end of unit u - 1, partial i the
-// beginning of unit u - 1 + i.  Which stream that is follows from the lengths
-// alone, so for small calls it is found while the units still run: after them
-// the statistics and the outputs are one round trip to memory.  Calls that can
-// be large have thousands of these blocks, most with nothing to join and none
-// resident before the units are done: there the units leave the answer in
-// memory.
+// Joins the partial results of the streams that several units share: block u
+// those of the stream that unit u starts inside of and unit u - 1 begins.
+// Partial 0 is the end of unit u - 1, partial i the beginning of unit
+// u - 1 + i; they are summed in a fixed order.
+//
+// Small calls share few streams among many units: a block is one query head,
+// its warps share the partial results out.  Which stream it is follows from
+// the lengths alone and is found while the units still run; after them the
+// statistics and the outputs are one round trip to memory (one context of
+// 131071 tokens: 25 us of joining before, 5 now).  Calls that can be large
+// have hundreds of streams shared by two or three units and no room on the
+// SMs before the units are done: there the units leave the answer in memory
+// and a warp is one head.
 constexpr int kJoinWarps = 4, kJoinBatch = 8;
 
 template <class Core>
@@ -687,7 +690,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
   __shared__ int4 s_split;
   __shared__ float s_o[kJoinWarps][HD];
   __shared__ float s_l[kJoinWarps];
-  const int u = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The team that joins a head: a warp, or the block's.
+  const int team = p.spares ? 1 : kJoinWarps, rank = p.spares ? 0 : warp, leader = p.spares ? warp : 0;
+  const int h = p.spares ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
   int4 split;
   if (p.spares) {
     pdl_wait();
@@ -708,9 +714,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
     pdl_wait();  // every block: the grid must not be over before the units are
     split = s_split;
   }
-  const int kv_head = split.y / p.chunks;
+  const int kv_head = kv_head_of(p, split.y);
   const int in_group = (split.y - kv_head * p.chunks) * CH;
-  if (split.z == 0 || h >= p.group - in_group) return;
+  if (split.z == 0 || h >= min(CH, p.group - in_group)) return;  // the whole team
   auto slot = [&](int i) { return (long long)(i == 0 ? 2 * (u - 1) + 1 : 2 * (u - 1 + i)) * CH + h; };
   // This warp's first partial results are on their way before the statistics
   // are looked at.
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
   auto load = [&](int from) {
 #pragma unroll
     for (int b = 0; b < kJoinBatch; ++b) {
-      const int i = from + b * kJoinWarps;
+      const int i = from + b * team;
       st_m[b] = kNegInf;
       st_l[b] = 0.f;
 #pragma unroll
@@ -733,7 +739,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
       }
     }
   };
-  load(warp);
+  load(rank);
   float m = kNegInf;
   bool bad = false;
   for (int i = lane; i < split.z; i += 32) {
@@ -743,15 +749,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if (__any_sync(0xffffffffu, bad)) {  // the same in every warp
-    if (threadIdx.x == 0) atomicOr(p.status, LORA_DEV_BAD_PAGE);
+  if (__any_sync(0xffffffffu, bad)) {  // the same in every warp of the team
+    if (rank == 0 && lane == 0) atomicOr(p.status, LORA_DEV_BAD_PAGE);
     return;
   }
   float l = 0.f, o[VPL] = {};
-  for (int from = warp; from < split.z; from += kJoinBatch * kJoinWarps) {
-    if (from != warp) load(from);
+  for (int from = rank; from < split.z; from += kJoinBatch * team) {
+    if (from != rank) load(from);
 #pragma unroll
     for (int b = 0; b < kJoinBatch; ++b) {
+      if (from + b * team >= split.z) break;
       const float f = weight_of(st_m[b], m);
       l = fmaf(st_l[b], f, l);
 #pragma unroll
@@ -761,20 +768,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
 #pragma unroll
   for (int e = 0; e < VPL; ++e) s_o[warp][e * 32 + lane] = o[e];
   if (lane == 0) s_l[warp] = l;
-  __syncthreads();
+  if (p.spares) __syncwarp();
+  else __syncthreads();
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) l += s_l[w];
+  for (int w = 0; w < kJoinWarps; ++w)
+    if (w < team) l += s_l[leader + w];
   const int head = kv_head * p.group + in_group + h;
   T* out = static_cast<T*>(p.out.data) + split.x * p.out.row_stride + head * p.out.head_stride;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int d = threadIdx.x; d < p.cache.head_dim; d += kJoinWarps * 32) {
+  for (int d = rank * 32 + lane; d < p.cache.head_dim; d += team * 32) {
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) sum += s_o[w][d];
+    for (int w = 0; w < kJoinWarps; ++w)
+      if (w < team) sum += s_o[leader + w][d];
     out[d] = from_f<T>(sum * inv);
   }
-  if (threadIdx.x == 0 && p.lse) p.lse[(long long)split.x * p.num_heads + head] = (m + log2f(l)) * kLn2;
+  if (rank == 0 && lane == 0 && p.lse) p.lse[(long long)split.x * p.num_heads + head] = (m + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------- host --
@@ -884,7 +894,8 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
   attention_kernel<Core><<<units, Core::W * 32, smem, s>>>(p);
   if ((e = noted(cudaGetLastError(), path)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units, std::min(Core::CH, p.group));
+  const int heads = std::min(Core::CH, p.group);
+  cfg.gridDim = dim3(units, p.spares ? (heads + kJoinWarps - 1) / kJoinWarps : heads);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
