@@ -297,12 +297,6 @@ struct Plan {
   }
 };
 
-// Keys and values that pass L2 by in size and are read by one CTA only are
-// first out: what is shared (partial results, tables, queries) then stays.
-__device__ __forceinline__ uint64_t cache_policy(const AttnDesc& p) {
-  return p.stream_cache && p.chunks == 1 ? policy_evict_first() : policy_evict_normal();
-}
-
 // Key/value head of a stream.
 __device__ __forceinline__ int kv_head_of(const AttnDesc& p, int stream) {
   return p.chunks == 1 ? stream : stream / p.chunks;
@@ -378,15 +372,18 @@ struct TileCursor {
   int tile;
   int page, slot;  // slot: token within the page; below 0: no token
 
+  // No branch per lane: a lane past the end looks its sequence's last token
+  // up, so the warp stays together.
   __device__ __forceinline__ void look_up(const AttnDesc& p) {
     const int j = tile * Core::TT + (int)(p.whole_grains ? (threadIdx.x & (GRAINS - 1)) * Core::GRAIN
                                                          : threadIdx.x & (Core::TT - 1));
     page = 0;
     slot = -1;
-    if (j < seg.len) {
-      const int i = (int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift);
-      slot = j - i * p.cache.page_size;
+    if (seg.len > 0) {  // the same on every lane
+      const int jj = min(j, seg.len - 1);
+      const int i = (int)(((unsigned long long)(unsigned)jj * p.page_magic) >> p.page_shift);
       page = p.tables[seg.seq * p.table_stride + i];
+      slot = j < seg.len ? jj - i * p.cache.page_size : -1;
     }
   }
   __device__ __forceinline__ void settle(const AttnDesc& p, int rank) {
@@ -414,8 +411,9 @@ struct TileCursor {
   __device__ __forceinline__ long long offset(const AttnDesc& p, bool* bad) const {
     const bool off_cache = slot >= 0 && (unsigned)page >= (unsigned)p.cache.num_pages;
     *bad = __any_sync(0xffffffffu, off_cache);
-    if (slot < 0 || off_cache) return -1;
-    return page * p.cache.page_stride + slot * p.cache.token_stride + kv_head_of(p, seg.stream) * p.cache.head_stride;
+    const long long at = page * p.cache.page_stride + slot * p.cache.token_stride +
+                         kv_head_of(p, seg.stream) * p.cache.head_stride;
+    return slot < 0 || off_cache ? -1 : at;
   }
   // Tokens of the tile.
   __device__ __forceinline__ int tokens() const { return min(Core::TT, seg.len - tile * Core::TT); }
@@ -559,6 +557,7 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   int asked = 0;  // requests for spare units answered so far
 #pragma unroll 1
   while (true) {
+    __syncwarp();  // ldmatrix and mma need the warp's lanes together; a block barrier does not promise that
     if (solo) core.begin_solo(p, seg.seq, head0, heads);
     else core.begin(p, heads);
     Segments<Core> after = seg;
@@ -871,10 +870,6 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
                           (size_t)Core::W * Core::COMB * ((Core::HD + 4) * 4 + 8) + Core::EXTRA_BYTES;
   static_assert(smem <= 227 * 1024 - 256, "a CTA's shared memory");
   p.chunks = chunks_of(c, p);
-  // The sequences' cache against L2 (129 MB): 256 ragged contexts 188.2 us as
-  // a stream against 191.4, one of 131071 tokens 91.4 against 95.0.
-  p.stream_cache = (double)p.num_seqs * p.max_len * p.cache.num_kv_heads * p.cache.head_dim * 2 *
-                       sizeof(typename Core::T) > 128e6;
   // page_size <= 2^log: magic = ceil(2^(31 + log) / page_size) is below 2^32
   // and exact for tokens below 2^31.
   int log = 0;
@@ -912,7 +907,7 @@ bool mma_attention_ok(const AttnDesc& p);
 CoreShape mma_attention_shape(const AttnDesc& p);
 cudaError_t launch_attention_mma(const AttnDesc& p, void* workspace, cudaStream_t s);
 // attention_generic.cu: fp32 arithmetic, any type, size and alignment.
-CoreShape generic_attention_shape(const AttnDesc& p);
+size_t generic_attention_workspace(const AttnDesc& p);
 cudaError_t launch_attention_generic(const AttnDesc& p, void* workspace, cudaStream_t s);
 
 }  // namespace lora

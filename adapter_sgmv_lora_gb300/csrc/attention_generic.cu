@@ -1,30 +1,70 @@
 // attention_generic.cu -- paged decode attention in fp32 arithmetic on the
-// CUDA cores: fp32 caches, and bf16 caches whose shapes or alignments the
-// tensor-core core does not take.  The frame is attention.cuh.
+// CUDA cores: fp32 caches, and bf16 caches whose page sizes, shapes or
+// alignments the tensor-core core does not take (pages that are not whole
+// grains of 16 tokens above all).  The frame is attention.cuh.
 //
-// One warp works on a tile of TT = 8 or 16 tokens held as fp32 rows in shared
-// memory.  Scores: lane (r, g) takes token r and every (32 / TT)-th 16-byte
-// chunk of its key, so the queries come as broadcasts; the chunks are swizzled
-// by the token so that 8 tokens' reads fall on different banks.  Output: each
-// lane owns HD / 32 neighbouring columns and walks the tokens.
+// One warp works on a tile of TT = 8 or 16 tokens held in shared memory in the
+// cache's type (fp32 where rows are not on 16-byte boundaries).  Scores: lane
+// (r, g) takes token r and every (32 / TT)-th 16-byte chunk of its key, so the
+// queries come as broadcasts; the chunks are swizzled by the token so that 8
+// tokens' reads fall on different banks.  Output: each lane owns HD / 32
+// neighbouring columns and walks the tokens.
+#include <type_traits>
+
 #include "attention.cuh"
 
 namespace lora {
 namespace {
 
-// ASYNC: fp32 rows on 16-byte boundaries come in by asynchronous copies; else
-// element by element, converted on the way.
+// N neighbouring values, 4 N or 2 N bytes on a boundary of as many.
+template <int N>
+__device__ __forceinline__ void read_row(const float* p, float (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 w = *reinterpret_cast<const float4*>(p + i);
+      v[i] = w.x;
+      v[i + 1] = w.y;
+      v[i + 2] = w.z;
+      v[i + 3] = w.w;
+    }
+  } else {
+    const float2 w = *reinterpret_cast<const float2*>(p);
+    v[0] = w.x;
+    v[1] = w.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void read_row(const __nv_bfloat16* p, float (&v)[N]) {
+  uint32_t w[N / 2];
+  if constexpr (N == 8) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+  else if constexpr (N == 4) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+  else w[0] = *reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// ASYNC: rows on 16-byte boundaries come in by asynchronous copies, as they
+// are; else element by element, converted to fp32 on the way.
 template <typename T_, int HD_, int CH_, bool ASYNC>
 struct GenericCore {
   using T = T_;
-  // 16 tokens where a tile of them is small: the fixed steps of a tile weigh less.
-  static constexpr int TT = HD_ == 64 ? 16 : 8, GRAIN = TT, GROUPS = 32 / TT, W = 4, HD = HD_, CH = CH_, COMB = CH_ < 4 ? CH_ : 4;
-  static constexpr int STAGE_BYTES = 2 * TT * HD * 4;
-  static constexpr int STAGES = CH == 8 && HD > 64 ? 2 : 3;
+  using S = std::conditional_t<ASYNC, T, float>;  // type of a staged row
+  static constexpr int HD = HD_, CH = CH_, COMB = CH_ < 4 ? CH_ : 4, W = 4;
+  // 16 tokens where a row of them is short: the fixed steps of a tile weigh less.
+  static constexpr int TT = HD * sizeof(S) <= 256 ? 16 : 8, GRAIN = TT, GROUPS = 32 / TT;
+  static constexpr int E = 16 / sizeof(S), CHUNKS = HD / E;  // of a row
+  static constexpr int STAGE_BYTES = 2 * TT * HD * sizeof(S);
   static constexpr int CTAS = HD <= 128 ? 2 : 1;
   static constexpr int VPL = HD / 32;  // output columns per lane
   static constexpr int STREAM_COST = 6;
   static constexpr int EXTRA_BYTES = W * (CH * HD + TT * CH) * 4;
+  // As many stages as leave room for CTAS blocks on an SM, up to six.
+  static constexpr int ROOM = (CTAS == 2 ? 115200 : 231000) - W * COMB * ((HD + 4) * 4 + 8) - EXTRA_BYTES;
+  static constexpr int STAGES = ROOM / (W * STAGE_BYTES) < 6 ? ROOM / (W * STAGE_BYTES) : 6;
   static_assert(CH <= 8, "");
 
   float* shared;
@@ -41,13 +81,14 @@ struct GenericCore {
         q(shared),
         prob(q + W * CH * HD + (threadIdx.x >> 5) * TT * CH),
         scale(p.scale * kLog2e),
-        policy(cache_policy(p)) {}
+        policy(policy_evict_first()) {}
 
-  static __device__ __forceinline__ int at(int r, int chunk) { return r * HD + ((chunk ^ (r & 7)) << 2); }
+  // Element of chunk c of row r.
+  static __device__ __forceinline__ int at(int r, int c) { return r * HD + (c ^ (r & 7)) * E; }
 
   __device__ __forceinline__ void load(const AttnDesc& p, uint8_t* stage, long long off, int n) const {
-    float* k = reinterpret_cast<float*>(stage);
-    float* v = k + TT * HD;
+    S* k = reinterpret_cast<S*>(stage);
+    S* v = k + TT * HD;
     const int lane = threadIdx.x & 31;
     const T* kg = static_cast<const T*>(p.cache.k);
     const T* vg = static_cast<const T*>(p.cache.v);
@@ -55,11 +96,11 @@ struct GenericCore {
     if (p.whole_grains) off = off < 0 || (lane & (TT - 1)) >= n ? -1 : off + (lane & (TT - 1)) * p.cache.token_stride;
     if constexpr (ASYNC) {
 #pragma unroll
-      for (int i = 0; i < TT * HD / 4 / 32; ++i) {
-        const int e = i * 32 + lane, r = e / (HD / 4), c = e % (HD / 4);
+      for (int i = 0; i < TT * CHUNKS / 32; ++i) {
+        const int e = i * 32 + lane, r = e / CHUNKS, c = e % CHUNKS;
         const long long row = __shfl_sync(0xffffffffu, off, r);
-        if (c * 4 < p.cache.head_dim) {
-          const long long src = row < 0 ? 0 : row + c * 4;
+        if (c * E < p.cache.head_dim) {
+          const long long src = row < 0 ? 0 : row + c * E;
           cp_async16_zfill(k + at(r, c), kg + src, row < 0 ? 0 : 16, policy);
           cp_async16_zfill(v + at(r, c), vg + src, row < 0 ? 0 : 16, policy);
         }
@@ -69,7 +110,7 @@ struct GenericCore {
       for (int r = 0; r < TT; ++r) {
         const long long row = __shfl_sync(0xffffffffu, off, r);
         for (int d = lane; d < p.cache.head_dim; d += 32) {
-          const int dst = at(r, d >> 2) + (d & 3);
+          const int dst = at(r, d / E) + d % E;
           k[dst] = row < 0 ? 0.f : to_f(kg[row + d]);
           v[dst] = row < 0 ? 0.f : to_f(vg[row + d]);
         }
@@ -121,22 +162,22 @@ struct GenericCore {
   }
 
   __device__ __forceinline__ void tile(const AttnDesc& p, const uint8_t* stage, int n) {
-    const float* k = reinterpret_cast<const float*>(stage);
-    const float* v = k + TT * HD;
+    const S* k = reinterpret_cast<const S*>(stage);
+    const S* v = k + TT * HD;
     const int lane = threadIdx.x & 31, r = lane % TT, g = lane / TT;
     float s[CH] = {};
 #pragma unroll 4
-    for (int i = 0; i < HD / 4 / GROUPS; ++i) {
+    for (int i = 0; i < CHUNKS / GROUPS; ++i) {
       const int c = i * GROUPS + g;
-      const float4 kv = *reinterpret_cast<const float4*>(k + at(r, c));
+      float kv[E];
+      read_row<E>(k + at(r, c), kv);
 #pragma unroll
       for (int h = 0; h < CH; ++h) {
         if (h < heads) {
-          const float4 qv = *reinterpret_cast<const float4*>(q + h * HD + c * 4);
-          s[h] = fmaf(kv.x, qv.x, s[h]);
-          s[h] = fmaf(kv.y, qv.y, s[h]);
-          s[h] = fmaf(kv.z, qv.z, s[h]);
-          s[h] = fmaf(kv.w, qv.w, s[h]);
+          float qv[E];
+          read_row<E>(q + h * HD + c * E, qv);
+#pragma unroll
+          for (int e = 0; e < E; ++e) s[h] = fmaf(kv[e], qv[e], s[h]);
         }
       }
     }
@@ -162,11 +203,16 @@ struct GenericCore {
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
+      // This lane's columns: within one chunk, or whole chunks (fp32, 256 wide).
       float vv[VPL];
+      constexpr int PART = VPL < E ? VPL : E;
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) {
+      for (int e = 0; e < VPL; e += PART) {
+        float part[PART];
         const int d = lane * VPL + e;
-        vv[e] = v[at(j, d >> 2) + (d & 3)];
+        read_row<PART>(v + at(j, d / E) + d % E, part);
+#pragma unroll
+        for (int x = 0; x < PART; ++x) vv[e + x] = part[x];
       }
 #pragma unroll
       for (int h = 0; h < CH; ++h) {
@@ -194,12 +240,13 @@ struct GenericCore {
   }
 };
 
-// fp32 rows on 16-byte boundaries.
+// Rows on 16-byte boundaries.
 bool async_ok(const AttnDesc& p) {
   const CacheDesc& c = p.cache;
+  const int e = p.dtype == LORA_DTYPE_BF16 ? 8 : 4;
   const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v);
-  return p.dtype == LORA_DTYPE_F32 && (low & 15) == 0 && c.head_dim % 4 == 0 && c.page_stride % 4 == 0 &&
-         c.token_stride % 4 == 0 && c.head_stride % 4 == 0;
+  return (low & 15) == 0 && c.head_dim % e == 0 && c.page_stride % e == 0 && c.token_stride % e == 0 &&
+         c.head_stride % e == 0;
 }
 
 template <typename T, int HD, bool ASYNC>
@@ -217,18 +264,27 @@ cudaError_t by_width(const AttnDesc& p, void* ws, cudaStream_t s) {
 
 }  // namespace
 
-CoreShape generic_attention_shape(const AttnDesc& p) {
-  const int hd = p.cache.head_dim <= 64 ? 64 : (p.cache.head_dim <= 128 ? 128 : 256);
-  CoreShape c = shape_of<GenericCore<float, 64, 8, true>>();
-  c.TT = hd <= 64 ? 16 : 8;
-  c.HD = hd;
-  c.CH = p.group == 1 ? 1 : 8;
-  c.CTAS = hd <= 128 ? 2 : 1;
-  return c;
+template <typename T>
+size_t most_workspace(const AttnDesc& p) {
+  auto of = [&](auto* core) { return workspace_bytes_of(shape_of<std::remove_pointer_t<decltype(core)>>(), p); };
+  auto both = [&](auto hd) {
+    constexpr int HD = decltype(hd)::value;
+    if (p.group == 1) return std::max(of((GenericCore<T, HD, 1, true>*)nullptr), of((GenericCore<T, HD, 1, false>*)nullptr));
+    return std::max(of((GenericCore<T, HD, 8, true>*)nullptr), of((GenericCore<T, HD, 8, false>*)nullptr));
+  };
+  if (p.cache.head_dim <= 64) return both(std::integral_constant<int, 64>());
+  if (p.cache.head_dim <= 128) return both(std::integral_constant<int, 128>());
+  return both(std::integral_constant<int, 256>());
+}
+
+size_t generic_attention_workspace(const AttnDesc& p) {
+  return p.dtype == LORA_DTYPE_BF16 ? most_workspace<__nv_bfloat16>(p) : most_workspace<float>(p);
 }
 
 cudaError_t launch_attention_generic(const AttnDesc& p, void* workspace, cudaStream_t s) {
-  if (p.dtype == LORA_DTYPE_BF16) return by_width<__nv_bfloat16, false>(p, workspace, s);
+  if (p.dtype == LORA_DTYPE_BF16)
+    return async_ok(p) ? by_width<__nv_bfloat16, true>(p, workspace, s)
+                       : by_width<__nv_bfloat16, false>(p, workspace, s);
   return async_ok(p) ? by_width<float, true>(p, workspace, s) : by_width<float, false>(p, workspace, s);
 }
 

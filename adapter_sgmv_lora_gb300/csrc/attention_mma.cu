@@ -49,7 +49,7 @@ struct MmaCore {
   uint4 next_q[(CH * HD / 8 + W * 32 - 1) / (W * 32)];
 
   __device__ __forceinline__ MmaCore(const AttnDesc& p, uint8_t* extra)
-      : scale(p.scale * kLog2e), policy(cache_policy(p)), q_shared(extra) {}
+      : scale(p.scale * kLog2e), policy(policy_evict_first()), q_shared(extra) {}
 
   // Byte offset of 16-byte chunk c of row r: swizzled, so the 8 rows of an
   // ldmatrix block fall on different banks.
@@ -62,33 +62,20 @@ struct MmaCore {
     const int lane = threadIdx.x & 31, r0 = lane / (HD / 8), c = lane % (HD / 8);
     const T* kg = static_cast<const T*>(p.cache.k);
     const T* vg = static_cast<const T*>(p.cache.v);
-    if (p.whole_grains) {
 #pragma unroll
-      for (int j = 0; j < GRAINS; ++j) {
-        const long long first = __shfl_sync(0xffffffffu, off, j);
-        if (c * 8 < p.cache.head_dim) {
-          long long src = (first < 0 ? 0 : first + r0 * p.cache.token_stride) + c * 8;
-          const long long step = first < 0 ? 0 : ROWS * p.cache.token_stride;
-          const int live = first < 0 ? 0 : n;
+    for (int j = 0; j < GRAINS; ++j) {
+      const long long first = __shfl_sync(0xffffffffu, off, j);
+      if (c * 8 < p.cache.head_dim) {
+        long long src = (first < 0 ? 0 : first + r0 * p.cache.token_stride) + c * 8;
+        const long long step = first < 0 ? 0 : ROWS * p.cache.token_stride;
+        const int live = first < 0 ? 0 : n;
 #pragma unroll
-          for (int i = 0; i < GRAIN / ROWS; ++i) {
-            const int r = j * GRAIN + i * ROWS + r0;
-            const uint32_t bytes = r < live ? 16 : 0;
-            cp_async16_zfill(stage + at(r, c), kg + src, bytes, policy);
-            cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, bytes, policy);
-            src += step;
-          }
-        }
-      }
-    } else {
-#pragma unroll 2
-      for (int i = 0; i < TT / ROWS; ++i) {
-        const int r = i * ROWS + r0;
-        const long long row = __shfl_sync(0xffffffffu, off, r);
-        if (c * 8 < p.cache.head_dim) {
-          const long long src = row < 0 ? 0 : row + c * 8;
-          cp_async16_zfill(stage + at(r, c), kg + src, row < 0 ? 0 : 16, policy);
-          cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, row < 0 ? 0 : 16, policy);
+        for (int i = 0; i < GRAIN / ROWS; ++i) {
+          const int r = j * GRAIN + i * ROWS + r0;
+          const uint32_t bytes = r < live ? 16 : 0;
+          cp_async16_zfill(stage + at(r, c), kg + src, bytes, policy);
+          cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, bytes, policy);
+          src += step;
         }
       }
     }
@@ -264,11 +251,13 @@ struct MmaCore {
 
 }  // namespace
 
+// Pages hold whole grains of 16 tokens; rows and queries are on 16-byte
+// boundaries.
 bool mma_attention_ok(const AttnDesc& p) {
   const CacheDesc& c = p.cache;
   const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) |
                    reinterpret_cast<uintptr_t>(p.q.data);
-  return p.dtype == LORA_DTYPE_BF16 && (low & 15) == 0 && c.head_dim % 8 == 0 && c.page_stride % 8 == 0 &&
+  return p.dtype == LORA_DTYPE_BF16 && c.page_size % 16 == 0 && (low & 15) == 0 && c.head_dim % 8 == 0 && c.page_stride % 8 == 0 &&
          c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && p.q.row_stride % 8 == 0 && p.q.head_stride % 8 == 0;
 }
 
@@ -301,7 +290,7 @@ cudaError_t launch_attention_mma(const AttnDesc& p, void* workspace, cudaStream_
 // The workspace is sized for either core, so that it depends on shapes only
 // and not on which one the alignments allow.
 size_t attention_workspace_bytes(const AttnDesc& p) {
-  size_t bytes = workspace_bytes_of(generic_attention_shape(p), p);
+  size_t bytes = generic_attention_workspace(p);
   if (p.dtype == LORA_DTYPE_BF16) bytes = std::max(bytes, workspace_bytes_of(mma_attention_shape(p), p));
   return bytes;
 }

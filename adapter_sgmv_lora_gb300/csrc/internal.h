@@ -237,7 +237,6 @@ struct AttnDesc {
   int chunks;
   int pieces;
   bool spares;
-  bool stream_cache;  // the cache is larger than L2
   unsigned page_magic;
   int page_shift;
   bool whole_grains;

@@ -353,9 +353,40 @@ def test_attention(case):
     dtype, lens, H, Hk, hd, ps, order = case
     a = make_attention(lens, H, Hk, hd, ps, dtype, order)
     out, lse = run_attention(a)
-    core = lk.PATH_MMA_ATTENTION if dtype == BF and hd % 8 == 0 and order != "gap" else lk.PATH_GENERIC_ATTENTION
+    mma = dtype == BF and hd % 8 == 0 and ps % 16 == 0 and order != "gap"
+    core = lk.PATH_MMA_ATTENTION if mma else lk.PATH_GENERIC_ATTENTION
     assert lk.lora_last_call_path()[0] & ~lk.PATH_JOIN == core
     check_attention(a, out, lse, 1.0 / hd ** 0.5, rows=range(0, len(lens), max(1, len(lens) // 40)))
+
+
+@pytest.mark.parametrize("dtype,lens,H,Hk,hd,ps,order", [
+    (BF, [8 + 37 * i % 129 for i in range(145)] + [0], 64, 8, 128, 1, "token"),
+    (BF, [8 + 37 * i % 129 for i in range(145)] + [0], 64, 8, 80, 1, "head"),
+    (BF, [300 + 37 * i % 129 for i in range(60)], 32, 16, 128, 24, "token"),
+    (BF, [5 + 53 * i % 400 for i in range(200)], 16, 8, 64, 3, "token"),
+    (BF, [5 + 53 * i % 400 for i in range(100)], 32, 8, 32, 8, "side"),
+    (BF, [5 + 53 * i % 200 for i in range(100)], 16, 8, 256, 5, "token"),
+    (BF, [5 + 53 * i % 200 for i in range(100)], 64, 4, 128, 1, "token"),
+    (F32, [5 + 53 * i % 200 for i in range(100)], 8, 8, 64, 3, "token"),
+    (F32, [5 + 53 * i % 200 for i in range(100)], 32, 8, 128, 1, "token"),
+    (BF, [1 + 11 * i % 128 for i in range(200)], 16, 4, 128, 1, "token"),   # warps on their own, up to 8 tiles
+    (BF, [1 + 11 * i % 128 for i in range(200)], 16, 4, 128, 16, "token"),
+    (BF, [900 + 53 * i % 400 for i in range(24)], 32, 8, 128, 16, "token"),
+    (BF, [900 + 53 * i % 400 for i in range(24)], 64, 8, 128, 16, "head"),
+    (BF, [900 + 53 * i % 400 for i in range(24)], 16, 8, 64, 32, "token"),
+    (BF, [300 + 53 * i % 200 for i in range(24)], 64, 4, 256, 16, "token"),
+    (BF, [300 + 53 * i % 200 for i in range(50)], 8, 8, 32, 16, "token"),
+    (BF, [1 + 11 * i % 256 for i in range(200)], 8, 4, 64, 5, "head"),
+    (F32, [1 + 11 * i % 64 for i in range(200)], 16, 4, 128, 3, "token"),
+])
+def test_attention_many_streams_a_block(dtype, lens, H, Hk, hd, ps, order):
+    """Several streams to every block, each of several tiles, with pages that end inside a tile: the lanes of a
+    warp look different pages up on the way from one stream to the next."""
+    a = make_attention(lens, H, Hk, hd, ps, dtype, order, seed=12)
+    out, lse = run_attention(a)
+    check_attention(a, out, lse, 1.0 / hd ** 0.5, rows=list(range(0, len(lens), 17)) + [len(lens) - 1])
+    again, lse2 = run_attention(a)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("dtype,lens,H,Hk,hd,order,tile", [
