@@ -1,7 +1,7 @@
 // attention_generic.cu -- paged decode attention in fp32 arithmetic on the
 // CUDA cores: fp32 caches, and bf16 caches whose page sizes, shapes or
 // alignments the tensor-core core does not take (pages that are not whole
-// grains of 16 tokens above all).  The frame is attention.cuh.
+// grains of 8 tokens above all).  The frame is attention.cuh.
 //
 // One warp works on a tile of TT = 8 or 16 tokens held in shared memory in the
 // cache's type (fp32 where rows are not on 16-byte boundaries).  Scores: lane

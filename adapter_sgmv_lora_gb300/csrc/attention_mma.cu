@@ -24,13 +24,14 @@
 namespace lora {
 namespace {
 
-// NT: query heads a stream, in eights.
-template <int HD_, int NT>
+// NT: query heads a stream, in eights.  GRAIN: tokens that lie in one page.
+template <int HD_, int NT, int GRAIN_>
 struct MmaCore {
   using T = __nv_bfloat16;
   // A stage is 8 KB (4 KB for the narrowest heads): narrow heads take two
-  // grains of 16 tokens a tile, so the fixed steps of a tile weigh the same.
-  static constexpr int GRAIN = 16, GRAINS = HD_ <= 64 ? 2 : 1, TT = GRAIN * GRAINS;
+  // blocks of 16 tokens a tile, so the fixed steps of a tile weigh the same.
+  static constexpr int BLOCKS = HD_ <= 64 ? 2 : 1, TT = 16 * BLOCKS;
+  static constexpr int GRAIN = GRAIN_, GRAINS = TT / GRAIN;
   static constexpr int W = 4, HD = HD_, CH = 8 * NT, COMB = 4;
   static constexpr int STAGE_BYTES = 2 * TT * HD * 2;
   static constexpr int STAGES = HD == 32 ? 6 : 3;
@@ -148,35 +149,35 @@ struct MmaCore {
   __device__ __forceinline__ void tile(const AttnDesc& p, const uint8_t* stage, int n_tokens) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
     const uint32_t kb = smem_addr(stage), vb = kb + TT * HD * 2;
-    // Scores: a grain's products in two chains (one where there are two
-    // grains), summed below.
-    constexpr int CHAINS = GRAINS == 1 ? 2 : 1;
-    float s[GRAINS][NT][CHAINS][4] = {};
+    // Scores: a block's products in two chains (one where there are two
+    // blocks), summed below.
+    constexpr int CHAINS = BLOCKS == 1 ? 2 : 1;
+    float s[BLOCKS][NT][CHAINS][4] = {};
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
 #pragma unroll
-      for (int j = 0; j < GRAINS; ++j) {
+      for (int j = 0; j < BLOCKS; ++j) {
         uint32_t a[4];
-        ldsm_x4(kb + at(j * GRAIN + (lane & 15), 2 * k + (lane >> 4)), a[0], a[1], a[2], a[3]);
+        ldsm_x4(kb + at(j * 16 + (lane & 15), 2 * k + (lane >> 4)), a[0], a[1], a[2], a[3]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) mma_bf16_16816(s[j][n][k % CHAINS], a, q[k][n][0], q[k][n][1]);
       }
     }
-    uint32_t hi[GRAINS][NT][2], lo[GRAINS][NT][2];
+    uint32_t hi[BLOCKS][NT][2], lo[BLOCKS][NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float x[GRAINS][4], keep[2];
+      float x[BLOCKS][4], keep[2];
 #pragma unroll
-      for (int j = 0; j < GRAINS; ++j)
+      for (int j = 0; j < BLOCKS; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[j][e] = (CHAINS == 2 ? s[j][n][0][e] + s[j][n][CHAINS - 1][e] : s[j][n][0][e]) * scale;
-          if (j * GRAIN + g + (e < 2 ? 0 : 8) >= n_tokens) x[j][e] = kNegInf;
+          if (j * 16 + g + (e < 2 ? 0 : 8) >= n_tokens) x[j][e] = kNegInf;
         }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float top = fmaxf(x[0][e], x[0][e + 2]);
-        if (GRAINS == 2) top = fmaxf(top, fmaxf(x[GRAINS - 1][e], x[GRAINS - 1][e + 2]));
+        if (BLOCKS == 2) top = fmaxf(top, fmaxf(x[BLOCKS - 1][e], x[BLOCKS - 1][e + 2]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float now = fmaxf(m[n][e], top);
@@ -185,7 +186,7 @@ struct MmaCore {
         m[n][e] = now;
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < GRAINS; ++j) {
+        for (int j = 0; j < BLOCKS; ++j) {
           x[j][e] = pow2(x[j][e] - base);
           x[j][e + 2] = pow2(x[j][e + 2] - base);
           sum += x[j][e] + x[j][e + 2];
@@ -193,7 +194,7 @@ struct MmaCore {
         l[n][e] = fmaf(l[n][e], keep[e], sum);  // this lane's tokens; summed over lanes in put
       }
 #pragma unroll
-      for (int j = 0; j < GRAINS; ++j) {
+      for (int j = 0; j < BLOCKS; ++j) {
         split_hi_lo_bf16x2(x[j][0], x[j][1], hi[j][n][0], lo[j][n][0]);
         split_hi_lo_bf16x2(x[j][2], x[j][3], hi[j][n][1], lo[j][n][1]);
 #pragma unroll
@@ -215,9 +216,9 @@ struct MmaCore {
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
 #pragma unroll
-      for (int j = 0; j < GRAINS; ++j) {
+      for (int j = 0; j < BLOCKS; ++j) {
         uint32_t a[4];
-        ldsm_x4_trans(vb + at(j * GRAIN + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), a[0], a[1],
+        ldsm_x4_trans(vb + at(j * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), a[0], a[1],
                       a[2], a[3]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -251,30 +252,34 @@ struct MmaCore {
 
 }  // namespace
 
-// Pages hold whole grains of 16 tokens; rows and queries are on 16-byte
+// Pages hold whole grains of 8 tokens; rows and queries are on 16-byte
 // boundaries.
 bool mma_attention_ok(const AttnDesc& p) {
   const CacheDesc& c = p.cache;
   const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) |
                    reinterpret_cast<uintptr_t>(p.q.data);
-  return p.dtype == LORA_DTYPE_BF16 && c.page_size % 16 == 0 && (low & 15) == 0 && c.head_dim % 8 == 0 && c.page_stride % 8 == 0 &&
+  return p.dtype == LORA_DTYPE_BF16 && c.page_size % 8 == 0 && (low & 15) == 0 && c.head_dim % 8 == 0 && c.page_stride % 8 == 0 &&
          c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && p.q.row_stride % 8 == 0 && p.q.head_stride % 8 == 0;
 }
 
-// f(a core's type) for the head width and group of p.
-template <class F>
-auto with_core(const AttnDesc& p, F f) {
+// f(a core's type) for the head width, group and page size of p.
+template <int GRAIN, class F>
+auto with_grain(const AttnDesc& p, F f) {
   const int hd = p.cache.head_dim;
   if (p.group <= 8) {
-    if (hd <= 32) return f((MmaCore<32, 1>*)nullptr);
-    if (hd <= 64) return f((MmaCore<64, 1>*)nullptr);
-    if (hd <= 128) return f((MmaCore<128, 1>*)nullptr);
-    return f((MmaCore<256, 1>*)nullptr);
+    if (hd <= 32) return f((MmaCore<32, 1, GRAIN>*)nullptr);
+    if (hd <= 64) return f((MmaCore<64, 1, GRAIN>*)nullptr);
+    if (hd <= 128) return f((MmaCore<128, 1, GRAIN>*)nullptr);
+    return f((MmaCore<256, 1, GRAIN>*)nullptr);
   }
-  if (hd <= 32) return f((MmaCore<32, 2>*)nullptr);
-  if (hd <= 64) return f((MmaCore<64, 2>*)nullptr);
-  if (hd <= 128) return f((MmaCore<128, 2>*)nullptr);
-  return f((MmaCore<256, 2>*)nullptr);
+  if (hd <= 32) return f((MmaCore<32, 2, GRAIN>*)nullptr);
+  if (hd <= 64) return f((MmaCore<64, 2, GRAIN>*)nullptr);
+  if (hd <= 128) return f((MmaCore<128, 2, GRAIN>*)nullptr);
+  return f((MmaCore<256, 2, GRAIN>*)nullptr);
+}
+template <class F>
+auto with_core(const AttnDesc& p, F f) {
+  return p.cache.page_size % 16 == 0 ? with_grain<16>(p, f) : with_grain<8>(p, f);
 }
 
 CoreShape mma_attention_shape(const AttnDesc& p) {

@@ -353,7 +353,7 @@ def test_attention(case):
     dtype, lens, H, Hk, hd, ps, order = case
     a = make_attention(lens, H, Hk, hd, ps, dtype, order)
     out, lse = run_attention(a)
-    mma = dtype == BF and hd % 8 == 0 and ps % 16 == 0 and order != "gap"
+    mma = dtype == BF and hd % 8 == 0 and ps % 8 == 0 and order != "gap"
     core = lk.PATH_MMA_ATTENTION if mma else lk.PATH_GENERIC_ATTENTION
     assert lk.lora_last_call_path()[0] & ~lk.PATH_JOIN == core
     check_attention(a, out, lse, 1.0 / hd ** 0.5, rows=range(0, len(lens), max(1, len(lens) // 40)))
@@ -373,6 +373,10 @@ def test_attention(case):
     (BF, [1 + 11 * i % 128 for i in range(200)], 16, 4, 128, 16, "token"),
     (BF, [900 + 53 * i % 400 for i in range(24)], 32, 8, 128, 16, "token"),
     (BF, [900 + 53 * i % 400 for i in range(24)], 64, 8, 128, 16, "head"),
+    (BF, [8 + 37 * i % 129 for i in range(145)] + [0], 64, 8, 128, 8, "token"),
+    (BF, [900 + 53 * i % 400 for i in range(24)], 16, 8, 64, 24, "token"),
+    (BF, [300 + 53 * i % 200 for i in range(24)], 64, 4, 256, 8, "token"),
+    (BF, [300 + 53 * i % 200 for i in range(30)], 18, 2, 128, 40, "head"),
     (BF, [900 + 53 * i % 400 for i in range(24)], 16, 8, 64, 32, "token"),
     (BF, [300 + 53 * i % 200 for i in range(24)], 64, 4, 256, 16, "token"),
     (BF, [300 + 53 * i % 200 for i in range(50)], 8, 8, 32, 16, "token"),
