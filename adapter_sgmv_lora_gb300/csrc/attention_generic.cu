@@ -165,7 +165,9 @@ struct GenericCore {
     const S* k = reinterpret_cast<const S*>(stage);
     const S* v = k + TT * HD;
     const int lane = threadIdx.x & 31, r = lane % TT, g = lane / TT;
-    float s[CH] = {};
+    float2 pair[CH];  // products go two to an instruction
+#pragma unroll
+    for (int h = 0; h < CH; ++h) pair[h] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int i = 0; i < CHUNKS / GROUPS; ++i) {
       const int c = i * GROUPS + g;
@@ -177,27 +179,33 @@ struct GenericCore {
           float qv[E];
           read_row<E>(q + h * HD + c * E, qv);
 #pragma unroll
-          for (int e = 0; e < E; ++e) s[h] = fmaf(kv[e], qv[e], s[h]);
+          for (int e = 0; e < E; e += 2)
+            pair[h] = fma_f32x2(make_float2(kv[e], kv[e + 1]), make_float2(qv[e], qv[e + 1]), pair[h]);
         }
       }
     }
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
       if (h >= heads) continue;
+      float s = pair[h].x + pair[h].y;
 #pragma unroll
-      for (int d = TT; d < 32; d <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], d);
-      s[h] = r < n ? s[h] * scale : kNegInf;
-      float top = s[h];
+      for (int d = TT; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      s = r < n ? s * scale : kNegInf;
+      float top = s;
 #pragma unroll
       for (int d = TT / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       const float now = fmaxf(m[h], top);
       const float base = now == kNegInf ? 0.f : now;  // nothing but -inf so far: every weight is 0
-      const float pr = pow2(s[h] - base);
+      const float pr = pow2(s - base);
       const float keep = pow2(m[h] - base);
       m[h] = now;
       l[h] = fmaf(l[h], keep, pr);  // this lane's token; the tokens are summed in put
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) o[h][e] *= keep;
+      for (int e = 0; e < VPL; e += 2) {
+        const float2 w = mul_f32x2(make_float2(o[h][e], o[h][e + 1]), make_float2(keep, keep));
+        o[h][e] = w.x;
+        o[h][e + 1] = w.y;
+      }
       if (g == 0) prob[r * CH + h] = pr;
     }
     __syncwarp();
@@ -219,7 +227,12 @@ struct GenericCore {
         if (h >= heads) continue;
         const float pr = prob[j * CH + h];
 #pragma unroll
-        for (int e = 0; e < VPL; ++e) o[h][e] = fmaf(pr, vv[e], o[h][e]);
+        for (int e = 0; e < VPL; e += 2) {
+          const float2 w = fma_f32x2(make_float2(pr, pr), make_float2(vv[e], vv[e + 1]),
+                                     make_float2(o[h][e], o[h][e + 1]));
+          o[h][e] = w.x;
+          o[h][e + 1] = w.y;
+        }
       }
     }
     __syncwarp();
