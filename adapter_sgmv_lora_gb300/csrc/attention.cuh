@@ -14,10 +14,12 @@
 // (256 ragged contexts: 25 streams against 4, 194 us against 151).  Every CTA
 // works the cut out from the lengths alone.
 //
-// Where every stream is short (kSoloTiles at most) and there are more streams
-// than CTAs, the pieces go to warps instead and a stream to the one whose piece
-// holds its first tile: no stream is shared, no warp waits for another (4720
-// streams of one or two tiles: 47 us before, 33 after, cold).
+// Where every stream is short (kSoloTokens at most) and there is one for more
+// than every other warp of the GPU, the pieces go to warps instead and a
+// stream to the one whose piece holds its first tile: no stream is shared, no
+// warp waits for another (4720 streams of one or two tiles: 47 us before, 27
+// after; 1216 of 14 tiles 31.9 and 27.8; 352 of 3 to 6 tiles 16.0 and 18.6, so
+// those stay with blocks).
 //
 // Within a CTA the warps take the tiles of a piece in turn, each through its
 // own ring of asynchronous copies; a ring runs ahead across the ends of
@@ -155,7 +157,7 @@ struct Piece {
   int seq;
 };
 
-constexpr int kSoloTiles = 8;
+constexpr int kSoloTokens = 256;
 
 // Sum over the warp of values below 2^32 / of any size.
 __device__ __forceinline__ long long warp_sum(unsigned v) {
@@ -261,7 +263,7 @@ struct Plan {
     if (report && bad) atomicOr(p.status, LORA_DEV_BAD_LENGTH);
     longest = __reduce_max_sync(0xffffffffu, longest);
     const long long one = tiles + Core::STREAM_COST * live;
-    solo = longest <= kSoloTiles + Core::STREAM_COST && live * streams > p.pieces;
+    solo = longest <= kSoloTokens / Core::TT + Core::STREAM_COST && 2 * live * streams > (long long)p.pieces * Core::W;
     // Pieces with a tile for every warp; on their own, a stream for every warp.
     const long long want = solo ? live * streams : (tiles * streams + Core::W - 1) / Core::W;
     const long long most = solo ? (long long)p.pieces * Core::W : p.pieces;

@@ -382,6 +382,9 @@ def test_attention(case):
     (BF, [300 + 53 * i % 200 for i in range(50)], 8, 8, 32, 16, "token"),
     (BF, [1 + 11 * i % 256 for i in range(200)], 8, 4, 64, 5, "head"),
     (F32, [1 + 11 * i % 64 for i in range(200)], 16, 4, 128, 3, "token"),
+    (BF, [1 + 37 * i % 256 for i in range(300)], 32, 4, 128, 16, "token"),  # up to 16 tiles
+    (BF, [1 + 37 * i % 256 for i in range(200)], 18, 2, 256, 8, "head"),
+    (F32, [1 + 37 * i % 256 for i in range(300)], 4, 4, 128, 16, "token"),
 ])
 def test_attention_many_streams_a_block(dtype, lens, H, Hk, hd, ps, order):
     """Several streams to every block, each of several tiles, with pages that end inside a tile: the lanes of a
