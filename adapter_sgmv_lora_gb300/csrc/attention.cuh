@@ -14,12 +14,13 @@
 // (256 ragged contexts: 25 streams against 4, 194 us against 151).  Every CTA
 // works the cut out from the lengths alone.
 //
-// Where every stream is short (kSoloTokens at most) and there is one for more
-// than every other warp of the GPU, the pieces go to warps instead and a
-// stream to the one whose piece holds its first tile: no stream is shared, no
-// warp waits for another (4720 streams of one or two tiles: 47 us before, 27
-// after; 1216 of 14 tiles 31.9 and 27.8; 352 of 3 to 6 tiles 16.0 and 18.6, so
-// those stay with blocks).
+// Where streams are many and short the pieces go to warps instead and a stream
+// to the one whose piece holds its first tile: no stream is shared, no warp
+// waits for another.  So with up to kSoloTokens tokens a stream and a stream
+// for more than every other warp of the GPU (4720 streams of one or two tiles:
+// 47 us before, 27 after; 1216 of 14 tiles 31.9 and 27.8; 352 of 3 to 6 tiles
+// 16.0 and 18.6, so those stay with blocks), or with one or two tiles and more
+// streams than SMs (592 streams of one tile 14.2 and 10.7).
 //
 // Within a CTA the warps take the tiles of a piece in turn, each through its
 // own ring of asynchronous copies; a ring runs ahead across the ends of
@@ -263,9 +264,16 @@ struct Plan {
     if (report && bad) atomicOr(p.status, LORA_DEV_BAD_LENGTH);
     longest = __reduce_max_sync(0xffffffffu, longest);
     const long long one = tiles + Core::STREAM_COST * live;
-    solo = longest <= kSoloTokens / Core::TT + Core::STREAM_COST && 2 * live * streams > (long long)p.pieces * Core::W;
-    // Pieces with a tile for every warp; on their own, a stream for every warp.
-    const long long want = solo ? live * streams : (tiles * streams + Core::W - 1) / Core::W;
+    const long long all = live * streams;
+    const int reach = longest - Core::STREAM_COST;  // tiles of the longest stream
+    solo = (reach <= kSoloTokens / Core::TT && 2 * all > (long long)Core::CTAS * p.sms * Core::W) ||
+           (reach <= 2 && all > p.sms);
+    // Else pieces with a tile for every warp, or a stream each while that is
+    // no more than a piece to an SM (72 streams of one tile 10.7 us, a warp
+    // each 17.1).
+    const long long full = (tiles * streams + Core::W - 1) / Core::W;
+    const long long apart = all < p.sms ? all : p.sms;
+    const long long want = solo ? all : (full > apart ? full : apart);
     const long long most = solo ? (long long)p.pieces * Core::W : p.pieces;
     line.cut(one * streams, (int)(want < 1 ? 1 : (want < most ? want : most)), !solo && p.spares);
     small = once && one < INT_MAX;
@@ -810,7 +818,8 @@ inline long long most_places(const CoreShape& c, const AttnDesc& p) {
 }
 
 // Pieces the line is cut into at most: what fits on the GPU at once, or less
-// when the longest sequences would not give every warp a tile.  *spares:
+// when the longest sequences would give every warp a tile with fewer (but one
+// for each stream).  *spares:
 // whether pieces can be long enough to give spare units, and streams are not
 // shared by more than eight pieces (where they are, joining the extra parts
 // costs more than evenness brings: one context of 131071 tokens 97.3 us with
@@ -819,7 +828,7 @@ inline int pieces_of(const CoreShape& c, const AttnDesc& p, int sms, bool* spare
   const long long most = (long long)c.CTAS * std::max(sms, 1), streams = streams_of(c, p);
   *spares = most_places(c, p) / most >= kSparePlaces && streams * 8 >= most;
   if (streams >= most * c.W) return (int)most;
-  return (int)std::max(1LL, std::min(most, (most_tiles(c, p) * streams + c.W - 1) / c.W));
+  return (int)std::max(1LL, std::min(most, std::max(std::min(streams, most), (most_tiles(c, p) * streams + c.W - 1) / c.W)));
 }
 inline int grid_of(int pieces, bool spares) { return spares ? pieces * (kSpare + 1) : pieces; }
 
@@ -880,6 +889,7 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
   p.page_magic = (unsigned)(((1ULL << p.page_shift) + p.cache.page_size - 1) / p.cache.page_size);
   p.whole_grains = p.cache.page_size % Core::GRAIN == 0;
   p.pieces = pieces_of(c, p, std::min(device_sm_count(), kMaxSmsForWorkspace), &p.spares);
+  p.sms = std::max(device_sm_count(), 1);
   const int units = grid_of(p.pieces, p.spares);
   const WorkspaceParts w = workspace_parts(c, units);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -236,6 +236,7 @@ struct AttnDesc {
   // grain of tokens crosses a page's end; and the workspace's three parts.
   int chunks;
   int pieces;
+  int sms;
   bool spares;
   unsigned page_magic;
   int page_shift;
