@@ -828,6 +828,8 @@ inline int pieces_of(const CoreShape& c, const AttnDesc& p, int sms, bool* spare
   const long long most = (long long)c.CTAS * std::max(sms, 1), streams = streams_of(c, p);
   *spares = most_places(c, p) / most >= kSparePlaces && streams * 8 >= most;
   if (streams >= most * c.W) return (int)most;
+  // Sure to be a warp each (Plan::make): no blocks beyond those.
+  if (most_tiles(c, p) <= 2 && streams > sms) return (int)std::min(most, (streams + c.W - 1) / c.W);
   return (int)std::max(1LL, std::min(most, std::max(std::min(streams, most), (most_tiles(c, p) * streams + c.W - 1) / c.W)));
 }
 inline int grid_of(int pieces, bool spares) { return spares ? pieces * (kSpare + 1) : pieces; }

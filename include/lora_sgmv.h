@@ -513,7 +513,8 @@ size_t lora_attention_workspace_bytes(const lora_attention_t* attention, const l
  * over j < lengths[b].  A sequence of length 0 (a padding entry of a batch)
  * gives out = 0 and lse = -inf, as does a row whose every score is -inf.
  * Scores, softmax sums and the output's accumulation are fp32; on the bf16
- * tensor-core path the probabilities enter the product with V as two bf16
+ * tensor-core path (pages of a multiple of 8 tokens, rows of cache and q on
+ * 16-byte boundaries) the probabilities enter the product with V as two bf16
  * terms (16 significant bits).  Cached values past a sequence's end and
  * block-table entries past its last page are never used.  A length below 0
  * or above max_pages * page_size raises LORA_DEV_BAD_LENGTH, a used page id
