@@ -108,50 +108,25 @@ __device__ __forceinline__ long long divide(long long a, int b) {  // a >= 0, b 
 
 // The line.  A stream takes C places that stand for what a CTA spends on any
 // stream it touches (joining its warps, starting the next), then one place a
-// tile.  The line is cut into `pieces` even parts.  Where those are long each
-// gives its last eighth up in kSpare spare units, which go to the CTAs that
-// are done first (attention_kernel): unit (kSpare + 1) u is the head of piece
-// u, the kSpare units after it its spares.  Else a piece is one unit.
-constexpr int kSpare = 2;
-constexpr int kSparePlaces = 192;  // places of a piece that gives spares
-
+// tile.  The line is cut into `pieces` even parts.
 struct Line {
-  long long total, base, head, spare;  // piece u: base places, the first `rest` pieces one more
+  long long total, base;  // piece u: base places, the first `rest` pieces one more
   int pieces, rest;
-  bool spares;
-  __device__ __forceinline__ void cut(long long total_, int pieces_, bool may_spare) {
+  __device__ __forceinline__ void cut(long long total_, int pieces_) {
     total = total_;
     pieces = pieces_;
     base = divide(total, pieces);
     rest = (int)(total - base * pieces);
-    spares = may_spare && base >= kSparePlaces;
-    spare = base >> 4;
-    head = base - kSpare * spare;
   }
-  __device__ __forceinline__ int units() const { return spares ? pieces * (kSpare + 1) : pieces; }
-  __device__ __forceinline__ long long piece_start(int u) const { return u * base + min(u, rest); }
-  __device__ __forceinline__ long long start(int v) const {
-    if (!spares) return piece_start(v);
-    const int u = v / (kSpare + 1), i = v - u * (kSpare + 1);
-    return piece_start(u) + (i == 0 ? 0 : head + (i - 1) * spare);
-  }
-  // First unit that starts at or after a place > 0.
+  __device__ __forceinline__ long long start(int u) const { return u * base + min(u, rest); }
+  // First piece that starts at or after a place.
   __device__ __forceinline__ int first_from(long long place) const {
     const long long wide = rest * (base + 1);
-    const int u = place <= wide ? (int)((place + base) / (base + 1)) : rest + (int)((place - wide + base - 1) / base);
-    if (!spares) return u;
-    const long long in = place - piece_start(u - 1);  // > 0: within piece u - 1 or at its end
-    const int i = in <= head ? 1 : 1 + (int)((in - head + spare - 1) / spare);
-    return i > kSpare ? u * (kSpare + 1) : (u - 1) * (kSpare + 1) + i;
-  }
-  // The unit that block b starts with; blocks past the pieces have the spares.
-  __device__ __forceinline__ int unit_of(int b) const {
-    if (!spares) return b;
-    return b < pieces ? b * (kSpare + 1) : (b - pieces) / kSpare * (kSpare + 1) + 1 + (b - pieces) % kSpare;
+    return place <= wide ? (int)((place + base) / (base + 1)) : rest + (int)((place - wide + base - 1) / base);
   }
 };
 
-// One unit's part of the line, [lo, hi), and the sequence that place lo
+// One piece of the line, [lo, hi), and the sequence that place lo
 // belongs to (whose first place is number origin).
 struct Piece {
   long long lo, hi, origin;
@@ -234,7 +209,7 @@ template <class Core>
 struct Plan {
   static constexpr int CHUNK = 32 * Count<Core>::PER;
   Line line;
-  bool solo;   // units are for warps, streams are whole
+  bool solo;   // pieces are for warps, streams are whole
   bool small;  // one count covers the sequences, and places fit 32 bits
 
   // c: the count of the first sequences.
@@ -275,19 +250,19 @@ struct Plan {
     const long long apart = all < p.sms ? all : p.sms;
     const long long want = solo ? all : (full > apart ? full : apart);
     const long long most = solo ? (long long)p.pieces * Core::W : p.pieces;
-    line.cut(one * streams, (int)(want < 1 ? 1 : (want < most ? want : most)), !solo && p.spares);
+    line.cut(one * streams, (int)(want < 1 ? 1 : (want < most ? want : most)));
     small = once && one < INT_MAX;
   }
 
-  // Unit v's part.  c: the count of the first sequences.
-  __device__ __forceinline__ Piece locate(const AttnDesc& p, Count<Core> c, int v) const {
+  // Piece u.  c: the count of the first sequences.
+  __device__ __forceinline__ Piece locate(const AttnDesc& p, Count<Core> c, int u) const {
     const int streams = p.cache.num_kv_heads * p.chunks, lane = threadIdx.x & 31;
     Piece r;
     r.lo = r.hi = r.origin = 0;
     r.seq = 0;
-    if (v >= line.units() || line.total == 0) return r;
-    r.lo = line.start(v);
-    r.hi = line.start(v + 1);
+    if (u >= line.pieces || line.total == 0) return r;
+    r.lo = line.start(u);
+    r.hi = line.start(u + 1);
     // The sequence whose one-stream places contain lo / streams.
     const long long place = divide(r.lo, streams);
     if (small) {
@@ -358,15 +333,15 @@ struct Segments {
   }
 };
 
-// A unit that starts inside a stream whose beginning lies in the unit before
-// it stands for that stream in the join: {sequence, stream, units that share
+// A piece that starts inside a stream whose beginning lies in the piece before
+// it stands for that stream in the join: {sequence, stream, pieces that share
 // it}; others {0, 0, 0}.
 template <class Core>
-__device__ __forceinline__ int4 split_of(const Line& line, const Piece& piece, const Segments<Core>& first, int v) {
+__device__ __forceinline__ int4 split_of(const Line& line, const Piece& piece, const Segments<Core>& first, int u) {
   if (!first.valid || first.t0 == 0) return make_int4(0, 0, 0, 0);  // so where streams are whole
   const long long begin = piece.lo - first.t0, end = begin + first.n;  // places of the stream's tiles
-  if (line.start(v - 1) > begin) return make_int4(0, 0, 0, 0);
-  return make_int4(first.seq, first.stream, line.first_from(end) - v + 1, 0);
+  if (line.start(u - 1) > begin) return make_int4(0, 0, 0, 0);
+  return make_int4(first.seq, first.stream, line.first_from(end) - u + 1, 0);
 }
 
 // One warp's walk over the tiles it loads: rank, rank + step, ... of each
@@ -377,8 +352,6 @@ template <class Core>
 struct TileCursor {
   static constexpr int GRAINS = Core::TT / Core::GRAIN;
   Segments<Core> seg;
-  Segments<Core> entry;  // the first segment of the unit after seg's, once it is known
-  bool has_entry;
   int tile;
   int page, slot;  // slot: token within the page; below 0: no token
 
@@ -399,20 +372,18 @@ struct TileCursor {
   __device__ __forceinline__ void settle(const AttnDesc& p, int rank) {
     while (seg.valid && tile >= seg.t1) {
       seg.next(p);
-      if (!seg.valid && has_entry) {
-        seg = entry;
-        has_entry = false;
-      }
-      tile = seg.t0 + rank;
+      tile = rank;
     }
     if (seg.valid) look_up(p);
   }
-  __device__ __forceinline__ void enter(const AttnDesc& p, const Segments<Core>& sg, int rank) {
+  __device__ __forceinline__ void first(const AttnDesc& p, const Segments<Core>& sg, int rank) {
     seg = sg;
+    if (!seg.valid) return;
     tile = seg.t0 + rank;
     settle(p, rank);
   }
   __device__ __forceinline__ void next(const AttnDesc& p, int rank, int step) {
+    if (!seg.valid) return;
     tile += step;
     settle(p, rank);
   }
@@ -428,37 +399,6 @@ struct TileCursor {
   // Tokens of the tile.
   __device__ __forceinline__ int tokens() const { return min(Core::TT, seg.len - tile * Core::TT); }
 };
-
-// Waits for the oldest of `pending` groups of asynchronous copies.
-template <int N>
-__device__ __forceinline__ void wait_oldest(int pending) {
-  if constexpr (N == 1) {
-    cp_async_wait<0>();
-  } else {
-    if (pending >= N) cp_async_wait<N - 1>();
-    else wait_oldest<N - 1>(pending);
-  }
-}
-
-// A CTA that is done takes over a block of the grid that has not started
-// (cluster launch control): the hardware hands each block out once, so spare
-// units go to whoever is free and nothing in memory has to start at zero.  A
-// unit's partial result has its place whoever computes it, so results do not
-// depend on who does.
-__device__ __forceinline__ void ask_for_block(uint4* answer, uint64_t* bar) {
-  fence_proxy_async_smem();  // the earlier answer's reads come before this write
-  mbar_arrive_expect_tx(bar, 16);
-  launch_control_try_cancel(answer, bar);
-}
-
-// The block taken over, or -1: none is left (or the wait ran out).
-__device__ __forceinline__ int answered_block(const uint4* answer, uint64_t* bar, uint32_t parity, unsigned* status) {
-  if (!mbar_wait(bar, parity) && !mbar_wait(bar, parity)) {
-    atomicOr(status, LORA_DEV_TIMEOUT);
-    return -1;
-  }
-  return launch_control_block(answer);
-}
 
 // The frame.  Core gives:
 //   T, TT (tokens a tile), W (warps), CTAS (resident per SM), HD (padded head
@@ -484,8 +424,6 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   constexpr int COMB = Core::COMB;
   constexpr int PITCH = HD + 4;  // floats per head of the join buffer: its columns fall on different banks
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) uint4 s_answer[2];
-  __shared__ uint64_t s_asked[2];
   uint8_t* ring = smem;
   float* comb = reinterpret_cast<float*>(smem + W * STAGES * Core::STAGE_BYTES);
   float2* stat = reinterpret_cast<float2*>(comb + W * COMB * PITCH);
@@ -498,14 +436,13 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   Plan<Core> plan;
   plan.make(p, count, blockIdx.x == 0);
   const bool solo = plan.solo;
-  int unit = plan.line.unit_of(solo ? blockIdx.x * W + warp : blockIdx.x);
+  const int u = solo ? blockIdx.x * W + warp : blockIdx.x;
   Segments<Core> seg;
   {
-    const Piece piece = plan.locate(p, count, unit);
+    const Piece piece = plan.locate(p, count, u);
     seg.first(p, piece, solo);
-    if (p.spares && threadIdx.x == 0)
-      p.splits[solo ? blockIdx.x : unit] =
-          solo ? make_int4(0, 0, 0, 0) : split_of<Core>(plan.line, piece, seg, unit);
+    if (p.large && threadIdx.x == 0)
+      p.splits[blockIdx.x] = solo ? make_int4(0, 0, 0, 0) : split_of<Core>(plan.line, piece, seg, u);
   }
   if (!seg.valid) return;  // the whole CTA, or a warp on its own
   // The team that works on a segment: the CTA's warps, or one.
@@ -533,38 +470,37 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   Core core(p, extra);
   int head0, heads = heads_of(seg, &head0);
   if (!solo) core.fetch(p, seg.seq, head0, heads);
-  if (plan.line.spares && threadIdx.x == 0) {
-    mbar_init(&s_asked[0], 1);
-    mbar_init(&s_asked[1], 1);
-    fence_mbar_init();
-    ask_for_block(&s_answer[0], &s_asked[0]);
-  }
-
-  // The ring: `pending` tiles are loaded or on their way, the oldest in stage
-  // `stage`, the next to load goes to stage `fill`.
   TileCursor<Core> cur;
-  cur.has_entry = false;
-  cur.enter(p, seg, rank);
   unsigned bad_stages = 0;
-  int stage = 0, fill = 0, pending = 0;
-  auto load = [&] {
-    bool bad;
-    const long long off = cur.offset(p, &bad);
-    bad_stages = (bad_stages & ~(1u << fill)) | ((unsigned)bad << fill);
-    core.load(p, my_ring + fill * Core::STAGE_BYTES, off, cur.tokens());
-    cp_async_commit();
-    ++pending;
-    fill = fill + 1 == STAGES ? 0 : fill + 1;
-    cur.next(p, rank, team);
+  auto load = [&](int stage, const TileCursor<Core>& c) {
+    if (c.seg.valid) {
+      bool bad;
+      const long long off = c.offset(p, &bad);
+      bad_stages = (bad_stages & ~(1u << stage)) | ((unsigned)bad << stage);
+      core.load(p, my_ring + stage * Core::STAGE_BYTES, off, c.tokens());
+    }
+    cp_async_commit();  // of a tile or of nothing: one a step, so the count of groups tells which tile has landed
   };
-#pragma unroll 1
-  while (pending < STAGES && cur.seg.valid) load();
+  {
+    // The first tiles' block-table reads all go out before any is waited for.
+    TileCursor<Core> ahead[STAGES];
+    ahead[0].first(p, seg, rank);
+#pragma unroll
+    for (int s = 1; s < STAGES; ++s) {
+      ahead[s] = ahead[s - 1];
+      ahead[s].next(p, rank, team);
+    }
+    cur = ahead[STAGES - 1];
+    cur.next(p, rank, team);
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) load(s, ahead[s]);
+  }
 
   if (!solo) {
     core.pass_on();
     __syncthreads();
   }
-  int asked = 0;  // requests for spare units answered so far
+  int stage = 0;
 #pragma unroll 1
   while (true) {
     __syncwarp();  // ldmatrix and mma need the warp's lanes together; a block barrier does not promise that
@@ -572,28 +508,6 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
     else core.begin(p, heads);
     Segments<Core> after = seg;
     after.next(p);
-    int after_unit = unit;
-    if (!after.valid && plan.line.spares && asked >= 0) {
-      // This unit ends here: on to a spare one, if one is left.
-      const int block = answered_block(&s_answer[asked & 1], &s_asked[asked & 1], (asked >> 1) & 1, p.status);
-      if (block < 0) {
-        asked = -1;
-      } else {
-        after_unit = plan.line.unit_of(block);
-        count.read(p, 0);
-        const Piece piece = plan.locate(p, count, after_unit);
-        after.first(p, piece, false);
-        if (threadIdx.x == 0) p.splits[after_unit] = split_of<Core>(plan.line, piece, after, after_unit);
-        if (cur.seg.valid) {
-          cur.entry = after;
-          cur.has_entry = true;
-        } else {
-          cur.enter(p, after, rank);
-#pragma unroll 1
-          while (pending < STAGES && cur.seg.valid) load();
-        }
-      }
-    }
     int after_head0 = 0, after_heads = 0;
     if (after.valid) {
       after_heads = heads_of(after, &after_head0);
@@ -602,18 +516,18 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
     bool bad = false;
 #pragma unroll 1
     for (int t = seg.t0 + rank; t < seg.t1; t += team) {
-      wait_oldest<STAGES>(pending);
+      cp_async_wait<STAGES - 1>();
       __syncwarp();
       bad |= (bad_stages >> stage) & 1;
       core.tile(p, my_ring + stage * Core::STAGE_BYTES, min(TT, seg.len - t * TT));
       __syncwarp();
-      --pending;
+      load(stage, cur);
+      cur.next(p, rank, team);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
-      if (cur.seg.valid) load();
     }
     // Join the warps.  A sum of -1 marks a page outside the cache.
     const bool whole = seg.t0 == 0 && seg.t1 == seg.n;
-    const long long slot = 2 * (long long)unit + (seg.t0 == 0 ? 1 : 0);  // of the workspace
+    const long long slot = 2 * (long long)u + (seg.t0 == 0 ? 1 : 0);  // of the workspace
 #pragma unroll 1
     for (int part = 0; part < CH / COMB; ++part) {
       const int part_heads = min(COMB, heads - part * COMB);
@@ -666,31 +580,28 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
     if (!after.valid) break;
     if (!solo) core.pass_on();
     team_sync();  // the join's buffer is free, the queries are there
-    if (after_unit != unit) {
-      unit = after_unit;
-      ++asked;  // every warp has the last answer, the buffer before it is free
-      if (threadIdx.x == 0) ask_for_block(&s_answer[asked & 1], &s_asked[asked & 1]);
-    }
     seg = after;
     head0 = after_head0;
     heads = after_heads;
   }
+  cp_async_wait<0>();
 }
 
-// Joins the partial results of the streams that several units share: block u
-// those of the stream that unit u starts inside of and unit u - 1 begins.
-// Partial 0 is the end of unit u - 1, partial i the beginning of unit
+// Joins the partial results of the streams that several pieces share: block u
+// those of the stream that piece u starts inside of and piece u - 1 begins.
+// Partial 0 is the end of piece u - 1, partial i the beginning of piece
 // u - 1 + i; they are summed in a fixed order.
 //
-// Small calls share few streams among many units: a block is one query head,
+// Small calls share few streams among many pieces: a block is one query head,
 // its warps share the partial results out.  Which stream it is follows from
-// the lengths alone and is found while the units still run; after them the
+// the lengths alone and is found while the pieces still run; after them the
 // statistics and the outputs are one round trip to memory (one context of
-// 131071 tokens: 25 us of joining before, 5 now).  Calls that can be large
-// have hundreds of streams shared by two or three units and no room on the
-// SMs before the units are done: there the units leave the answer in memory
-// and a warp is one head.
+// 131071 tokens: 25 us of joining before, 5 now).  Large calls have hundreds
+// of streams shared by two or three pieces and no room on the SMs before the
+// pieces are done: there the pieces leave the answer in memory and a warp is
+// one head (256 ragged contexts 186.9 and 183.6 us).
 constexpr int kJoinWarps = 4, kJoinBatch = 8;
+constexpr int kLargePlaces = 192;  // places a piece of a large call
 
 template <class Core>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ AttnDesc p) {
@@ -701,10 +612,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
   __shared__ float s_l[kJoinWarps];
   const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The team that joins a head: a warp, or the block's.
-  const int team = p.spares ? 1 : kJoinWarps, rank = p.spares ? 0 : warp, leader = p.spares ? warp : 0;
-  const int h = p.spares ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
+  const int team = p.large ? 1 : kJoinWarps, rank = p.large ? 0 : warp, leader = p.large ? warp : 0;
+  const int h = p.large ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
   int4 split;
-  if (p.spares) {
+  if (p.large) {
     pdl_wait();
     split = p.splits[u];
   } else {
@@ -720,7 +631,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
       if (lane == 0) s_split = split;
     }
     __syncthreads();
-    pdl_wait();  // every block: the grid must not be over before the units are
+    pdl_wait();  // every block: the grid must not be over before the pieces are
     split = s_split;
   }
   const int kv_head = kv_head_of(p, split.y);
@@ -777,7 +688,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
 #pragma unroll
   for (int e = 0; e < VPL; ++e) s_o[warp][e * 32 + lane] = o[e];
   if (lane == 0) s_l[warp] = l;
-  if (p.spares) __syncwarp();
+  if (p.large) __syncwarp();
   else __syncthreads();
   l = 0.f;
 #pragma unroll
@@ -819,20 +730,19 @@ inline long long most_places(const CoreShape& c, const AttnDesc& p) {
 
 // Pieces the line is cut into at most: what fits on the GPU at once, or less
 // when the longest sequences would give every warp a tile with fewer (but one
-// for each stream).  *spares:
-// whether pieces can be long enough to give spare units, and streams are not
-// shared by more than eight pieces (where they are, joining the extra parts
-// costs more than evenness brings: one context of 131071 tokens 97.3 us with
-// spares, 93.9 without; 256 ragged contexts 191.7 and 197.9).
-inline int pieces_of(const CoreShape& c, const AttnDesc& p, int sms, bool* spares) {
+// for each stream).
+inline int pieces_of(const CoreShape& c, const AttnDesc& p, int sms) {
   const long long most = (long long)c.CTAS * std::max(sms, 1), streams = streams_of(c, p);
-  *spares = most_places(c, p) / most >= kSparePlaces && streams * 8 >= most;
   if (streams >= most * c.W) return (int)most;
   // Sure to be a warp each (Plan::make): no blocks beyond those.
   if (most_tiles(c, p) <= 2 && streams > sms) return (int)std::min(most, (streams + c.W - 1) / c.W);
   return (int)std::max(1LL, std::min(most, std::max(std::min(streams, most), (most_tiles(c, p) * streams + c.W - 1) / c.W)));
 }
-inline int grid_of(int pieces, bool spares) { return spares ? pieces * (kSpare + 1) : pieces; }
+// Long pieces, and streams that are not shared by more than eight of them.
+inline bool large_of(const CoreShape& c, const AttnDesc& p, int sms) {
+  const long long most = (long long)c.CTAS * std::max(sms, 1);
+  return most_places(c, p) / most >= kLargePlaces && streams_of(c, p) * 8 >= most;
+}
 
 inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -840,21 +750,16 @@ struct WorkspaceParts {
   size_t stats, partial, bytes;  // offsets (the splits come first), and the whole
 };
 
-inline WorkspaceParts workspace_parts(const CoreShape& c, int units) {
+inline WorkspaceParts workspace_parts(const CoreShape& c, int pieces) {
   WorkspaceParts w;
-  w.stats = round256((size_t)units * sizeof(int4));
-  w.partial = w.stats + round256((size_t)2 * units * c.CH * sizeof(float2));
-  w.bytes = w.partial + round256((size_t)2 * units * c.CH * c.HD * sizeof(float));
+  w.stats = round256((size_t)pieces * sizeof(int4));
+  w.partial = w.stats + round256((size_t)2 * pieces * c.CH * sizeof(float2));
+  w.bytes = w.partial + round256((size_t)2 * pieces * c.CH * c.HD * sizeof(float));
   return w;
 }
 
-// Enough on any GPU: one with fewer SMs cuts fewer pieces, but they may be
-// long enough to give spares where those of a larger one are not.
 inline size_t workspace_bytes_of(const CoreShape& c, const AttnDesc& p) {
-  bool spares = false;
-  const int pieces = pieces_of(c, p, kMaxSmsForWorkspace, &spares);
-  const long long long_pieces = std::min<long long>(pieces, most_places(c, p) / kSparePlaces);
-  return workspace_parts(c, std::max(pieces, grid_of((int)long_pieces, true))).bytes;
+  return workspace_parts(c, pieces_of(c, p, kMaxSmsForWorkspace)).bytes;
 }
 
 template <class Core>
@@ -890,21 +795,22 @@ cudaError_t launch_core(AttnDesc p, void* workspace, cudaStream_t s, unsigned pa
   p.page_shift = 31 + log;
   p.page_magic = (unsigned)(((1ULL << p.page_shift) + p.cache.page_size - 1) / p.cache.page_size);
   p.whole_grains = p.cache.page_size % Core::GRAIN == 0;
-  p.pieces = pieces_of(c, p, std::min(device_sm_count(), kMaxSmsForWorkspace), &p.spares);
+  const int sms = std::min(device_sm_count(), kMaxSmsForWorkspace);
+  p.pieces = pieces_of(c, p, sms);
+  p.large = large_of(c, p, sms);
   p.sms = std::max(device_sm_count(), 1);
-  const int units = grid_of(p.pieces, p.spares);
-  const WorkspaceParts w = workspace_parts(c, units);
+  const WorkspaceParts w = workspace_parts(c, p.pieces);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.splits = reinterpret_cast<int4*>(ws);
   p.stats = reinterpret_cast<float2*>(ws + w.stats);
   p.partial = reinterpret_cast<float*>(ws + w.partial);
   cudaError_t e = allow_smem<Core>((int)smem);
   if (e != cudaSuccess) return e;
-  attention_kernel<Core><<<units, Core::W * 32, smem, s>>>(p);
+  attention_kernel<Core><<<p.pieces, Core::W * 32, smem, s>>>(p);
   if ((e = noted(cudaGetLastError(), path)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int heads = std::min(Core::CH, p.group);
-  cfg.gridDim = dim3(units, p.spares ? (heads + kJoinWarps - 1) / kJoinWarps : heads);
+  cfg.gridDim = dim3(p.pieces, p.large ? (heads + kJoinWarps - 1) / kJoinWarps : heads);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

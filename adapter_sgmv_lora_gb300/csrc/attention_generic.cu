@@ -71,7 +71,6 @@ struct GenericCore {
   float* q;  // [CH][HD]: the CTA's queries, or this warp's where it is on its own
   float* prob;  // [TT][CH], this warp's
   float scale;
-  uint64_t policy;
   int heads;
   float m[CH], l[CH], o[CH][VPL];
   float next_q[(CH * HD + W * 32 - 1) / (W * 32)];
@@ -80,8 +79,7 @@ struct GenericCore {
       : shared(reinterpret_cast<float*>(extra)),
         q(shared),
         prob(q + W * CH * HD + (threadIdx.x >> 5) * TT * CH),
-        scale(p.scale * kLog2e),
-        policy(policy_evict_first()) {}
+        scale(p.scale * kLog2e) {}
 
   // Element of chunk c of row r.
   static __device__ __forceinline__ int at(int r, int c) { return r * HD + (c ^ (r & 7)) * E; }
@@ -101,8 +99,8 @@ struct GenericCore {
         const long long row = __shfl_sync(0xffffffffu, off, r);
         if (c * E < p.cache.head_dim) {
           const long long src = row < 0 ? 0 : row + c * E;
-          cp_async16_zfill(k + at(r, c), kg + src, row < 0 ? 0 : 16, policy);
-          cp_async16_zfill(v + at(r, c), vg + src, row < 0 ? 0 : 16, policy);
+          cp_async16_zfill(k + at(r, c), kg + src, row < 0 ? 0 : 16);
+          cp_async16_zfill(v + at(r, c), vg + src, row < 0 ? 0 : 16);
         }
       }
     } else {

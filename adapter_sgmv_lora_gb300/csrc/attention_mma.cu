@@ -44,13 +44,12 @@ struct MmaCore {
   float o[KT][NT][4];     // O^T accumulators: rows 16 k + lane / 4 (+ 8), heads 2 (lane % 4) (+ 1)
   float m[NT][2], l[NT][2];
   float scale;
-  uint64_t policy;
 
   uint8_t* q_shared;
   uint4 next_q[(CH * HD / 8 + W * 32 - 1) / (W * 32)];
 
   __device__ __forceinline__ MmaCore(const AttnDesc& p, uint8_t* extra)
-      : scale(p.scale * kLog2e), policy(policy_evict_first()), q_shared(extra) {}
+      : scale(p.scale * kLog2e), q_shared(extra) {}
 
   // Byte offset of 16-byte chunk c of row r: swizzled, so the 8 rows of an
   // ldmatrix block fall on different banks.
@@ -74,8 +73,8 @@ struct MmaCore {
         for (int i = 0; i < GRAIN / ROWS; ++i) {
           const int r = j * GRAIN + i * ROWS + r0;
           const uint32_t bytes = r < live ? 16 : 0;
-          cp_async16_zfill(stage + at(r, c), kg + src, bytes, policy);
-          cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, bytes, policy);
+          cp_async16_zfill(stage + at(r, c), kg + src, bytes);
+          cp_async16_zfill(stage + TT * HD * 2 + at(r, c), vg + src, bytes);
           src += step;
         }
       }

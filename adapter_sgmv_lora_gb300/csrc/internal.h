@@ -230,20 +230,20 @@ struct AttnDesc {
   float* lse;  // or nullptr
   unsigned* status;
   // Filled in by the launcher: heads of a group are taken CH at a time
-  // (chunks per key/value head); the work is cut into at most `pieces` parts,
-  // which may give spare units; token / page_size is
+  // (chunks per key/value head); the work is cut into at most `pieces` parts;
+  // large: their joins are found by them; token / page_size is
   // token * page_magic >> page_shift for tokens below 2^31; whole_grains: no
   // grain of tokens crosses a page's end; and the workspace's three parts.
   int chunks;
   int pieces;
   int sms;
-  bool spares;
+  bool large;
   unsigned page_magic;
   int page_shift;
   bool whole_grains;
-  int4* splits;    // [units] streams that several units share (calls that may give spares)
-  float2* stats;   // [2 * units, CH] running maximum and sum of a partial result
-  float* partial;  // [2 * units, CH, HD] its unnormalised output
+  int4* splits;    // [pieces] streams that several pieces share (large calls)
+  float2* stats;   // [2 * pieces, CH] running maximum and sum of a partial result
+  float* partial;  // [2 * pieces, CH, HD] its unnormalised output
 };
 size_t attention_workspace_bytes(const AttnDesc& p);
 cudaError_t launch_attention(const AttnDesc& p, void* workspace, cudaStream_t s);

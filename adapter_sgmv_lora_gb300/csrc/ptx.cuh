@@ -90,12 +90,9 @@ __device__ __forceinline__ void cp_async16(void* smem_dst, const void* gmem_src)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem_dst)), "l"(gmem_src)
                : "memory");
 }
-// The same, reading only the first `bytes` (0 or 16) and zero-filling the rest,
-// under an L2 cache policy.
-__device__ __forceinline__ void cp_async16_zfill(void* smem_dst, const void* gmem_src, uint32_t bytes,
-                                                 uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(smem_addr(smem_dst)),
-               "l"(gmem_src), "r"(bytes), "l"(policy)
+// The same, reading only the first `bytes` (0 or 16) and zero-filling the rest.
+__device__ __forceinline__ void cp_async16_zfill(void* smem_dst, const void* gmem_src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem_dst)), "l"(gmem_src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -168,31 +165,6 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// Cluster launch control: asks for a block of this grid that has not started
-// to be cancelled and handed to this CTA; the 16-byte answer completes on
-// `bar`.  After an answer that says no, nothing more may be asked.
-__device__ __forceinline__ void launch_control_try_cancel(void* answer, uint64_t* bar) {
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-          smem_addr(answer)),
-      "r"(smem_addr(bar))
-      : "memory");
-}
-// The x index of the block handed over, or -1.
-__device__ __forceinline__ int launch_control_block(const void* answer) {
-  int x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
-      "ld.shared.b128 h, [%1];\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-      "mov.s32 %0, -1;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
-      : "=r"(x)
-      : "r"(smem_addr(answer))
-      : "memory");
-  return x;
-}
 
 // Two fp32 additions in one packed instruction (each lane rounds to nearest
 // like a scalar add).

@@ -402,12 +402,12 @@ def test_attention_many_streams_a_block(dtype, lens, H, Hk, hd, ps, order):
     (F32, [2100, 7, 3333, 1500] * 20, 8, 8, 64, "token", 16),
     (BF, [1000 + 7 * i for i in range(300)], 16, 2, 128, "token", 16),   # more lengths than one count covers
 ])
-def test_attention_spare_units(dtype, lens, H, Hk, hd, order, tile):
-    """Calls long enough that CTAs which are done take over spare units: whole streams and shared ones; the
-    same bits every time, whoever computed what."""
+def test_attention_large_calls(dtype, lens, H, Hk, hd, order, tile):
+    """Calls with long pieces, whose joins the pieces name: whole streams and shared ones; the same bits every
+    time."""
     a = make_attention(lens, H, Hk, hd, 16, dtype, order, seed=11)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    assert sum(-(-n // tile) for n in lens) * Hk >= 2 * sms * 192   # else no spares
+    assert sum(-(-n // tile) for n in lens) * Hk >= 2 * sms * 192   # else a small call
     out, lse = run_attention(a)
     check_attention(a, out, lse, 1.0 / hd ** 0.5, rows=range(0, len(lens), max(1, len(lens) // 12)))
     for _ in range(5):
