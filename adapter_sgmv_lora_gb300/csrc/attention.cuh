@@ -18,13 +18,14 @@
 // to the one whose piece holds its first tile: no stream is shared, no warp
 // waits for another.  So with up to kSoloTokens tokens a stream and a stream
 // for more than every other warp of the GPU (4720 streams of one or two tiles:
-// 47 us before, 27 after; 1216 of 14 tiles 31.9 and 27.8; 352 of 3 to 6 tiles
-// 16.0 and 18.6, so those stay with blocks), or with one or two tiles and more
-// streams than SMs (592 streams of one tile 14.2 and 10.7).
+// 46.8 us by blocks, 26.0 by warps; 1216 of 14 tiles 32.4 and 28.8; 352 of 3 to
+// 6 tiles 16.0 and 18.6, so those stay with blocks), or with one or two tiles
+// and more streams than SMs (592 streams of one tile 16.6 and 10.2).
 //
 // Within a CTA the warps take the tiles of a piece in turn, each through its
 // own ring of asynchronous copies; a ring runs ahead across the ends of
-// streams, so memory stays busy while results are put together.  Each warp
+// streams, so memory stays busy while results are put together.  Each step
+// commits one group of copies, an empty one where no tile is left.  Each warp
 // keeps a running maximum m, sum l and unnormalised output O of the softmax
 // (one pass over the keys): a tile with scores s and values v does
 //   m' = max(m, max s), O = O 2^(m-m') + sum 2^(s-m') v, l likewise,
@@ -244,7 +245,7 @@ struct Plan {
     solo = (reach <= kSoloTokens / Core::TT && 2 * all > (long long)Core::CTAS * p.sms * Core::W) ||
            (reach <= 2 && all > p.sms);
     // Else pieces with a tile for every warp, or a stream each while that is
-    // no more than a piece to an SM (72 streams of one tile 10.7 us, a warp
+    // no more than a piece to an SM (72 streams of one tile 9.1 us, a warp
     // each 17.1).
     const long long full = (tiles * streams + Core::W - 1) / Core::W;
     const long long apart = all < p.sms ? all : p.sms;
@@ -599,7 +600,8 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
 // 131071 tokens: 25 us of joining before, 5 now).  Large calls have hundreds
 // of streams shared by two or three pieces and no room on the SMs before the
 // pieces are done: there the pieces leave the answer in memory and a warp is
-// one head (256 ragged contexts 186.9 and 183.6 us).
+// one head (256 ragged contexts 192.8 us, in the small calls' way 195.3; 24
+// long ones 300.5 and 306.4).
 constexpr int kJoinWarps = 4, kJoinBatch = 8;
 constexpr int kLargePlaces = 192;  // places a piece of a large call
 
