@@ -20,7 +20,11 @@
 // for more than every other warp of the GPU (4720 streams of one or two tiles:
 // 46.8 us by blocks, 26.0 by warps; 1216 of 14 tiles 32.4 and 28.8; 352 of 3 to
 // 6 tiles 16.0 and 18.6, so those stay with blocks), or with one or two tiles
-// and more streams than SMs (592 streams of one tile 16.6 and 10.2).
+// and more streams than SMs (592 streams of one tile 16.6 and 10.2).  Where
+// streams are short and no more than the blocks that fit on the GPU each takes
+// one: nothing to join (224 streams of 4 to 7 tiles 20.6 us by even pieces,
+// 15.3 so; 128 of up to 16 tiles 14.8 and 13.2).  Past four tiles a warp even
+// pieces are as fast or faster (32 of 19 to 38 tiles 13.0 and 16.2).
 //
 // Within a CTA the warps take the tiles of a piece in turn, each through its
 // own ring of asynchronous copies; a ring runs ahead across the ends of
@@ -135,6 +139,7 @@ struct Piece {
 };
 
 constexpr int kSoloTokens = 256;
+constexpr int kEachTiles = 4;  // tiles a warp
 
 // Sum over the warp of values below 2^32 / of any size.
 __device__ __forceinline__ long long warp_sum(unsigned v) {
@@ -211,6 +216,7 @@ struct Plan {
   static constexpr int CHUNK = 32 * Count<Core>::PER;
   Line line;
   bool solo;   // pieces are for warps, streams are whole
+  bool each;   // piece u is stream u: lo is its number in the sequence
   bool small;  // one count covers the sequences, and places fit 32 bits
 
   // c: the count of the first sequences.
@@ -244,15 +250,12 @@ struct Plan {
     const int reach = longest - Core::STREAM_COST;  // tiles of the longest stream
     solo = (reach <= kSoloTokens / Core::TT && 2 * all > (long long)Core::CTAS * p.sms * Core::W) ||
            (reach <= 2 && all > p.sms);
-    // Else pieces with a tile for every warp, or a stream each while that is
-    // no more than a piece to an SM (72 streams of one tile 9.1 us, a warp
-    // each 17.1).
-    const long long full = (tiles * streams + Core::W - 1) / Core::W;
-    const long long apart = all < p.sms ? all : p.sms;
-    const long long want = solo ? all : (full > apart ? full : apart);
+    // Else pieces with a tile for every warp.
+    const long long want = solo ? all : (tiles * streams + Core::W - 1) / Core::W;
     const long long most = solo ? (long long)p.pieces * Core::W : p.pieces;
-    line.cut(one * streams, (int)(want < 1 ? 1 : (want < most ? want : most)));
     small = once && one < INT_MAX;
+    each = !solo && reach <= kEachTiles * Core::W && all <= p.pieces && live == p.num_seqs;
+    line.cut(one * streams, (int)(each ? all : want < 1 ? 1 : want < most ? want : most));
   }
 
   // Piece u.  c: the count of the first sequences.
@@ -262,6 +265,12 @@ struct Plan {
     r.lo = r.hi = r.origin = 0;
     r.seq = 0;
     if (u >= line.pieces || line.total == 0) return r;
+    if (each) {
+      r.seq = u / streams;
+      r.lo = u - r.seq * streams;
+      r.hi = r.lo + 1;
+      return r;
+    }
     r.lo = line.start(u);
     r.hi = line.start(u + 1);
     // The sequence whose one-stream places contain lo / streams.
@@ -294,26 +303,27 @@ template <class Core>
 struct Segments {
   long long room;  // places of the piece from this stream's first tile on
   int seq, stream, len, n, t0, t1;
-  bool valid, solo;
+  bool valid, whole;  // whole: streams are not cut
 
   __device__ __forceinline__ void clip() {
-    t1 = n <= room || solo ? n : (int)room;
+    t1 = n <= room || whole ? n : (int)room;
     valid = room > 0 && t1 > t0;
   }
-  __device__ __forceinline__ void first(const AttnDesc& p, const Piece& r, bool solo_) {
+  __device__ __forceinline__ void first(const AttnDesc& p, const Piece& r, const Plan<Core>& plan) {
     valid = r.lo < r.hi;
     if (!valid) return;
     seq = r.seq;
     len = p.lengths[seq];
     n = tiles_of<Core::TT>(p, len);
+    whole = plan.solo || plan.each;
     const long long in = r.lo - r.origin;
     const int places = n + Core::STREAM_COST;
-    stream = (int)divide(in, places);
-    const long long tile0 = r.origin + (long long)stream * places + Core::STREAM_COST;  // place of the first tile
+    stream = plan.each ? (int)r.lo : (int)divide(in, places);
+    const long long tile0 =  // place of the first tile
+        plan.each ? r.lo : r.origin + (long long)stream * places + Core::STREAM_COST;
     t0 = r.lo > tile0 ? (int)(r.lo - tile0) : 0;
     room = r.hi - tile0;
-    solo = solo_;
-    if (solo && t0 > 0) next(p);  // the stream is the piece's before
+    if (whole && t0 > 0) next(p);  // the stream is the piece's before
     else clip();
   }
   __device__ __forceinline__ void next(const AttnDesc& p) {
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
   Segments<Core> seg;
   {
     const Piece piece = plan.locate(p, count, u);
-    seg.first(p, piece, solo);
+    seg.first(p, piece, plan);
     if (p.large && threadIdx.x == 0)
       p.splits[blockIdx.x] = solo ? make_int4(0, 0, 0, 0) : split_of<Core>(plan.line, piece, seg, u);
   }
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
       plan.make(p, count, false);
       const Piece piece = plan.locate(p, count, u);
       Segments<Core> sg;
-      sg.first(p, piece, plan.solo);
+      sg.first(p, piece, plan);
       split = split_of<Core>(plan.line, piece, sg, u);
       if (lane == 0) s_split = split;
     }

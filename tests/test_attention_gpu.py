@@ -396,6 +396,17 @@ def test_attention_many_streams_a_block(dtype, lens, H, Hk, hd, ps, order):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dtype,H,Hk,hd,ps", [(BF, 8, 8, 128, 16), (BF, 24, 1, 64, 8), (F32, 6, 2, 80, 5), (BF, 9, 1, 256, 1)])
+@pytest.mark.parametrize("lens", [[1], [0], [0, 0, 7], [64, 63, 1, 0, 17, 33, 2, 0], [0, 128, 127, 65] * 7])
+def test_attention_short_streams_few(dtype, H, Hk, hd, ps, lens):
+    """So few and short that every stream may have a block of its own, empty sequences among them."""
+    a = make_attention(lens, H, Hk, hd, ps, dtype, "token", seed=13)
+    out, lse = run_attention(a)
+    check_attention(a, out, lse, 1.0 / hd ** 0.5)
+    again, lse2 = run_attention(a)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("dtype,lens,H,Hk,hd,order,tile", [
     (BF, [4000, 6500, 9000, 1, 0, 5555] * 8, 16, 8, 128, "token", 16),
     (BF, [17000, 33, 9111, 20001] * 12, 16, 4, 64, "head", 32),
