@@ -8,9 +8,10 @@
 //   S^T [16 tokens, 8 heads] = K [16, HD] Q^T       K by ldmatrix, Q in registers
 //   O^T [HD, 8 heads]       += V^T [HD, 16] P       V by transposing ldmatrix
 // P comes out of the first product with tokens along its rows and is turned
-// into the second's operand in registers (movmatrix).  It enters as two bf16
-// terms, p = hi + lo, so its rounding stays near 2^-17; one term would put an
-// error as large as the output's own rounding on top of it.
+// into the second's operand in registers (movmatrix).  It enters as three bf16
+// terms whose sum is p to fp32's own 24 bits: two leave 2^-18, which moves one
+// output in some hundreds to the neighbouring bf16 value.  Every term of a
+// p > 0 is positive, so an infinite value comes out as that infinity.
 //
 // A call reads 512 bytes of cache per token and key/value head (128 wide) and
 // does 4096 flops on them for 8 heads: at memory speed that is some 55
@@ -162,7 +163,7 @@ struct MmaCore {
         for (int n = 0; n < NT; ++n) mma_bf16_16816(s[j][n][k % CHAINS], a, q[k][n][0], q[k][n][1]);
       }
     }
-    uint32_t hi[BLOCKS][NT][2], lo[BLOCKS][NT][2];
+    uint32_t pt[BLOCKS][NT][2][3];  // P's terms
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float x[BLOCKS][4], keep[2];
@@ -194,12 +195,11 @@ struct MmaCore {
       }
 #pragma unroll
       for (int j = 0; j < BLOCKS; ++j) {
-        split_hi_lo_bf16x2(x[j][0], x[j][1], hi[j][n][0], lo[j][n][0]);
-        split_hi_lo_bf16x2(x[j][2], x[j][3], hi[j][n][1], lo[j][n][1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          hi[j][n][e] = transpose_8x8(hi[j][n][e]);
-          lo[j][n][e] = transpose_8x8(lo[j][n][e]);
+          split3_bf16x2(x[j][2 * e], x[j][2 * e + 1], pt[j][n][e]);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) pt[j][n][e][i] = transpose_8x8(pt[j][n][e][i]);
         }
       }
       if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
@@ -221,8 +221,8 @@ struct MmaCore {
                       a[2], a[3]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma_bf16_16816(o[k][n], a, hi[j][n][0], hi[j][n][1]);
-          mma_bf16_16816(o[k][n], a, lo[j][n][0], lo[j][n][1]);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) mma_bf16_16816(o[k][n], a, pt[j][n][0][i], pt[j][n][1][i]);
         }
       }
     }

@@ -219,6 +219,22 @@ __device__ __forceinline__ void split_hi_lo_bf16x2(float a, float b, uint32_t& h
   lo = round_pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
 }
 
+// Two values v >= 0 as three bf16 terms each, every pair packed (first value in
+// the low half).  The first two terms are the leading eight bits of what is
+// left, taken just below it, so something is left for the next: all three are
+// positive where v is (down to 2^-110, where the last runs out of exponents),
+// and their sum is v to 24 bits.
+__device__ __forceinline__ void split3_bf16x2(float a, float b, uint32_t (&terms)[3]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t ta = max(__float_as_uint(a), 1u) - 1, tb = max(__float_as_uint(b), 1u) - 1;  // the floats below
+    terms[i] = __byte_perm(ta, tb, 0x7632);
+    a -= __uint_as_float(ta & 0xFFFF0000u);
+    b -= __uint_as_float(tb & 0xFFFF0000u);
+  }
+  terms[2] = round_pack_bf16x2(a, b);
+}
+
 // ------------------------------------------------ TMA tensor copies (tiled)
 // L2 cache policies for TMA and stores: streamed data first out, reused
 // weights last out.

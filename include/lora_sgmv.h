@@ -514,8 +514,8 @@ size_t lora_attention_workspace_bytes(const lora_attention_t* attention, const l
  * gives out = 0 and lse = -inf, as does a row whose every score is -inf.
  * Scores, softmax sums and the output's accumulation are fp32; on the bf16
  * tensor-core path (pages of a multiple of 8 tokens, rows of cache and q on
- * 16-byte boundaries) the probabilities enter the product with V as two bf16
- * terms (16 significant bits).  Cached values past a sequence's end and
+ * 16-byte boundaries) the probabilities enter the product with V as three
+ * bf16 terms, whose sum has fp32's 24 bits.  Cached values past a sequence's end and
  * block-table entries past its last page are never used.  A length below 0
  * or above max_pages * page_size raises LORA_DEV_BAD_LENGTH, a used page id
  * outside the cache LORA_DEV_BAD_PAGE; that sequence's rows of out and lse
