@@ -651,6 +651,8 @@ class KVCaches:
     layers: Sequence[KVCache]
 
     def __post_init__(self):
+        if any(c.k.device != self.layers[0].k.device for c in self.layers):
+            raise ValueError("the layers must be on one device")
         arr = (_KVCache * max(len(self.layers), 1))(*[c._struct for c in self.layers])
         object.__setattr__(self, "_struct", arr)
         object.__setattr__(self, "_ref", ctypes.addressof(arr))
