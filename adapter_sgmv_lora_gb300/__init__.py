@@ -651,6 +651,7 @@ class KVCaches:
     layers: Sequence[KVCache]
 
     def __post_init__(self):
+        object.__setattr__(self, "layers", tuple(self.layers))  # the caller's list may change, the structs do not
         if any(c.k.device != self.layers[0].k.device for c in self.layers):
             raise ValueError("the layers must be on one device")
         arr = (_KVCache * max(len(self.layers), 1))(*[c._struct for c in self.layers])

@@ -27,3 +27,12 @@ def test_caches_on_one_device():
     lk.KVCaches([layer(), layer()])
     with pytest.raises(ValueError):
         lk.KVCaches([layer(), layer(), layer("cuda:1")])
+
+
+def test_caches_keep_their_layers():
+    """A list that grows later does not change what was described: the count handed over is of the same layers."""
+    layers = [layer()]
+    caches = lk.KVCaches(layers)
+    layers.append(layer())
+    assert len(caches.layers) == 1 and len(caches._struct) == 1
+    assert len(lk.KVCaches([]).layers) == 0
