@@ -776,10 +776,23 @@ def lora_paged_attention(problem: AttentionProblem, workspace, stream=None) -> N
            "lora_paged_attention")
 
 
+def _page_numbers(name: str, pages) -> np.ndarray:
+    """int32 array of page numbers; what numpy would wrap or cut to one is refused."""
+    a = np.asarray(pages)
+    if a.dtype == np.int32:
+        return a
+    if a.size > 0:
+        if a.dtype.kind not in "iu":
+            raise ValueError("%s must hold integers" % name)
+        if a.min() < -2 ** 31 or a.max() >= 2 ** 31:
+            raise LoraError(2, "lora_kv_copy_pages")
+    return a.astype(np.int32)
+
+
 def lora_kv_copy_pages(caches: KVCaches, src, dst, stream=None) -> None:
     """Copy pages src[i] -> dst[i] (host integers) in every layer's K and V."""
-    s = np.asarray(src, dtype=np.int32)
-    d = np.asarray(dst, dtype=np.int32)
+    s = _page_numbers("src", src)
+    d = _page_numbers("dst", dst)
     if s.ndim != 1 or s.shape != d.shape:
         raise ValueError("src and dst must be 1-D and the same length")
     # As bytes: copying the list is cheaper than asking an array for its address.

@@ -36,3 +36,36 @@ def test_caches_keep_their_layers():
     layers.append(layer())
     assert len(caches.layers) == 1 and len(caches._struct) == 1
     assert len(lk.KVCaches([]).layers) == 0
+
+
+class Calls:
+    """Stands in for the library: keeps what a call hands over."""
+
+    def __init__(self):
+        self.got = None
+
+    def lora_kv_copy_pages(self, ref, num_caches, src, dst, n, stream):
+        self.got = (num_caches, np.frombuffer(src, np.int32).tolist(), np.frombuffer(dst, np.int32).tolist(), n)
+        return 0
+
+
+def test_copy_page_numbers_are_taken_as_they_are(monkeypatch):
+    calls = Calls()
+    monkeypatch.setattr(lk, "lib", lambda: calls)
+    caches = lk.KVCaches([layer()])
+    for good in ([3, 5], (3, 5), np.array([3, 5], np.int64), np.array([3, 5], np.uint8), [np.int32(3), 5]):
+        lk.lora_kv_copy_pages(caches, good, np.array([7, 2 ** 31 - 1], np.int32), stream=0)
+        assert calls.got == (1, [3, 5], [7, 2 ** 31 - 1], 2)
+    lk.lora_kv_copy_pages(caches, [], [], stream=0)
+    assert calls.got == (1, [], [], 0)
+    calls.got = None
+    for bad in ([2 ** 32 + 3, 5], np.array([2 ** 32 + 3, 5]), np.array([3, -2 ** 31 - 1]), np.array([3, 2 ** 31], np.uint32),
+                np.array([2 ** 64 - 1, 3], np.uint64)):
+        for pair in ((bad, [1, 2]), ([1, 2], bad)):
+            with pytest.raises(lk.LoraError) as e:   # a page outside the caches
+                lk.lora_kv_copy_pages(caches, *pair, stream=0)
+            assert e.value.status == 2
+    for bad in ([1.7, 5], np.array([3.0, 5.0]), [True, False], ["3", "5"], [2 ** 70, 3]):
+        with pytest.raises(ValueError):
+            lk.lora_kv_copy_pages(caches, bad, [1, 2], stream=0)
+    assert calls.got is None
