@@ -579,6 +579,16 @@ def _heads(name: str, t, shape, dtype) -> _Heads:
     return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
 
 
+def _i32(value, what: str) -> int:
+    """A whole number that an int32 argument holds as it is (ctypes would wrap it)."""
+    i = int(value)
+    if i != value:
+        raise ValueError("%s: %r is not a whole number" % (what, value))
+    if not -2 ** 31 <= i < 2 ** 31:
+        raise LoraError(2, what)
+    return i
+
+
 def lora_build_rope(rotary_dim: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                     original_max_positions: int = 0, low_turns: float = 1.0, high_turns: float = 4.0,
                     frequencies=None, attention_scale: float = 1.0) -> dict:
@@ -592,14 +602,17 @@ def lora_build_rope(rotary_dim: int, theta: float = 10000.0, scaling: str = "non
     instead of theta's."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
-    D = int(rotary_dim)
+    D = _i32(rotary_dim, "lora_build_rope")
+    positions = _i32(original_max_positions, "lora_build_rope")
+    if D > MAX_HEAD_DIM:
+        raise LoraError(2, "lora_build_rope")
     freq = None
     if frequencies is not None:
         freq = np.ascontiguousarray(frequencies, dtype=np.float64)
         if freq.shape != (D // 2,):
             raise ValueError("frequencies must hold rotary_dim / 2 values")
     turns = np.zeros(max(D // 2, 1), dtype=np.uint64)
-    rc = lib().lora_build_rope(D, float(theta), ROPE_SCALINGS[scaling], float(factor), int(original_max_positions),
+    rc = lib().lora_build_rope(D, float(theta), ROPE_SCALINGS[scaling], float(factor), positions,
                                float(low_turns), float(high_turns), None if freq is None else freq.ctypes.data,
                                turns.ctypes.data)
     _check(rc, "lora_build_rope")
@@ -806,7 +819,9 @@ class Pages:
     upload; only the methods change them."""
 
     def __init__(self, num_pages: int, page_size: int, max_seqs: int, max_pages: int):
-        if min(num_pages, page_size, max_seqs, max_pages) < 1:
+        sizes = [_i32(n, "lora_pages_init") for n in (num_pages, page_size, max_seqs, max_pages)]
+        num_pages, page_size, max_seqs, max_pages = sizes
+        if min(sizes) < 1:
             raise LoraError(2, "lora_pages_init")
         self.tables = np.empty((max_seqs, max_pages), dtype=np.int32)
         self.lengths = np.empty(max_seqs, dtype=np.int32)
@@ -823,23 +838,26 @@ class Pages:
     def append(self, seq: int, num_tokens: int):
         """(cache rows of the new tokens, page copies to run first as (src,
         dst) pairs: at most one)."""
-        rows = np.empty(max(int(num_tokens), 0), dtype=np.int32)
+        seq, num_tokens = _i32(seq, "lora_pages_append"), _i32(num_tokens, "lora_pages_append")
+        rows = np.empty(max(num_tokens, 0), dtype=np.int32)
         src, dst = ctypes.c_int32(), ctypes.c_int32()
-        _check(lib().lora_pages_append(ctypes.byref(self._c), int(seq), int(num_tokens), rows.ctypes.data,
+        _check(lib().lora_pages_append(ctypes.byref(self._c), seq, num_tokens, rows.ctypes.data,
                                        ctypes.byref(src), ctypes.byref(dst)), "lora_pages_append")
         return rows, ([(src.value, dst.value)] if src.value >= 0 else [])
 
     def fork(self, parent: int, child: int, num_tokens: Optional[int] = None) -> None:
         """child shares parent's first num_tokens (None: all of them)."""
+        parent, child = _i32(parent, "lora_pages_fork"), _i32(child, "lora_pages_fork")
         if num_tokens is None:
             if not 0 <= parent < self.lengths.size:
                 raise LoraError(2, "lora_pages_fork")
             num_tokens = int(self.lengths[parent])
-        _check(lib().lora_pages_fork(ctypes.byref(self._c), int(parent), int(child), int(num_tokens)),
+        _check(lib().lora_pages_fork(ctypes.byref(self._c), parent, child, _i32(num_tokens, "lora_pages_fork")),
                "lora_pages_fork")
 
     def trim(self, seq: int, num_tokens: int = 0) -> None:
-        _check(lib().lora_pages_trim(ctypes.byref(self._c), int(seq), int(num_tokens)), "lora_pages_trim")
+        _check(lib().lora_pages_trim(ctypes.byref(self._c), _i32(seq, "lora_pages_trim"),
+                                     _i32(num_tokens, "lora_pages_trim")), "lora_pages_trim")
 
     def compact(self):
         """(src, dst) page moves to run with lora_kv_copy_pages; the tables are already rewritten."""

@@ -69,3 +69,39 @@ def test_copy_page_numbers_are_taken_as_they_are(monkeypatch):
         with pytest.raises(ValueError):
             lk.lora_kv_copy_pages(caches, bad, [1, 2], stream=0)
     assert calls.got is None
+
+
+BIG = 2 ** 32
+
+
+def test_pages_numbers_are_taken_as_they_are():
+    """What passes 32 bits, or is no whole number, is not another sequence or another count."""
+    for sizes in ((BIG + 4, 4, 2, 3), (4, BIG + 4, 2, 3), (4, 4, BIG + 2, 3), (4, 4, 2, BIG + 3)):
+        with pytest.raises(lk.LoraError) as e:
+            lk.Pages(*sizes)
+        assert e.value.status == 2
+    with pytest.raises(ValueError):
+        lk.Pages(4, 4.5, 2, 3)
+    p = lk.Pages(8, 4, 2, 3)
+    p.append(np.int64(0), np.int32(6))
+    before = p.tables.copy(), p.lengths.copy()
+    for f in (lambda: p.append(BIG, 1), lambda: p.append(0, BIG + 1), lambda: p.append(1, -BIG + 2),
+              lambda: p.fork(BIG, 1, 2), lambda: p.fork(0, BIG + 1), lambda: p.fork(0, 1, BIG + 2),
+              lambda: p.trim(BIG), lambda: p.trim(0, BIG + 2), lambda: p.trim(-BIG)):
+        with pytest.raises(lk.LoraError) as e:
+            f()
+        assert e.value.status == 2
+    for f in (lambda: p.append(0.5, 1), lambda: p.append(0, 1.7), lambda: p.fork(0, 1, 2.5), lambda: p.trim(0, 2.5)):
+        with pytest.raises(ValueError):
+            f()
+    assert np.array_equal(p.tables, before[0]) and np.array_equal(p.lengths, before[1])
+
+
+def test_rope_numbers_are_taken_as_they_are():
+    for kw in (dict(rotary_dim=BIG + 64), dict(rotary_dim=-BIG + 64),
+               dict(rotary_dim=64, scaling="parts", factor=2.0, original_max_positions=BIG + 8192)):
+        with pytest.raises(lk.LoraError) as e:
+            lk.lora_build_rope(**kw)
+        assert e.value.status == 2
+    with pytest.raises(ValueError):
+        lk.lora_build_rope(64.5)
