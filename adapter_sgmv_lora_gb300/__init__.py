@@ -194,8 +194,12 @@ def _stream_handle(stream) -> Optional[int]:
     import torch
     if stream is None:
         # The raw handle: building a Stream object costs more than a small call's kernel.
+        # It comes from private functions of torch; a version without them has the public one.
         if torch.cuda.is_initialized():
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            try:
+                return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            except AttributeError:
+                pass
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 

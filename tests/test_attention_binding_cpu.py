@@ -105,3 +105,17 @@ def test_rope_numbers_are_taken_as_they_are():
         assert e.value.status == 2
     with pytest.raises(ValueError):
         lk.lora_build_rope(64.5)
+
+
+def test_current_stream_without_torchs_private_calls(monkeypatch):
+    """The short way to the current stream's handle is torch's own business: without it the public one serves."""
+    import torch
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    assert lk._stream_handle(None) == 1003
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name)
+        assert lk._stream_handle(None) == 77
+    assert lk._stream_handle(5) == 5 and lk._stream_handle(types.SimpleNamespace(cuda_stream=9)) == 9
