@@ -788,7 +788,11 @@ def new_attention_workspace(problem: AttentionProblem):
 
 def lora_paged_attention(problem: AttentionProblem, workspace, stream=None) -> None:
     """Attention of one new token per sequence over its cached pages (include/lora_sgmv.h)."""
-    ws, nbytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.device != problem.q.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        ws, nbytes = workspace.data_ptr(), workspace.nbytes
     _check(lib().lora_paged_attention(problem._ref, problem.cache._ref, ws, nbytes, _stream_handle(stream)),
            "lora_paged_attention")
 

@@ -119,3 +119,21 @@ def test_current_stream_without_torchs_private_calls(monkeypatch):
         monkeypatch.delattr(torch._C, name)
         assert lk._stream_handle(None) == 77
     assert lk._stream_handle(5) == 5 and lk._stream_handle(types.SimpleNamespace(cuda_stream=9)) == 9
+
+
+def test_attention_workspace_is_memory_of_the_call(monkeypatch):
+    """A workspace of the host, of another device, or whose bytes are not all there never reaches the kernel."""
+    import torch
+    calls = []
+    monkeypatch.setattr(lk, "lib", lambda: types.SimpleNamespace(
+        lora_paged_attention=lambda problem, cache, ws, nbytes, stream: calls.append((ws, nbytes)) or 0))
+    problem = types.SimpleNamespace(_ref=1, cache=types.SimpleNamespace(_ref=2), q=types.SimpleNamespace(device="cuda:0"))
+    ws = lambda **kw: types.SimpleNamespace(**{**dict(is_cuda=True, device="cuda:0", is_contiguous=lambda: True,
+                                                      data_ptr=lambda: 4096, nbytes=512), **kw})
+    lk.lora_paged_attention(problem, ws(), stream=0)
+    lk.lora_paged_attention(problem, None, stream=0)      # the library refuses it
+    assert calls == [(4096, 512), (None, 0)]
+    for bad in (torch.empty(128), ws(device="cuda:1"), ws(is_contiguous=lambda: False)):
+        with pytest.raises(ValueError):
+            lk.lora_paged_attention(problem, bad, stream=0)
+    assert len(calls) == 2
