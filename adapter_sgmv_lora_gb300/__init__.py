@@ -630,6 +630,13 @@ class Rope:
     rotary_dim: int
     attention_scale: float = 1.0
 
+    def __post_init__(self):
+        import torch
+        t = self.turns
+        if t.dtype not in (torch.int64, torch.uint64) or t.dim() != 1 or not t.is_contiguous() or \
+                t.numel() < self.rotary_dim // 2:
+            raise ValueError("turns must be a contiguous int64 tensor of rotary_dim / 2 values")
+
 
 def rope_to_device(r: dict, device="cuda") -> Rope:
     """Upload the host table from lora_build_rope."""
@@ -709,8 +716,6 @@ class RopeProblem:
                  turns=self.rope.turns if self.rope is not None else None, cache_rows=self.cache_rows,
                  cache=self.cache.k if self.cache is not None else None, q_weight=self.q_weight,
                  k_weight=self.k_weight)
-        if self.rope is not None and self.rope.turns.numel() < rot // 2:
-            raise ValueError("turns must hold rotary_dim / 2 values")
         for name, t in (("positions", self.positions), ("cache_rows", self.cache_rows)):
             if t is not None:
                 _int32(name, t, (T,))

@@ -137,3 +137,12 @@ def test_attention_workspace_is_memory_of_the_call(monkeypatch):
         with pytest.raises(ValueError):
             lk.lora_paged_attention(problem, bad, stream=0)
     assert len(calls) == 2
+
+
+def test_rope_table_holds_its_words():
+    import torch
+    t = lk.rope_to_device(lk.lora_build_rope(64), "cpu").turns
+    assert lk.Rope(t, 64).turns is t and lk.Rope(t, 32).rotary_dim == 32
+    for bad in (t.float(), t.int(), t.reshape(4, 8), t[:31], t[:1].expand(32), torch.cat([t, t])[::2]):
+        with pytest.raises(ValueError):
+            lk.Rope(bad, 64)
