@@ -34,6 +34,8 @@ extern "C" lora_status_t lora_build_rope(int32_t rotary_dim, double theta, lora_
       if (!std::isfinite(frequencies[i])) return LORA_ERR_SHAPE;
   double base = theta;
   if (scaling == LORA_ROPE_NTK) base = theta * std::pow(factor, rotary_dim / (rotary_dim - 2.0));
+  if (!frequencies && !(base > 0.0 && std::isfinite(base))) return LORA_ERR_SHAPE;
+  double scaled[LORA_MAX_HEAD_DIM / 2];
   for (int32_t i = 0; i < n; ++i) {
     double f = frequencies ? frequencies[i] : std::pow(base, -2.0 * i / rotary_dim);
     if (scaling == LORA_ROPE_LINEAR) f /= factor;
@@ -43,7 +45,11 @@ extern "C" lora_status_t lora_build_rope(int32_t rotary_dim, double theta, lora_
       g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
       f = g * f + (1.0 - g) * f / factor;
     }
-    double t = f / kTwoPi;
+    if (!std::isfinite(f)) return LORA_ERR_SHAPE;
+    scaled[i] = f;
+  }
+  for (int32_t i = 0; i < n; ++i) {
+    double t = scaled[i] / kTwoPi;
     t -= std::floor(t);  // [0, 1]: a tiny negative turn rounds up to 1, the same angle as 0
     turns[i] = t < 1.0 ? static_cast<uint64_t>(std::ldexp(t, 64)) : 0;
   }

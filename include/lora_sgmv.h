@@ -433,8 +433,8 @@ typedef enum {
  * lora_rope_t.turns.  Errors: LORA_ERR_SHAPE (rotary_dim odd, < 2 or >
  * LORA_MAX_HEAD_DIM; theta or factor not positive and finite; NTK with
  * frequencies given or rotary_dim < 4; PARTS with original_max_positions < 1
- * or high_turns <= low_turns; a frequency that is not finite; an unknown
- * scaling), LORA_ERR_NULL.
+ * or high_turns <= low_turns; a frequency, or the NTK base, that is not finite
+ * as given or as scaled; an unknown scaling), LORA_ERR_NULL.
  */
 lora_status_t lora_build_rope(int32_t rotary_dim, double theta, lora_rope_scaling_t scaling, double factor,
                               int32_t original_max_positions, double low_turns, double high_turns,

@@ -146,3 +146,24 @@ def test_rope_table_holds_its_words():
     for bad in (t.float(), t.int(), t.reshape(4, 8), t[:31], t[:1].expand(32), torch.cat([t, t])[::2]):
         with pytest.raises(ValueError):
             lk.Rope(bad, 64)
+
+
+@pytest.mark.parametrize("kw", [dict(rotary_dim=64, scaling="linear", factor=1e-310),
+                                dict(rotary_dim=4, scaling="ntk", factor=1e200),
+                                dict(rotary_dim=4, theta=1e308, scaling="ntk", factor=8.0),
+                                dict(rotary_dim=4, theta=1e-300, scaling="ntk", factor=1e-200),
+                                dict(rotary_dim=2, frequencies=[1e300], scaling="linear", factor=1e-300),
+                                dict(rotary_dim=2, frequencies=[1e300], scaling="parts", factor=1e-300,
+                                     original_max_positions=1, low_turns=1e305, high_turns=1e306)])
+def test_rope_frequencies_that_overflow_in_scaling(kw):
+    """A scaled frequency that is not finite is an error and nothing is written, not a pair without rotation."""
+    with pytest.raises(lk.LoraError) as e:
+        lk.lora_build_rope(**kw)
+    assert e.value.status == 2
+    turns = np.full(2, 77, np.uint64)
+    f = np.array(kw["frequencies"]) if "frequencies" in kw else None
+    args = (kw["rotary_dim"], kw.get("theta", 1e4), lk.ROPE_SCALINGS[kw["scaling"]], kw["factor"],
+            kw.get("original_max_positions", 0), kw.get("low_turns", 1.0), kw.get("high_turns", 4.0),
+            None if f is None else f.ctypes.data, turns.ctypes.data)
+    if kw["rotary_dim"] <= 4:
+        assert lk.lib().lora_build_rope(*args) == 2 and turns.tolist() == [77, 77]
