@@ -61,14 +61,16 @@ lora_status_t validate_input(const lora_heads_t& h, int dtype) {
   return aligned(h.data, elem_bytes(dtype)) ? LORA_OK : LORA_ERR_ALIGN;
 }
 
-// `in` is the view that `out` may be written over.
+// `in` is the view that `out` may be written over: with the same strides,
+// where they reach anything.
 lora_status_t validate_output(const lora_heads_t& out, const lora_heads_t& in, int64_t rows, int64_t heads,
                               int64_t head_dim, int dtype) {
   if (!out.data) return LORA_ERR_NULL;
   if (!aligned(out.data, elem_bytes(dtype))) return LORA_ERR_ALIGN;
   std::pair<int64_t, int64_t> dims[2] = {{out.row_stride, rows}, {out.head_stride, heads}};
   if (!disjoint(dims, head_dim)) return LORA_ERR_SHAPE;
-  if (out.data == in.data && (out.row_stride != in.row_stride || out.head_stride != in.head_stride))
+  if (out.data == in.data && ((rows > 1 && out.row_stride != in.row_stride) ||
+                              (heads > 1 && out.head_stride != in.head_stride)))
     return LORA_ERR_SHAPE;
   return LORA_OK;
 }

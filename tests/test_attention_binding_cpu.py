@@ -167,3 +167,32 @@ def test_rope_frequencies_that_overflow_in_scaling(kw):
             None if f is None else f.ctypes.data, turns.ctypes.data)
     if kw["rotary_dim"] <= 4:
         assert lk.lib().lora_build_rope(*args) == 2 and turns.tolist() == [77, 77]
+
+
+def test_in_place_strides_that_reach_nothing():
+    """Over its input an output needs the same strides, but a row stride of one row (a head stride of one head)
+    reaches nothing: torch gives such dimensions any stride."""
+    import ctypes
+    L = lk.lib()
+    ref = ctypes.addressof
+    cache = lk._KVCache(lk.DTYPE_BF16, 4, 16, 1, 64, 4096, 8192, 1024, 64, 64)
+
+    def attend(seqs, heads, q, out):
+        a = lk._Attention(seqs, heads, lk._Heads(4096, *q), lk._Heads(4096, *out), 4096, 8, 8, 4096, 1.0, None)
+        return L.lora_paged_attention(ref(a), ref(cache), None, 0, None)
+
+    assert attend(1, 4, (999, 64), (256, 64)) == 8          # on to the workspace
+    assert attend(3, 1, (256, 64), (256, 999)) == 8
+    assert attend(2, 4, (999, 64), (256, 64)) == 2
+    assert attend(1, 4, (256, 128), (256, 64)) == 2
+
+    def rotate(tokens, heads, q, q_out):
+        h = lk._Heads(4096, *q)
+        none = lk._Heads(None, 0, 0)
+        r = lk._Rope(lk.DTYPE_BF16, tokens, heads, 1, 64, 64, 0, 1.0, 1e-6, 4096, 4096, h, h, none,
+                     lk._Heads(4096, *q_out), none, None, None, 4096)
+        return L.lora_rope_append(ref(r), ref(cache), None)
+
+    assert rotate(1, 4, (999, 64), (256, 64)) == 1           # on to the missing v
+    assert rotate(3, 1, (256, 64), (256, 999)) == 1
+    assert rotate(2, 4, (999, 64), (256, 64)) == 2
