@@ -66,16 +66,24 @@ class AttentionLayer:
         return y
 
     def _append(self, seqs, counts):
-        """Rows and positions of counts[i] more tokens of seqs[i]; runs the copies that shared pages need."""
-        rows, positions, copies = [], [], []
-        for s, n in zip(seqs, counts):
-            start = int(self.pages.lengths[s])
-            r, c = self.pages.append(s, n)
-            rows.append(r)
-            copies += c
-            positions.append(np.arange(start, start + n, dtype=np.int32))
-        if copies:
-            lk.lora_kv_copy_pages(self.caches, *zip(*copies))
+        """Rows and positions of counts[i] more tokens of seqs[i]; runs the copies that shared pages need.  Where
+        the pages do not suffice for all of them the sequences stay as long as they were."""
+        rows, positions, copies, starts = [], [], [], []
+        try:
+            for s, n in zip(seqs, counts):
+                start = int(self.pages.lengths[s])
+                r, c = self.pages.append(s, n)
+                starts.append(start)
+                rows.append(r)
+                copies += c
+                positions.append(np.arange(start, start + n, dtype=np.int32))
+        except lk.LoraError:
+            for s, start in reversed(list(zip(seqs, starts))):
+                self.pages.trim(s, start)
+            raise
+        finally:  # the tables name the copies already, on an error too
+            if copies:
+                lk.lora_kv_copy_pages(self.caches, *zip(*copies))
         up = lambda a: torch.from_numpy(np.concatenate(a).astype(np.int32)).to(self.device)
         return up(rows), up(positions)
 

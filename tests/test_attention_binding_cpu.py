@@ -196,3 +196,32 @@ def test_in_place_strides_that_reach_nothing():
     assert rotate(1, 4, (999, 64), (256, 64)) == 1           # on to the missing v
     assert rotate(3, 1, (256, 64), (256, 999)) == 1
     assert rotate(2, 4, (999, 64), (256, 64)) == 2
+
+
+def test_example_append_that_runs_out_of_pages(monkeypatch):
+    """A step that does not fit changes no sequence: what was copied on write before the refusal has its contents."""
+    from examples.attention_layer import AttentionLayer
+    ps = 4
+    L = object.__new__(AttentionLayer)
+    L.device, L.caches, L.pages = "cpu", None, lk.Pages(5, ps, 4, 8)
+    cells = np.zeros((5, ps), dtype=np.int64)
+
+    def copy(caches, src, dst):
+        cells[list(dst)] = cells[list(src)]
+
+    monkeypatch.setattr(lk, "lora_kv_copy_pages", copy)
+    read = lambda s: [int(cells[L.pages.tables[s, j // ps], j % ps]) for j in range(L.pages.lengths[s])]
+    rows, positions = L._append([0, 2], [6, 8])              # four of the five pages
+    cells.reshape(-1)[rows.numpy()] = np.arange(1, 15)
+    assert positions.tolist() == list(range(6)) + list(range(8))
+    L.pages.fork(0, 1)
+    before = [read(s) for s in range(3)], L.pages.lengths.copy()
+    with pytest.raises(lk.LoraError) as e:
+        L._append([1, 0, 2], [1, 1, 1])                      # the fork's copy takes the last page
+    assert e.value.status == 11
+    assert np.array_equal(L.pages.lengths, before[1])
+    assert [read(s) for s in range(3)] == before[0]
+    L.pages.trim(2, 0)
+    rows, _ = L._append([1, 0], [1, 1])
+    cells.reshape(-1)[rows.numpy()] = [90, 91]
+    assert read(1) == before[0][0] + [90] and read(0) == before[0][0] + [91]
