@@ -607,13 +607,13 @@ __global__ void __launch_bounds__(Core::W * 32, Core::CTAS) attention_kernel(con
 // its warps share the partial results out.  Which stream it is follows from
 // the lengths alone and is found while the pieces still run; after them the
 // statistics and the outputs are one round trip to memory (one context of
-// 131071 tokens: 25 us of joining before, 5 now).  Large calls have hundreds
-// of streams shared by two or three pieces and no room on the SMs before the
-// pieces are done: there the pieces leave the answer in memory and a warp is
-// one head (256 ragged contexts 192.8 us, in the small calls' way 195.3; 24
-// long ones 300.5 and 306.4).
+// 131071 tokens: 25 us of joining before, 5 now).  Calls that may be large
+// (large_of) mostly have hundreds of streams shared by two or three pieces and
+// no room on the SMs before the pieces are done: there the pieces leave the
+// answer in memory and a warp is one head (256 ragged contexts 192.8 us, in
+// the small calls' way 195.3; 24 long ones 300.5 and 306.4).
 constexpr int kJoinWarps = 4, kJoinBatch = 8;
-constexpr int kLargePlaces = 192;  // places a piece of a large call
+constexpr int kLargePlaces = 192;  // places a piece, where every sequence fills its table
 
 template <class Core>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ AttnDesc p) {
@@ -742,7 +742,10 @@ inline long long most_places(const CoreShape& c, const AttnDesc& p) {
 
 // Pieces the line is cut into at most: what fits on the GPU at once, or less
 // when the longest sequences would give every warp a tile with fewer (but one
-// for each stream).
+// for each stream).  The longest the block tables allow: the lengths are on the
+// device.  A table wider than need be costs the blocks that find no work, and
+// their joins (one context of 517 tokens: 10.5 us with a table of 33 pages,
+// 12.6 with one of 8192; 16 of 60 tokens 8.5 and 8.8).
 inline int pieces_of(const CoreShape& c, const AttnDesc& p, int sms) {
   const long long most = (long long)c.CTAS * std::max(sms, 1), streams = streams_of(c, p);
   if (streams >= most * c.W) return (int)most;
@@ -750,7 +753,13 @@ inline int pieces_of(const CoreShape& c, const AttnDesc& p, int sms) {
   if (most_tiles(c, p) <= 2 && streams > sms) return (int)std::min(most, (streams + c.W - 1) / c.W);
   return (int)std::max(1LL, std::min(most, std::max(std::min(streams, most), (most_tiles(c, p) * streams + c.W - 1) / c.W)));
 }
-// Long pieces, and streams that are not shared by more than eight of them.
+// Whether pieces are long, and streams shared by no more than eight of them,
+// where every sequence fills its table.  The lengths may be anything below
+// that.  Joining as a large call is no slower then (64 contexts of 200 tokens
+// in tables of 2048 pages 22.3 us, in the small calls' way 25.3; 40 of 1000 38.2
+// and 40.7; 300 of 64 26.0 and 28.8), unless one context outweighs the others and
+// its many parts are a warp's to join (one of 131071 tokens among 39 of 200:
+// 103.2 and 101.5).
 inline bool large_of(const CoreShape& c, const AttnDesc& p, int sms) {
   const long long most = (long long)c.CTAS * std::max(sms, 1);
   return most_places(c, p) / most >= kLargePlaces && streams_of(c, p) * 8 >= most;

@@ -29,8 +29,9 @@ namespace {
 template <int HD_, int NT, int GRAIN_>
 struct MmaCore {
   using T = __nv_bfloat16;
-  // A stage is 8 KB (4 KB for the narrowest heads): narrow heads take two
-  // blocks of 16 tokens a tile, so the fixed steps of a tile weigh the same.
+  // A stage is 8 KB (16 KB for the widest heads, 4 KB for the narrowest): narrow
+  // heads take two blocks of 16 tokens a tile, so the fixed steps of a tile weigh
+  // the same.
   static constexpr int BLOCKS = HD_ <= 64 ? 2 : 1, TT = 16 * BLOCKS;
   static constexpr int GRAIN = GRAIN_, GRAINS = TT / GRAIN;
   static constexpr int W = 4, HD = HD_, CH = 8 * NT, COMB = 4;
@@ -257,8 +258,9 @@ bool mma_attention_ok(const AttnDesc& p) {
   const CacheDesc& c = p.cache;
   const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) |
                    reinterpret_cast<uintptr_t>(p.q.data);
-  return p.dtype == LORA_DTYPE_BF16 && c.page_size % 8 == 0 && (low & 15) == 0 && c.head_dim % 8 == 0 && c.page_stride % 8 == 0 &&
-         c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && p.q.row_stride % 8 == 0 && p.q.head_stride % 8 == 0;
+  return p.dtype == LORA_DTYPE_BF16 && c.page_size % 8 == 0 && (low & 15) == 0 && c.head_dim % 8 == 0 &&
+         c.page_stride % 8 == 0 && c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && p.q.row_stride % 8 == 0 &&
+         p.q.head_stride % 8 == 0;
 }
 
 // f(a core's type) for the head width, group and page size of p.
@@ -276,6 +278,10 @@ auto with_grain(const AttnDesc& p, F f) {
   if (hd <= 128) return f((MmaCore<128, 2, GRAIN>*)nullptr);
   return f((MmaCore<256, 2, GRAIN>*)nullptr);
 }
+// Grains of 16 where pages hold them, else of 8: fewer table look-ups and
+// offsets a tile (24 contexts of 4000 to 16000 tokens, 256 wide, 16 heads a
+// group 233 us against 243 by grains of 8; 256 ragged ones 64 wide 119.5 and
+// 121.3; 24 long ones 128 wide 303.4 and 305.1).
 template <class F>
 auto with_core(const AttnDesc& p, F f) {
   return p.cache.page_size % 16 == 0 ? with_grain<16>(p, f) : with_grain<8>(p, f);
