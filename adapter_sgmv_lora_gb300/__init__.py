@@ -601,9 +601,11 @@ def lora_build_rope(rotary_dim: int, theta: float = 10000.0, scaling: str = "non
 
     scaling: "none", "linear" (position interpolation), "ntk", or "parts" (by
     parts between low_turns and high_turns turns over original_max_positions:
-    1 and 4 for Llama 3's rule, 1 and 32 for YaRN's, whose attention_scale is
-    0.1 ln(factor) + 1).  frequencies: rotary_dim / 2 radians per position
-    instead of theta's."""
+    1 and 4 for Llama 3's rule, 1 and 32 for YaRN's formula, whose
+    attention_scale is 0.1 ln(factor) + 1).  The parts blend linearly in the
+    turns, as those formulas do.  Checkpoints whose code blends linearly in the
+    pair's index between the bounds' pairs need their frequencies given.
+    frequencies: rotary_dim / 2 radians per position instead of theta's."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
     D = _i32(rotary_dim, "lora_build_rope")

@@ -9,10 +9,12 @@
 // The angle.  turns[i] is the pair's frequency as a 64-bit fixed-point
 // fraction of a turn, so the wrapped product position * turns[i] IS the
 // fractional turn: its top 32 bits, read as a signed number of 2^-31 half
-// turns, go to sincospi.  No range reduction is needed and the error stays
-// near 2^-32 of a turn at any position, where an fp32 product position * f
-// loses whole hundredths of a radian at 100k tokens.  The table is one
-// 64-bit word per pair instead of a cos/sin row per position.
+// turns, go to sincospi.  No range reduction is needed.  What is lost is fp32's
+// rounding of that number, 2^-26 of a turn at most, and the table's own (an
+// entry comes from a double and is off by up to 2^-55 of a turn: 2^-24 at
+// position 2^31), where an fp32 product position * f loses whole hundredths of
+// a radian at 100k tokens.  The table is one 64-bit word per pair instead of a
+// cos/sin row per position.
 #include <cuda_bf16.h>
 #include <type_traits>
 
@@ -58,7 +60,10 @@ __device__ __forceinline__ long long cache_offset(const RopeDesc& p, int t) {
 }
 
 // Any type, size and alignment: one warp per head, element by element.  Block
-// = one token and a share of its heads (query, key, then value heads).
+// = one token and a share of its heads (query, key, then value heads).  Bound by
+// its instructions, an access of 2 or 4 bytes per element: 8192 bf16 tokens of
+// 32 + 2 x 8 heads, 80 wide, that rotate 20 take 106 us, rotating 64 by the
+// kernel below 34; 96 wide and 24 123, all 96 36.
 constexpr int kGenericWarps = 8;
 
 template <typename T>
@@ -135,16 +140,16 @@ __global__ void __launch_bounds__(kGenericWarps * 32) rope_generic_kernel(const 
 // flight.  Products go two to an instruction (f32x2).  What is larger than L2
 // anyway is read and written as streams (either alone gains nothing).
 //
-// Bounded by memory: 8192 bf16 tokens of 64 + 2 x 8 heads, 336 MB, take 58 us
-// (5.8 TB/s; a plain copy of as many bytes takes 58, too), 66.6 us without the
-// streams.  With norms (40 + 2 x 8 heads, 235 MB) 58 us: there the reductions'
-// latency shows.
+// Bounded by memory: 8192 bf16 tokens of 64 + 2 x 8 heads, 336 MB, take 55.6 us
+// (6.0 TB/s; a plain copy of as many bytes takes 57.9), and took 66.6 where
+// they take 57.3 with the streams.  With norms (40 + 2 x 8 heads, 235 MB) 57.3
+// us: there the reductions' latency shows.
 constexpr int kRopeWarps = 4;  // per block
 // Groups a batch; measured 5 / 4: 80 heads 57.3 / 60.9 us, 48 heads 39.4 / 39.4,
 // 56 heads with norms 60.9 / 57.9.
 constexpr int kRopeBatch = 5, kRopeNormBatch = 4;
 
-// Four chunk elements (two for fp32) as fp32, and back.
+// A chunk's elements, eight (four of fp32), as fp32, and back.
 template <typename T>
 struct Chunk;
 template <>

@@ -429,7 +429,8 @@ typedef enum {
  * scaled, as a 64-bit fixed-point fraction of a turn:
  *   turns[i] = floor(frac(f_i / (2 pi)) * 2^64).
  * position * turns[i] modulo 2^64 is then the angle's fractional turn with
- * no range reduction and no loss at long contexts; upload it for
+ * no range reduction; the entry's own rounding, that of a double (2^-55 of a
+ * turn), is all that grows with the position.  Upload it for
  * lora_rope_t.turns.  Errors: LORA_ERR_SHAPE (rotary_dim odd, < 2 or >
  * LORA_MAX_HEAD_DIM; theta or factor not positive and finite; NTK with
  * frequencies given or rotary_dim < 4; PARTS with original_max_positions < 1
@@ -479,9 +480,10 @@ typedef struct {
  * raises LORA_DEV_BAD_PAGE.  cache may be NULL exactly when cache_rows is.
  * q_out (k_out) may be q (k) itself, with the same strides, but must not
  * overlap the inputs otherwise.  num_tokens == 0 is a valid no-op.
- * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_SHAPE (sizes, a negative
- * input stride, output strides that let two elements share an address, a
- * cache whose type, heads or head_dim differ).
+ * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE (an unknown type, a cache of another),
+ * LORA_ERR_SHAPE (sizes, a negative input stride, output strides that let two
+ * elements share an address, a cache whose heads or head_dim differ),
+ * LORA_ERR_ALIGN (a pointer that is not on its element's boundary).
  */
 lora_status_t lora_rope_append(const lora_rope_t* rope, const lora_kv_cache_t* cache, lora_stream_t stream);
 
@@ -515,12 +517,13 @@ size_t lora_attention_workspace_bytes(const lora_attention_t* attention, const l
  * Scores, softmax sums and the output's accumulation are fp32; on the bf16
  * tensor-core path (pages of a multiple of 8 tokens, rows of cache and q on
  * 16-byte boundaries) the probabilities enter the product with V as three
- * bf16 terms, whose sum has fp32's 24 bits.  Cached values past a sequence's end and
- * block-table entries past its last page are never used.  A length below 0
- * or above max_pages * page_size raises LORA_DEV_BAD_LENGTH, a used page id
- * outside the cache LORA_DEV_BAD_PAGE; that sequence's rows of out and lse
- * are left as they were, the others are computed.  The cached tokens are shared out evenly over the GPU
- * whatever the lengths; the same lengths on the same GPU give the same bits.
+ * bf16 terms, whose sum has fp32's 24 bits.  Cached values past a sequence's
+ * end and block-table entries past its last page are never used.  A length
+ * below 0 or above max_pages * page_size raises LORA_DEV_BAD_LENGTH, a used
+ * page id outside the cache LORA_DEV_BAD_PAGE; that sequence's rows of out and
+ * lse are left as they were, the others are computed.  The cached tokens are
+ * shared out evenly over the GPU whatever the lengths; the same lengths, with
+ * tables of the same width on the same GPU, give the same bits.
  * workspace: >= lora_attention_workspace_bytes, 16-byte aligned, contents on
  * entry ignored; two calls that may overlap need two.
  * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_SHAPE, LORA_ERR_WORKSPACE,
@@ -537,8 +540,8 @@ lora_status_t lora_paged_attention(const lora_attention_t* attention, const lora
  * forks); a destination may not, nor be a source as well: the copies have no
  * order among themselves (LORA_ERR_SHAPE, as for a page outside the caches).
  * Gaps between strided rows are not touched.  Copies are exact, whatever the
- * values.  Errors also: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_WORKSPACE (no
- * host memory to check a long list).
+ * values.  Errors also: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_ALIGN,
+ * LORA_ERR_WORKSPACE (no host memory to check a long list).
  */
 lora_status_t lora_kv_copy_pages(const lora_kv_cache_t* caches, int32_t num_caches, const int32_t* src,
                                  const int32_t* dst, int32_t num_copies, lora_stream_t stream);
