@@ -11,7 +11,14 @@
 // into the second's operand in registers (movmatrix).  It enters as three bf16
 // terms whose sum is p to fp32's own 24 bits: two leave 2^-18, which moves one
 // output in some hundreds to the neighbouring bf16 value.  Every term of a
-// p > 0 is positive, so an infinite value comes out as that infinity.
+// p > 0 is positive, so an infinite value comes out as that infinity.  The
+// second product starts from zero in every tile and O takes it up by rounded
+// fused multiply-adds, which hold the softmax's rescaling too: accumulated by
+// the instruction itself, long contexts lost a bit of every step (24 of 8192
+// to 32768 tokens: 1000 of 196608 outputs not the nearest bf16 to the exact
+// result, now 80; the definition in fp32 321).  Four steps of the head go
+// together so that their chains overlap (256-wide heads 308 us, one by one 327;
+// with 16 heads a group two, 128 wide: 167 and 175).
 //
 // A call reads 512 bytes of cache per token and key/value head (128 wide) and
 // does 4096 flops on them for 8 heads: at memory speed that is some 55
@@ -165,6 +172,7 @@ struct MmaCore {
       }
     }
     uint32_t pt[BLOCKS][NT][2][3];  // P's terms
+    float2 kept[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float x[BLOCKS][4], keep[2];
@@ -203,29 +211,39 @@ struct MmaCore {
           for (int i = 0; i < 3; ++i) pt[j][n][e][i] = transpose_8x8(pt[j][n][e][i]);
         }
       }
-      if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
-#pragma unroll
-        for (int k = 0; k < KT; ++k) {
-          o[k][n][0] *= keep[0];
-          o[k][n][1] *= keep[1];
-          o[k][n][2] *= keep[0];
-          o[k][n][3] *= keep[1];
-        }
-      }
+      kept[n] = make_float2(keep[0], keep[1]);
     }
+    // The instruction cuts what it adds to an accumulator off instead of
+    // rounding it, so a tile's products are summed apart and join O rounded.
+    constexpr int KG = NT == 1 && KT >= 4 ? 4 : 2;  // steps of the head at a time
 #pragma unroll
-    for (int k = 0; k < KT; ++k) {
+    for (int k0 = 0; k0 < KT; k0 += KG) {
+      float now[KG][NT][4] = {};
 #pragma unroll
       for (int j = 0; j < BLOCKS; ++j) {
-        uint32_t a[4];
-        ldsm_x4_trans(vb + at(j * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), a[0], a[1],
-                      a[2], a[3]);
+        uint32_t a[KG][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int k = 0; k < KG; ++k)
+          ldsm_x4_trans(vb + at(j * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * (k0 + k) + ((lane >> 3) & 1)), a[k][0],
+                        a[k][1], a[k][2], a[k][3]);
 #pragma unroll
-          for (int i = 0; i < 3; ++i) mma_bf16_16816(o[k][n], a, pt[j][n][0][i], pt[j][n][1][i]);
-        }
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int k = 0; k < KG; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_bf16_16816(now[k][n], a[k], pt[j][n][0][i], pt[j][n][1][i]);
       }
+#pragma unroll
+      for (int k = 0; k < KG; ++k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const float2 sum = fma_f32x2(make_float2(o[k0 + k][n][e], o[k0 + k][n][e + 1]), kept[n],
+                                         make_float2(now[k][n][e], now[k][n][e + 1]));
+            o[k0 + k][n][e] = sum.x;
+            o[k0 + k][n][e + 1] = sum.y;
+          }
     }
   }
 

@@ -80,3 +80,33 @@ def test_infinite_values(dtype, H, Hk, hd, ps, n):
             out[0, :, d] = 0
             a["v"][0][:, :, d] = 0
     check_attention(a, out, lse, 1.0 / hd ** 0.5)
+
+
+@pytest.mark.parametrize("dtype,H,Hk,hd,ps,tile", [(BF, 8, 8, 32, 16, 32), (BF, 64, 8, 64, 16, 32),
+                                                   (BF, 32, 8, 128, 16, 16), (BF, 128, 8, 128, 8, 16),
+                                                   (F32, 8, 8, 64, 16, 16)])
+def test_long_sums_are_rounded(dtype, H, Hk, hd, ps, tile):
+    """The second half of a context has the first half's keys and the opposite values: the output is 0 but for what
+    the long sum loses.  One stream to a block, four warps, so a warp adds n / 4 tile tiles of which each has its
+    opposite.
+
+    Rounded sums: half an ulp, e |o|, a tile.  |o| rises to half the weight of all and falls again, a quarter of it on
+    average (4% more for the spread of the weights).  16 e for the sums within a tile and the joins.  Cut-off sums lose
+    an e |o| on average in each of two steps a tile, always to the same side."""
+    n, blocks = 16384, 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    B = blocks // Hk
+    g = torch.Generator().manual_seed(7)
+    k0 = torch.randn((B, n // 2, Hk), generator=g).to(dtype).cuda()
+    kc = torch.zeros((B * n // ps, ps, Hk, hd), dtype=dtype, device="cuda")
+    vc = torch.ones_like(kc)
+    kc.view(B, 2, n // 2, Hk, hd)[..., 0] = k0[:, None]
+    vc.view(B, 2, n // 2, Hk, hd)[:, 1] = -1
+    q = torch.zeros((B, H, hd), dtype=dtype, device="cuda")
+    q[:, :, 0] = 0.5
+    out = torch.full_like(q, float("nan"))
+    tables = torch.arange(B * n // ps, dtype=torch.int32, device="cuda").view(B, -1)
+    prob = lk.AttentionProblem(q=q, out=out, cache=lk.KVCache(kc, vc), block_tables=tables, scale=1.0,
+                               lengths=torch.full((B,), n, dtype=torch.int32, device="cuda"))
+    lk.lora_paged_attention(prob, lk.new_attention_workspace(prob))
+    worst = out.double().abs().max().item()
+    assert worst <= (0.26 * (n / (4 * tile)) + 16) * E * (1 + 2.0 ** -8), worst / E
