@@ -285,6 +285,8 @@ def prepare(case, seed):
         s["lse"] = torch.zeros(s["q"].shape[:2], device="cuda") if case["lse"] else None
         if own:
             import adapter_sgmv_lora_gb300 as lk
+            if s["masks"] is not None and case["pad"]:   # the library wants a mask row for each row of q
+                s["masks"] = torch.nn.functional.pad(s["masks"], (0, 0, 0, case["pad"]))
             s["problem"] = lk.TreeAttentionProblem(q=s["q"], out=s["out"], cache=lk.KVCache(s["kc"], s["vc"]),
                                                    block_tables=s["tables"], lengths=s["lengths"],
                                                    row_offsets=s["offsets"], masks=s["masks"], scale=s["scale"],
