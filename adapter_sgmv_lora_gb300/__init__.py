@@ -13,7 +13,9 @@ Names follow the C ABI: ``lora_build_routing``, ``lora_set_slot``,
 between the projections ``lora_build_rope``, ``lora_rope_append``,
 ``lora_attention_workspace_bytes``, ``lora_paged_attention``,
 ``lora_kv_copy_pages`` and the page bookkeeping ``lora_pages_*`` (class
-``Pages``).
+``Pages``); for the verification of drafted tokens ``lora_base_q4_apply``,
+``lora_build_tree``, ``lora_tree_attention_workspace_bytes``,
+``lora_tree_attention`` and ``lora_kv_keep_rows``.
 """
 from __future__ import annotations
 
@@ -43,6 +45,8 @@ PATH_PREP, PATH_BASE_GEMM = 0x80, 0x100
 PATH_ROPE, PATH_GENERIC_ROPE = 0x200, 0x400
 PATH_MMA_ATTENTION, PATH_GENERIC_ATTENTION, PATH_JOIN = 0x800, 0x1000, 0x2000
 PATH_PAGES = 0x4000
+PATH_MMA_Q4, PATH_TC_Q4, PATH_GENERIC_Q4 = 0x8000, 0x10000, 0x20000
+PATH_TC_TREE, PATH_GENERIC_TREE, PATH_KEEP = 0x40000, 0x80000, 0x100000
 MAX_SLICES = 3
 
 
@@ -99,6 +103,27 @@ class _Attention(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("q", _Heads), ("out", _Heads),
                 ("block_tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32),
                 ("lengths", ctypes.c_void_p), ("scale", ctypes.c_float), ("lse", ctypes.c_void_p)]
+
+
+class _TreeAttention(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_rows", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("q", _Heads), ("out", _Heads), ("block_tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int32), ("lengths", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p),
+                ("masks", ctypes.c_void_p), ("mask_words", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("lse", ctypes.c_void_p)]
+
+
+class _Keep(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("block_tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int32), ("lengths", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p),
+                ("path", ctypes.c_void_p), ("path_stride", ctypes.c_int64), ("max_kept", ctypes.c_int32),
+                ("new_lengths", ctypes.c_void_p)]
+
+
+class _Q4Weight(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("scale_row_stride", ctypes.c_int64), ("zeros", ctypes.c_void_p), ("zero_row_stride", ctypes.c_int64),
+                ("group_size", ctypes.c_int32)]
 
 
 class _Pages(ctypes.Structure):
@@ -170,6 +195,16 @@ def lib():
     L.lora_paged_attention.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]
     L.lora_kv_copy_pages.restype = ctypes.c_int
     L.lora_kv_copy_pages.argtypes = [vp, i32, vp, vp, i32, vp]
+    L.lora_base_q4_apply.restype = ctypes.c_int
+    L.lora_base_q4_apply.argtypes = [vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.lora_build_tree.restype = ctypes.c_int
+    L.lora_build_tree.argtypes = [i32, vp, i32, vp, vp]
+    L.lora_tree_attention_workspace_bytes.restype = ctypes.c_size_t
+    L.lora_tree_attention_workspace_bytes.argtypes = [vp, vp]
+    L.lora_tree_attention.restype = ctypes.c_int
+    L.lora_tree_attention.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]
+    L.lora_kv_keep_rows.restype = ctypes.c_int
+    L.lora_kv_keep_rows.argtypes = [vp, i32, vp, vp]
     pg = ctypes.POINTER(_Pages)
     L.lora_pages_init.restype = ctypes.c_int
     L.lora_pages_init.argtypes = [pg]
@@ -567,7 +602,7 @@ def _int32(name: str, t, shape) -> None:
     import torch
     if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
         raise ValueError("%s must be an int32 tensor of shape %s" % (name, tuple(shape)))
-    if t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1 and 0 not in t.shape:
         raise ValueError("%s must be contiguous along its last dimension" % name)
 
 
@@ -826,6 +861,228 @@ def lora_kv_copy_pages(caches: KVCaches, src, dst, stream=None) -> None:
     # As bytes: copying the list is cheaper than asking an array for its address.
     _check(lib().lora_kv_copy_pages(caches._ref, len(caches.layers), s.tobytes(), d.tobytes(), s.size,
                                     _stream_handle(stream)), "lora_kv_copy_pages")
+
+
+# ---------------------------------------- verification of drafted tokens --
+
+MAX_MASK_WORDS, MAX_KEPT = 16, 1024
+
+
+@dataclass(frozen=True)
+class Q4Weight:
+    """4-bit base weight of one slice: q uint8 [out, ceil(in / 2)] (input 2 i
+    in the low half of byte i), scales [out, groups] in the problem's dtype,
+    zeros uint8 [out, groups] (None: 8), group_size inputs a group."""
+    q: object
+    scales: object
+    group_size: int
+    zeros: object = None
+
+    def __post_init__(self):
+        import torch
+        for name, t in (("q", self.q), ("scales", self.scales), ("zeros", self.zeros)):
+            if t is None and name == "zeros":
+                continue
+            if t.dim() != 2 or t.shape[0] != self.q.shape[0] or (t.shape[1] > 1 and t.stride(1) != 1):
+                raise ValueError("%s must be 2-D [out, ...] with unit column stride" % name)
+            if name != "scales" and t.dtype != torch.uint8:
+                raise ValueError("%s must be uint8" % name)
+        _dtype_code(self.scales)
+        if self.zeros is not None and self.zeros.shape != self.scales.shape:
+            raise ValueError("zeros must have the shape of scales")
+        object.__setattr__(self, "group_size", _i32(self.group_size, "lora_base_q4_apply"))
+        if self.group_size < 1:
+            raise LoraError(2, "lora_base_q4_apply")
+        _on_cuda(q=self.q, scales=self.scales, zeros=self.zeros)
+
+
+@dataclass(frozen=True)
+class BaseQ4Problem:
+    """One lora_base_q4_apply call: a problem, its routing and a Q4Weight per
+    slice.  Routing(None, None, 0, 0) adds no adapter."""
+    problem: Problem
+    routing: Routing
+    weights: Sequence[Q4Weight]
+
+    def __post_init__(self):
+        object.__setattr__(self, "weights", tuple(self.weights))
+        x, slices = self.problem.x, self.problem.slices
+        if len(self.weights) != len(slices):
+            raise ValueError("one base weight per slice")
+        c, r = self.problem._c(), self.routing._c()
+        arr = (_Q4Weight * MAX_SLICES)()
+        rows = lambda t: t.stride(0) if t.shape[0] > 1 else t.shape[1]  # of one row any stride will do
+        for j, (w, s) in enumerate(zip(self.weights, slices)):
+            if w.scales.dtype != x.dtype:
+                raise ValueError("scales must have the dtype of x")
+            if w.q.shape != (s.out_dim, (x.shape[1] + 1) // 2):
+                raise ValueError("q must have shape [out, ceil(in / 2)]")
+            if w.scales.shape[1] != -(-x.shape[1] // w.group_size):
+                raise ValueError("scales must have ceil(in / group_size) columns")
+            _on_cuda(x=x, y=s.y, q=w.q)
+            arr[j] = _Q4Weight(w.q.data_ptr(), rows(w.q), w.scales.data_ptr(), rows(w.scales),
+                               w.zeros.data_ptr() if w.zeros is not None else None,
+                               rows(w.zeros) if w.zeros is not None else 0, w.group_size)
+        object.__setattr__(self, "_structs", (c, r, arr, self.routing._host_keep))  # what the structs point to
+        object.__setattr__(self, "_refs", tuple(ctypes.addressof(o) for o in (c, r, arr)))
+
+
+def _on_current(t) -> None:
+    """Launches go to the current device: the call's tensors must be there."""
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("the tensors are on %s, which is not the current device" % t.device)
+
+
+def _workspace(workspace, like):
+    _on_current(like)
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def lora_base_q4_apply(problem: BaseQ4Problem, workspace, stream=None) -> None:
+    """The base projection on 4-bit weights with the LoRA delta joined before
+    the one rounding (include/lora_sgmv.h); workspace as new_workspace makes it."""
+    ws, nbytes = _workspace(workspace, problem.problem.x)
+    _check(lib().lora_base_q4_apply(*problem._refs, ws, nbytes, _stream_handle(stream)), "lora_base_q4_apply")
+
+
+def lora_build_tree(parents, words: Optional[int] = None) -> dict:
+    """Masks and depths of a tree of drafted tokens (host; include/lora_sgmv.h):
+    parents[i] in [-1, i), -1 where node i hangs on the context's end.  {"masks":
+    uint64 [n, words] (words None: as few as hold n bits), "depths": int32 [n]}."""
+    par = np.asarray(parents)
+    if par.ndim != 1 or (par.size > 0 and par.dtype.kind not in "iu"):
+        raise ValueError("parents must be a list of integers")
+    if par.size > 0 and (par.min() < -1 or par.max() >= par.size):
+        raise LoraError(2, "lora_build_tree")
+    par = np.ascontiguousarray(par, dtype=np.int32)
+    words = max(1, -(-par.size // 64)) if words is None else _i32(words, "lora_build_tree")
+    if not 1 <= words <= MAX_MASK_WORDS:
+        raise LoraError(2, "lora_build_tree")
+    masks = np.zeros((par.size, words), dtype=np.uint64)
+    depths = np.zeros(par.size, dtype=np.int32)
+    _check(lib().lora_build_tree(par.size, par.ctypes.data, words, masks.ctypes.data, depths.ctypes.data),
+           "lora_build_tree")
+    return {"masks": masks, "depths": depths}
+
+
+@dataclass(frozen=True)
+class TreeAttentionProblem:
+    """One lora_tree_attention call: q and out [N, heads, head_dim] (out may be
+    q), block_tables int32 [B, max_pages], lengths int32 [B] (drafted tokens
+    included), row_offsets int32 [B + 1], masks int64 [N, words] holding the
+    uint64 bits of lora_build_tree (None: chains), scale (None: 1 /
+    sqrt(head_dim)), optionally lse float32 [N, heads]."""
+    q: object
+    out: object
+    cache: KVCache
+    block_tables: object
+    lengths: object
+    row_offsets: object
+    masks: object = None
+    scale: Optional[float] = None
+    lse: object = None
+
+    def __post_init__(self):
+        import torch
+        q, cc = self.q, self.cache._struct
+        if q.dim() != 3:
+            raise ValueError("q must be 3-D [rows, heads, head_dim]")
+        N, H, hd = q.shape
+        if hd != cc.head_dim:
+            raise ValueError("q must have the cache's head_dim")
+        _on_cuda(q=q, out=self.out, block_tables=self.block_tables, lengths=self.lengths,
+                 row_offsets=self.row_offsets, masks=self.masks, lse=self.lse, cache=self.cache.k)
+        if self.block_tables.dim() != 2:
+            raise ValueError("block_tables must be 2-D [sequences, max_pages]")
+        B, M = self.block_tables.shape
+        _int32("block_tables", self.block_tables, (B, M))
+        _int32("lengths", self.lengths, (B,))
+        _int32("row_offsets", self.row_offsets, (B + 1,))
+        words = 0
+        if self.masks is not None:
+            m = self.masks
+            if m.dtype not in (torch.int64, torch.uint64) or m.dim() != 2 or m.shape[0] != N or not m.is_contiguous():
+                raise ValueError("masks must be a contiguous int64 tensor [rows, words]")
+            words = m.shape[1]
+        if self.lse is not None and (self.lse.dtype != torch.float32 or tuple(self.lse.shape) != (N, H) or
+                                     not self.lse.is_contiguous()):
+            raise ValueError("lse must be a contiguous float32 [rows, heads] tensor")
+        scale = 1.0 / hd ** 0.5 if self.scale is None else float(self.scale)
+        dt = self.cache.k.dtype
+        ptr = lambda t: t.data_ptr() if t is not None else None
+        c = _TreeAttention(B, N, H, _heads("q", q, (N, H, hd), dt), _heads("out", self.out, (N, H, hd), dt),
+                           self.block_tables.data_ptr() or None, self.block_tables.stride(0) if B > 1 else M, M,
+                           self.lengths.data_ptr(), self.row_offsets.data_ptr(), ptr(self.masks), words, scale,
+                           ptr(self.lse))
+        object.__setattr__(self, "_struct", c)
+        object.__setattr__(self, "_ref", ctypes.addressof(c))
+
+
+def lora_tree_attention_workspace_bytes(problem: TreeAttentionProblem) -> int:
+    return int(lib().lora_tree_attention_workspace_bytes(problem._ref, problem.cache._ref))
+
+
+def new_tree_attention_workspace(problem: TreeAttentionProblem):
+    """A workspace tensor of lora_tree_attention_workspace_bytes(problem) bytes."""
+    import torch
+    nbytes = max(lora_tree_attention_workspace_bytes(problem), 256)
+    return torch.empty((nbytes + 15) // 16 * 4, dtype=torch.float32, device=problem.q.device)
+
+
+def lora_tree_attention(problem: TreeAttentionProblem, workspace, stream=None) -> None:
+    """Attention of drafted tokens to their context and their own branch over
+    the paged cache (include/lora_sgmv.h)."""
+    ws, nbytes = _workspace(workspace, problem.q)
+    _check(lib().lora_tree_attention(problem._ref, problem.cache._ref, ws, nbytes, _stream_handle(stream)),
+           "lora_tree_attention")
+
+
+@dataclass(frozen=True)
+class KeepRowsProblem:
+    """One lora_kv_keep_rows call: the layers' caches, block_tables, lengths and
+    row_offsets as of the tree attention, path int32 [B, max_kept] (ascending
+    drafted tokens, -1 ends a row), optionally new_lengths int32 [B]."""
+    caches: KVCaches
+    block_tables: object
+    lengths: object
+    row_offsets: object
+    path: object
+    new_lengths: object = None
+
+    def __post_init__(self):
+        if not self.caches.layers:
+            raise ValueError("caches must hold a layer")
+        _on_cuda(cache=self.caches.layers[0].k, block_tables=self.block_tables, lengths=self.lengths,
+                 row_offsets=self.row_offsets, path=self.path, new_lengths=self.new_lengths)
+        if self.block_tables.dim() != 2 or self.path.dim() != 2:
+            raise ValueError("block_tables and path must be 2-D")
+        B, M = self.block_tables.shape
+        K = self.path.shape[1]
+        _int32("block_tables", self.block_tables, (B, M))
+        _int32("lengths", self.lengths, (B,))
+        _int32("row_offsets", self.row_offsets, (B + 1,))
+        _int32("path", self.path, (B, K))
+        if self.new_lengths is not None:
+            _int32("new_lengths", self.new_lengths, (B,))
+        c = _Keep(B, self.block_tables.data_ptr() or None, self.block_tables.stride(0) if B > 1 else M, M,
+                  self.lengths.data_ptr(), self.row_offsets.data_ptr(), self.path.data_ptr() or None,
+                  self.path.stride(0) if B > 1 else K, K,
+                  self.new_lengths.data_ptr() if self.new_lengths is not None else None)
+        object.__setattr__(self, "_struct", c)
+        object.__setattr__(self, "_ref", ctypes.addressof(c))
+
+
+def lora_kv_keep_rows(problem: KeepRowsProblem, stream=None) -> None:
+    """Move the accepted drafted tokens' cache rows up behind the context, in
+    every layer (include/lora_sgmv.h)."""
+    _on_current(problem.caches.layers[0].k)
+    _check(lib().lora_kv_keep_rows(problem.caches._ref, len(problem.caches.layers), problem._ref,
+                                   _stream_handle(stream)), "lora_kv_keep_rows")
 
 
 class Pages:

@@ -421,6 +421,59 @@ extern "C" lora_status_t lora_base_gemm_apply(const lora_problem_t* problem, con
   return cuda_status(launch_base_gemm_simple(d, wts, u, !noop, s));
 }
 
+extern "C" lora_status_t lora_base_q4_apply(const lora_problem_t* problem, const lora_routing_t* routing,
+                                            const lora_q4_weight_t* base, void* workspace, size_t workspace_bytes,
+                                            lora_stream_t stream) {
+  begin_call();
+  lora_status_t st = validate_problem(problem);
+  if (st != LORA_OK) return st;
+  if ((st = validate_routing(problem, routing)) != LORA_OK) return st;
+  if (routing->token_rows) return LORA_ERR_SHAPE;  // rows must be in sorted order
+  if (!base) return LORA_ERR_NULL;
+  Q4Weights wts{};
+  for (int j = 0; j < problem->num_slices; ++j) {
+    const lora_q4_weight_t& b = base[j];
+    if (!b.q || !b.scales) return LORA_ERR_NULL;
+    if (b.group_size < 1) return LORA_ERR_SHAPE;
+    const int64_t group = b.group_size < problem->in_dim ? b.group_size : problem->in_dim;
+    const int64_t groups = (problem->in_dim + group - 1) / group;
+    if (b.q_row_stride < ((int64_t)problem->in_dim + 1) / 2 || b.scale_row_stride < groups ||
+        (b.zeros && b.zero_row_stride < groups))
+      return LORA_ERR_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(b.scales) & (problem->dtype == LORA_DTYPE_BF16 ? 1u : 3u)) != 0)
+      return LORA_ERR_ALIGN;
+    wts.w[j] = Q4Desc{b.q,     (long long)b.q_row_stride,    b.scales,  (long long)b.scale_row_stride,
+                      b.zeros, (long long)b.zero_row_stride, (int)group};
+  }
+  if (problem->num_tokens == 0) return LORA_OK;
+  const bool noop = is_noop(routing);
+  if (!noop && (!workspace || workspace_bytes < ws_bytes(problem, routing->end))) return LORA_ERR_WORKSPACE;
+  if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return LORA_ERR_ALIGN;
+  ProblemDesc d = make_desc(problem, routing);
+  if (!d.status) return LORA_ERR_CUDA;
+  if (noop) {  // base rows only: no groups to add
+    d.G = 0;
+    d.end = 0;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  float* u = static_cast<float*>(workspace);
+  int nsplit = noop ? 0 : 1;
+  if (!noop) {
+    cudaError_t e = cudaErrorNotSupported;
+    const bool fast = fast_path_ok(d, u) && q4_fast_ok(d, wts);  // the generic kernel takes one plane of u
+    if (fast && tc_shrink_ok(d)) {
+      nsplit = tc_shrink_splits(d.end, d.in_dim, device_sm_count());
+      e = launch_tc_shrink(d, u, s, nsplit);
+    }
+    if (e == cudaErrorNotSupported) {
+      nsplit = fast ? apply_splits_for(d) : 1;
+      e = fast ? launch_shrink_partial_bf16(d, u, s) : launch_shrink_simple(d, u, s);
+    }
+    if ((st = cuda_status(e)) != LORA_OK) return st;
+  }
+  return cuda_status(q4_fast_ok(d, wts) ? launch_q4(d, wts, u, nsplit, !noop, s) : launch_q4_simple(d, wts, u, s));
+}
+
 extern "C" lora_status_t lora_selftest_wait_timeout(uint32_t polls, lora_stream_t stream) {
   begin_call();
   unsigned* p = status_ptr();

@@ -1,6 +1,6 @@
 // attention_api.cu -- the extern "C" entry points between the projections
-// (rotation + cache append, paged attention, page copies): argument
-// validation and dispatch.  The host bookkeeping of pages is in pages.cpp.
+// (rotation + cache append, paged attention, tree attention, page copies, kept
+// rows): argument validation and dispatch.  The host bookkeeping of pages is in pages.cpp.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -82,6 +82,11 @@ CacheDesc cache_desc(const lora_kv_cache_t* c) {
           c->num_pages,   c->page_size, c->num_kv_heads,           c->head_dim};
 }
 
+// A token's number plus a tile stays within 32 bits.
+int max_length(int32_t max_pages, const lora_kv_cache_t* c) {
+  return (int)std::min<int64_t>((int64_t)max_pages * c->page_size, INT32_MAX - 256);
+}
+
 lora_status_t validate_attention(const lora_attention_t* a, const lora_kv_cache_t* c) {
   if (!a) return LORA_ERR_NULL;
   lora_status_t st = validate_cache(c);
@@ -109,8 +114,7 @@ AttnDesc attention_desc(const lora_attention_t* a, const lora_kv_cache_t* c) {
   d.tables = a->block_tables;
   d.table_stride = (long long)a->table_stride;
   d.max_pages = a->max_pages;
-  // A token's number plus a tile stays within 32 bits.
-  d.max_len = (int)std::min<int64_t>((int64_t)a->max_pages * c->page_size, INT32_MAX - 256);
+  d.max_len = max_length(a->max_pages, c);
   d.lengths = a->lengths;
   d.scale = a->scale;
   d.lse = a->lse;
@@ -140,6 +144,68 @@ lora_status_t check_copies(const int32_t* src, const int32_t* dst, int32_t n, in
   }
   std::free(mark);
   return st;
+}
+
+// A list of layers' caches: one geometry and type.
+lora_status_t validate_layers(const lora_kv_cache_t* caches, int32_t num_caches) {
+  lora_status_t st;
+  if ((st = validate_cache(&caches[0])) != LORA_OK) return st;
+  for (int32_t i = 1; i < num_caches; ++i) {
+    const lora_kv_cache_t &a = caches[i], &b = caches[0];
+    const bool same = a.num_pages == b.num_pages && a.page_size == b.page_size && a.num_kv_heads == b.num_kv_heads &&
+                      a.head_dim == b.head_dim && a.page_stride == b.page_stride &&
+                      a.token_stride == b.token_stride && a.head_stride == b.head_stride;
+    // A layer like the first has its pointers left to check.
+    if (same && a.dtype == b.dtype && a.k && a.v && aligned(a.k, elem_bytes(a.dtype)) &&
+        aligned(a.v, elem_bytes(a.dtype)))
+      continue;
+    if ((st = validate_cache(&a)) != LORA_OK) return st;
+    return a.dtype != b.dtype ? LORA_ERR_DTYPE : LORA_ERR_SHAPE;
+  }
+  return LORA_OK;
+}
+
+lora_status_t validate_tree(const lora_tree_attention_t* a, const lora_kv_cache_t* c) {
+  if (!a) return LORA_ERR_NULL;
+  lora_status_t st = validate_cache(c);
+  if (st != LORA_OK) return st;
+  if (a->num_seqs < 0 || a->num_rows < 0 || a->num_heads < 1 || a->num_heads % c->num_kv_heads != 0)
+    return LORA_ERR_SHAPE;
+  if ((int64_t)a->num_rows * a->num_heads > INT32_MAX / 4 || a->num_seqs > INT32_MAX / 4 / a->num_heads)
+    return LORA_ERR_SHAPE;  // streams are counted in 32 bits
+  if (a->max_pages < 0 || a->table_stride < 0 || (a->num_seqs > 1 && a->table_stride < a->max_pages))
+    return LORA_ERR_SHAPE;
+  if (a->masks && (a->mask_words < 1 || a->mask_words > LORA_MAX_MASK_WORDS)) return LORA_ERR_SHAPE;
+  if (a->num_seqs == 0 || a->num_rows == 0) return LORA_OK;  // nothing is read or written
+  if ((st = validate_input(a->q, c->dtype)) != LORA_OK) return st;
+  if ((st = validate_output(a->out, a->q, a->num_rows, a->num_heads, c->head_dim, c->dtype)) != LORA_OK) return st;
+  if (!a->lengths || !a->row_offsets || (a->max_pages > 0 && !a->block_tables)) return LORA_ERR_NULL;
+  if (!aligned(a->lengths, 4) || !aligned(a->row_offsets, 4) || !aligned(a->block_tables, 4) || !aligned(a->lse, 4) ||
+      !aligned(a->masks, 8))
+    return LORA_ERR_ALIGN;
+  return LORA_OK;
+}
+
+TreeDesc tree_desc(const lora_tree_attention_t* a, const lora_kv_cache_t* c) {
+  TreeDesc d{};
+  d.dtype = c->dtype;
+  d.num_seqs = a->num_seqs;
+  d.num_rows = a->num_rows;
+  d.num_heads = a->num_heads;
+  d.group = a->num_heads / c->num_kv_heads;
+  d.q = heads(a->q);
+  d.out = heads(a->out);
+  d.cache = cache_desc(c);
+  d.tables = a->block_tables;
+  d.table_stride = (long long)a->table_stride;
+  d.max_len = max_length(a->max_pages, c);
+  d.lengths = a->lengths;
+  d.offsets = a->row_offsets;
+  d.masks = reinterpret_cast<const unsigned long long*>(a->masks);
+  d.words = a->mask_words;
+  d.scale = a->scale;
+  d.lse = a->lse;
+  return d;
 }
 
 }  // namespace
@@ -231,21 +297,66 @@ extern "C" lora_status_t lora_kv_copy_pages(const lora_kv_cache_t* caches, int32
   if (num_caches == 0) return LORA_OK;
   if (!caches || (num_copies > 0 && (!src || !dst))) return LORA_ERR_NULL;
   lora_status_t st;
-  if ((st = validate_cache(&caches[0])) != LORA_OK) return st;
-  for (int32_t i = 1; i < num_caches; ++i) {
-    const lora_kv_cache_t &a = caches[i], &b = caches[0];
-    const bool same = a.num_pages == b.num_pages && a.page_size == b.page_size && a.num_kv_heads == b.num_kv_heads &&
-                      a.head_dim == b.head_dim && a.page_stride == b.page_stride &&
-                      a.token_stride == b.token_stride && a.head_stride == b.head_stride;
-    // A layer like the first has its pointers left to check.
-    if (same && a.dtype == b.dtype && a.k && a.v && aligned(a.k, elem_bytes(a.dtype)) &&
-        aligned(a.v, elem_bytes(a.dtype)))
-      continue;
-    if ((st = validate_cache(&a)) != LORA_OK) return st;
-    return a.dtype != b.dtype ? LORA_ERR_DTYPE : LORA_ERR_SHAPE;
-  }
+  if ((st = validate_layers(caches, num_caches)) != LORA_OK) return st;
   if ((st = check_copies(src, dst, num_copies, caches[0].num_pages)) != LORA_OK) return st;
   if (num_copies == 0) return LORA_OK;
   return cuda_status(launch_copy_pages(cache_desc(&caches[0]), caches[0].dtype, caches, num_caches, src, dst,
                                        num_copies, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t lora_tree_attention_workspace_bytes(const lora_tree_attention_t* attention,
+                                                      const lora_kv_cache_t* cache) {
+  if (validate_tree(attention, cache) != LORA_OK || attention->num_seqs == 0 || attention->num_rows == 0) return 0;
+  return tree_workspace_bytes(tree_desc(attention, cache));
+}
+
+extern "C" lora_status_t lora_tree_attention(const lora_tree_attention_t* attention, const lora_kv_cache_t* cache,
+                                             void* workspace, size_t workspace_bytes, lora_stream_t stream) {
+  begin_call();
+  const lora_status_t st = validate_tree(attention, cache);
+  if (st != LORA_OK) return st;
+  if (attention->num_seqs == 0 || attention->num_rows == 0) return LORA_OK;
+  TreeDesc d = tree_desc(attention, cache);
+  if (!workspace || workspace_bytes < tree_workspace_bytes(d)) return LORA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return LORA_ERR_ALIGN;
+  if (!(d.status = status_ptr())) return LORA_ERR_CUDA;
+  return cuda_status(launch_tree(d, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" lora_status_t lora_kv_keep_rows(const lora_kv_cache_t* caches, int32_t num_caches, const lora_keep_t* keep,
+                                           lora_stream_t stream) {
+  begin_call();
+  if (!keep || !caches) return LORA_ERR_NULL;
+  if (num_caches < 1 || keep->num_seqs < 0 || keep->max_pages < 0 || keep->table_stride < 0 || keep->max_kept < 0 ||
+      keep->max_kept > LORA_MAX_KEPT || keep->path_stride < 0)
+    return LORA_ERR_SHAPE;
+  if (keep->num_seqs > 1 && (keep->table_stride < keep->max_pages || keep->path_stride < keep->max_kept))
+    return LORA_ERR_SHAPE;
+  const lora_status_t st = validate_layers(caches, num_caches);
+  if (st != LORA_OK) return st;
+  if (keep->num_seqs == 0) return LORA_OK;
+  if (!keep->lengths || !keep->row_offsets || (keep->max_pages > 0 && !keep->block_tables) ||
+      (keep->max_kept > 0 && !keep->path))
+    return LORA_ERR_NULL;
+  if (!aligned(keep->lengths, 4) || !aligned(keep->row_offsets, 4) || !aligned(keep->block_tables, 4) ||
+      !aligned(keep->path, 4) || !aligned(keep->new_lengths, 4))
+    return LORA_ERR_ALIGN;
+  if (keep->new_lengths) {  // other blocks still read the lengths when the new ones are written
+    const uintptr_t a = reinterpret_cast<uintptr_t>(keep->lengths), b = reinterpret_cast<uintptr_t>(keep->new_lengths);
+    if ((a > b ? a - b : b - a) < (uintptr_t)keep->num_seqs * 4) return LORA_ERR_SHAPE;
+  }
+  KeepDesc d{};
+  d.cache = cache_desc(&caches[0]);
+  d.tables = keep->block_tables;
+  d.table_stride = (long long)keep->table_stride;
+  d.max_len = max_length(keep->max_pages, &caches[0]);
+  d.lengths = keep->lengths;
+  d.offsets = keep->row_offsets;
+  d.path = keep->path;
+  d.path_stride = (long long)keep->path_stride;
+  d.num_seqs = keep->num_seqs;
+  d.max_kept = keep->max_kept;
+  d.new_lengths = keep->new_lengths;
+  if (!(d.status = status_ptr())) return LORA_ERR_CUDA;
+  return cuda_status(launch_keep_rows(d, caches[0].dtype, caches, num_caches, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -252,4 +252,74 @@ cudaError_t launch_attention(const AttnDesc& p, void* workspace, cudaStream_t s)
 cudaError_t launch_copy_pages(const CacheDesc& geometry, int dtype, const lora_kv_cache_t* caches, int num_caches,
                               const int* src, const int* dst, int n, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Verifying drafted tokens (attention_api.cu and api.cu validate and call).
+
+// A validated lora_tree_attention call.
+struct TreeDesc {
+  int dtype, num_seqs, num_rows, num_heads, group;  // group: query heads per key/value head
+  HeadsDesc q, out;
+  CacheDesc cache;
+  const int* tables;
+  long long table_stride;
+  int max_len;  // max_pages * page_size, or a little below INT_MAX
+  const int* lengths;
+  const int* offsets;
+  const unsigned long long* masks;  // nullptr: chains
+  int words;
+  float scale;
+  float* lse;  // or nullptr
+  unsigned* status;
+  // Filled in by the launcher: pieces of the line; value parts that a head is
+  // taken in; token / page_size is token * page_magic >> page_shift for tokens
+  // below 2^31; the workspace's parts.
+  int pieces, parts;
+  unsigned page_magic;
+  int page_shift;
+  int4* splits;    // [pieces] the stream that piece u begins and others go on with
+  float2* stats;   // [2 * pieces, rows of a chunk] maximum and sum of a partial result
+  float* partial;  // [2 * pieces] its unnormalised output
+};
+size_t tree_workspace_bytes(const TreeDesc& p);
+cudaError_t launch_tree(const TreeDesc& p, void* workspace, cudaStream_t s);
+
+// A validated lora_kv_keep_rows call.
+struct KeepDesc {
+  CacheDesc cache;  // geometry; k and v of each layer travel apart
+  const int* tables;
+  long long table_stride;
+  int max_len;
+  const int* lengths;
+  const int* offsets;
+  const int* path;
+  long long path_stride;
+  int num_seqs, max_kept;
+  int* new_lengths;
+  unsigned* status;
+};
+cudaError_t launch_keep_rows(const KeepDesc& p, int dtype, const lora_kv_cache_t* caches, int num_caches,
+                             cudaStream_t s);
+
+// 4-bit base weights of the slices (lora_q4_weight_t).
+struct Q4Desc {
+  const uint8_t* q;
+  long long q_stride;
+  const void* scales;
+  long long s_stride;
+  const uint8_t* zeros;  // nullptr: 8
+  long long z_stride;
+  int group;  // at most in_dim
+};
+struct Q4Weights {
+  Q4Desc w[LORA_MAX_SLICES];
+};
+// Whether the tensor-core kernels take the shapes (the problem's own
+// fast_path_ok is asked apart).
+bool q4_fast_ok(const ProblemDesc& p, const Q4Weights& w);
+// u: nsplit fp32 planes from a shrink launched just before (after_shrink), or
+// unused when end == 0.
+cudaError_t launch_q4(const ProblemDesc& p, const Q4Weights& w, const float* u, int nsplit, bool after_shrink,
+                      cudaStream_t s);
+cudaError_t launch_q4_simple(const ProblemDesc& p, const Q4Weights& w, const float* u, cudaStream_t s);
+
 }  // namespace lora

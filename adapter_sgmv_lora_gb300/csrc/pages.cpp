@@ -1,6 +1,7 @@
 // pages.cpp -- host side of the paged cache: the frequency table of the
-// position rotation (lora_build_rope) and the bookkeeping of a cache's pages
-// (lora_pages_*) in arrays that the caller owns.  Nothing here allocates, so
+// position rotation (lora_build_rope), the masks of a tree of drafted tokens
+// (lora_build_tree) and the bookkeeping of a cache's pages (lora_pages_*) in
+// arrays that the caller owns.  Nothing here allocates, so
 // nothing here can throw.
 #include <climits>
 #include <cmath>
@@ -52,6 +53,24 @@ extern "C" lora_status_t lora_build_rope(int32_t rotary_dim, double theta, lora_
     double t = scaled[i] / kTwoPi;
     t -= std::floor(t);  // [0, 1]: a tiny negative turn rounds up to 1, the same angle as 0
     turns[i] = t < 1.0 ? static_cast<uint64_t>(std::ldexp(t, 64)) : 0;
+  }
+  return LORA_OK;
+}
+
+extern "C" lora_status_t lora_build_tree(int32_t num_nodes, const int32_t* parents, int32_t mask_words,
+                                         uint64_t* masks, int32_t* depths) {
+  if (num_nodes < 0 || mask_words < 1 || mask_words > LORA_MAX_MASK_WORDS || num_nodes > 64 * mask_words)
+    return LORA_ERR_SHAPE;
+  if (num_nodes > 0 && !parents) return LORA_ERR_NULL;
+  for (int32_t i = 0; i < num_nodes; ++i)
+    if (parents[i] < -1 || parents[i] >= i) return LORA_ERR_SHAPE;
+  for (int32_t i = 0; i < num_nodes; ++i) {
+    const int32_t p = parents[i];
+    if (depths) depths[i] = p < 0 ? 0 : depths[p] + 1;
+    if (!masks) continue;
+    uint64_t* row = masks + (int64_t)i * mask_words;
+    for (int32_t w = 0; w < mask_words; ++w) row[w] = p < 0 ? 0 : masks[(int64_t)p * mask_words + w];
+    row[i >> 6] |= 1ull << (i & 63);
   }
   return LORA_OK;
 }

@@ -366,6 +366,47 @@ lora_status_t lora_base_gemm_apply(const lora_problem_t* problem, const lora_rou
                                    const lora_base_weight_t* base, void* workspace, size_t workspace_bytes,
                                    lora_stream_t stream);
 
+/*
+ * 4-bit base projection weight of one slice, W0 [out_dim, in_dim]:
+ *   W0[o, i] = scales[o, i / group_size] * (code[o, i] - zeros[o, i / group_size])
+ * code[o, i], 0..15, is the low half of byte q[o*q_row_stride + i / 2] for an
+ * even i and its high half for an odd one; scales has the problem's storage
+ * type (row stride in elements), zeros bytes of 0..255 (NULL: 8 everywhere).
+ * A row has ceil(in_dim / group_size) groups, the last one maybe short; a
+ * group_size of in_dim or more is one group a row.
+ */
+typedef struct {
+  const uint8_t* q;
+  int64_t q_row_stride;
+  const void* scales;
+  int64_t scale_row_stride;
+  const uint8_t* zeros;
+  int64_t zero_row_stride;
+  int32_t group_size;
+} lora_q4_weight_t;
+
+/*
+ * lora_base_q4_apply -- lora_base_gemm_apply on 4-bit base weights, for the
+ * few rows of a decode or verification step (any number is taken; W0 is
+ * unpacked anew for every 128 rows):
+ *   y_j[t, o] = rn( sum_i W0_j[o, i] x[t, i]
+ *                   + [t < end] (bias_j[s, o] + sum_k B_j[s, o, k] u[t, j*R + k]) )
+ * for every row t < num_tokens, y written and never read, one rounding.  A
+ * weight is never rounded to the storage type: codes less their zero are exact
+ * in the products, a group's sum is fp32 and takes its scale there.
+ * base[num_slices] gives each slice's W0 (DEVICE).  workspace as for
+ * lora_base_gemm_apply; token_rows is refused likewise.
+ * Kernels: bf16 fast-path shapes with group sizes of a multiple of 32 (or one
+ * group a row), q on 16-byte boundaries and scales on their own run on the
+ * tensor cores; others on a generic kernel.
+ * Errors: as lora_base_gemm_apply (LORA_ERR_SHAPE also for a group_size < 1 or
+ * row strides below the row's bytes or groups; LORA_ERR_ALIGN for scales off
+ * their element's boundary).
+ */
+lora_status_t lora_base_q4_apply(const lora_problem_t* problem, const lora_routing_t* routing,
+                                 const lora_q4_weight_t* base, void* workspace, size_t workspace_bytes,
+                                 lora_stream_t stream);
+
 /* ==========================================================================
  * Attention between the projections: what a served layer does with the
  * q/k/v rows that lora_sgmv_apply or lora_base_gemm_apply leaves, before the
@@ -532,6 +573,109 @@ size_t lora_attention_workspace_bytes(const lora_attention_t* attention, const l
 lora_status_t lora_paged_attention(const lora_attention_t* attention, const lora_kv_cache_t* cache,
                                    void* workspace, size_t workspace_bytes, lora_stream_t stream);
 
+/* Most 64-bit words of a tree mask row. */
+#define LORA_MAX_MASK_WORDS 16
+
+/*
+ * lora_build_tree -- HOST ONLY.  The mask and depth of each node of a tree of
+ * drafted tokens: parents[i] in [-1, i) (-1: the node hangs on the context's
+ * end).  masks[i * mask_words + w], bit j: node 64 w + j is i itself or one of
+ * its ancestors.  depths[i]: ancestors of i, so the token's position is the
+ * context's length plus depths[i].  Either output may be NULL.  Errors:
+ * LORA_ERR_NULL, LORA_ERR_SHAPE (num_nodes < 0, a parent out of range,
+ * mask_words not in [1, LORA_MAX_MASK_WORDS] or too few for num_nodes).
+ */
+lora_status_t lora_build_tree(int32_t num_nodes, const int32_t* parents, int32_t mask_words, uint64_t* masks,
+                              int32_t* depths);
+
+/* One lora_tree_attention call; every pointer is DEVICE memory.  Sequence b
+ * has the rows row_offsets[b] to row_offsets[b + 1] - 1 of q and out, one for
+ * each of its drafted tokens, whose keys and values are the last tokens of its
+ * lengths[b] cached ones, in the same order.  What is cached before them is
+ * its context. */
+typedef struct {
+  int32_t num_seqs;
+  int32_t num_rows;   /* rows of q, out, masks and lse; those behind the last sequence's are left as they were */
+  int32_t num_heads;  /* a multiple of the cache's num_kv_heads */
+  lora_heads_t q;     /* the cache's type */
+  lora_heads_t out;   /* the cache's type; may be q itself */
+  const int32_t* block_tables; /* row b lists the pages of sequence b in order */
+  int64_t table_stride;
+  int32_t max_pages;
+  const int32_t* lengths;     /* [num_seqs]: cached tokens, the drafted ones included */
+  const int32_t* row_offsets; /* [num_seqs + 1], not decreasing, within [0, num_rows] */
+  const uint64_t* masks;      /* [num_rows, mask_words]: bit j of a row names drafted token j of its sequence;
+                                 NULL: a chain, row i sees drafted tokens 0..i */
+  int32_t mask_words;         /* 1..LORA_MAX_MASK_WORDS; not read without masks */
+  float scale;
+  float* lse;                 /* optional [num_rows, num_heads] */
+} lora_tree_attention_t;
+
+/* DEVICE workspace of lora_tree_attention.  Depends on shapes only; 0 for
+ * arguments that the call would refuse. */
+size_t lora_tree_attention_workspace_bytes(const lora_tree_attention_t* attention, const lora_kv_cache_t* cache);
+
+/*
+ * lora_tree_attention -- attention of the drafted tokens of each sequence to
+ * its context and to the drafted tokens that each one's mask names:
+ * out_h = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q_h . k_j) over what the
+ * row sees.  Mask bits of tokens that the sequence does not have are ignored.
+ * A row that sees nothing, or whose every score is -inf, gives out = 0 and
+ * lse = -inf.  What a row does not see has no part in it, be it infinite or
+ * NaN.  Scores, softmax sums and the output's accumulation are fp32; on the
+ * tensor-core path (bf16; rows of cache, q and out on 16-byte boundaries) the
+ * probabilities enter the product with V as two bf16 terms, 16 bits.  A
+ * sequence without rows reads nothing.  A length below the sequence's rows or
+ * above max_pages * page_size, or more rows than the masks have bits, raises
+ * LORA_DEV_BAD_LENGTH, a used page id outside the cache LORA_DEV_BAD_PAGE; that
+ * sequence's rows of out and lse are left as they were, the others are
+ * computed.  Row offsets that decrease or leave [0, num_rows] raise
+ * LORA_DEV_BAD_OFFSETS and nothing is computed.  The same arguments give the
+ * same bits on the same GPU.
+ * workspace: >= lora_tree_attention_workspace_bytes, 16-byte aligned, contents
+ * on entry ignored; two calls that may overlap need two.
+ * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_SHAPE, LORA_ERR_WORKSPACE,
+ * LORA_ERR_ALIGN.
+ */
+lora_status_t lora_tree_attention(const lora_tree_attention_t* attention, const lora_kv_cache_t* cache,
+                                  void* workspace, size_t workspace_bytes, lora_stream_t stream);
+
+/* Most entries of a path of lora_kv_keep_rows. */
+#define LORA_MAX_KEPT 1024
+
+/* One lora_kv_keep_rows call; every pointer is DEVICE memory.  block_tables,
+ * lengths and row_offsets as in lora_tree_attention_t. */
+typedef struct {
+  int32_t num_seqs;
+  const int32_t* block_tables;
+  int64_t table_stride;
+  int32_t max_pages;
+  const int32_t* lengths;
+  const int32_t* row_offsets;
+  const int32_t* path;  /* [num_seqs, max_kept]: the drafted tokens to keep, ascending; -1 ends a row */
+  int64_t path_stride;
+  int32_t max_kept;     /* 0..LORA_MAX_KEPT */
+  int32_t* new_lengths; /* optional [num_seqs]: context + kept tokens; must not overlap lengths */
+} lora_keep_t;
+
+/*
+ * lora_kv_keep_rows -- after a verification: in every one of num_caches caches
+ * (the layers of a model: same geometry and type) the K and V of drafted token
+ * path[b][k] of sequence b become those of its cached token context + k, for
+ * every k before the row's first -1, as if all were read before any is
+ * written.  The sequence then has new_lengths[b] tokens; what its pages hold
+ * behind them is unspecified (lora_pages_trim gives the pages back).  Copies
+ * are exact, gaps between strided rows are not touched.  Pages that are
+ * written must not be shared (lora_pages_append saw to that).  A length or
+ * offsets as refused by lora_tree_attention raise LORA_DEV_BAD_LENGTH, a path
+ * that does not ascend or names a token that the sequence does not have
+ * LORA_DEV_BAD_ROW, a used page outside the cache LORA_DEV_BAD_PAGE; that
+ * sequence and its new length are left as they were.
+ * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_SHAPE, LORA_ERR_ALIGN.
+ */
+lora_status_t lora_kv_keep_rows(const lora_kv_cache_t* caches, int32_t num_caches, const lora_keep_t* keep,
+                                lora_stream_t stream);
+
 /*
  * lora_kv_copy_pages -- K and V of page dst[i] become those of page src[i],
  * for every i < num_copies and every one of num_caches caches (the layers of
@@ -627,6 +771,12 @@ lora_status_t lora_get_device_status(lora_stream_t stream, uint32_t* flags);
 #define LORA_PATH_GENERIC_ATTENTION 0x1000u /* paged attention in fp32 arithmetic */
 #define LORA_PATH_JOIN 0x2000u         /* join of the contexts that CTAs shared */
 #define LORA_PATH_PAGES 0x4000u        /* page copies */
+#define LORA_PATH_MMA_Q4 0x8000u       /* 4-bit base projection on mma.sync */
+#define LORA_PATH_TC_Q4 0x10000u       /* 4-bit base projection on tcgen05 */
+#define LORA_PATH_GENERIC_Q4 0x20000u  /* 4-bit base projection in fp32 arithmetic */
+#define LORA_PATH_TC_TREE 0x40000u     /* tree attention on tcgen05 (bf16) */
+#define LORA_PATH_GENERIC_TREE 0x80000u /* tree attention in fp32 arithmetic */
+#define LORA_PATH_KEEP 0x100000u       /* kept cache rows */
 
 /*
  * lora_last_call_path -- the OR of LORA_PATH_* bits of the kernels launched
