@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -199,6 +200,14 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2)
   }
   __syncthreads();
   const bool far = s_far != 0;
+  // The slots' B rows of these outputs are wanted at the end: into L2 now.
+  const bool wide_b = p.R % 8 == 0 && ((reinterpret_cast<uintptr_t>(sl.B) | (uintptr_t)(sl.B_slot_stride * 2)) & 15) == 0;
+  for (int r = warp; r < TN; r += kMmaWarps)
+    if (s_slot[r] >= 0 && (r == 0 || s_slot[r] != s_slot[r - 1])) {
+      const char* b = static_cast<const char*>(sl.B) + (s_slot[r] * sl.B_slot_stride + (long long)o0 * p.R) * 2;
+      const int bytes = min(kMmaOuts, sl.out_dim - o0) * p.R * 2;
+      for (int e = lane * 128; e < bytes; e += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + e));
+    }
   float y[MW][NT][4] = {};
   // Rows of x past the batch's last count as zero.
   const T* xrow[NT];
@@ -288,9 +297,25 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2)
   __syncthreads();
   if (!w.wait_first) pdl_wait();  // u comes from the shrink
   if (!s_ok) return;
-  for (int e = threadIdx.x; e < kMmaOuts * TN; e += kMmaWarps * 32) {
-    const int o = e % kMmaOuts, r = e / kMmaOuts, row = t0 + r;
-    if (row >= p.num_tokens || o0 + o >= sl.out_dim) continue;
+  // The delta, on the CUDA cores: a lane is an output, a warp takes every
+  // eighth row; u's planes are summed into shared memory first.
+  float* s_u = s_sum + kMmaWarps * kMmaOuts * SUM_PITCH;  // [TN][R]
+  const int routed = min(max(p.end - t0, 0), TN);
+  if (routed > 0) {
+    const float* ur = u + ((long long)t0 * p.n_slices + j) * p.R;
+    for (int e = threadIdx.x; e < routed * p.R; e += kMmaWarps * 32) {
+      const int r = e / p.R, k = e - r * p.R;
+      const float* at = ur + (long long)r * p.n_slices * p.R + k;
+      float v = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < w.nsplit; ++c) v += __ldcg(at + c * w.plane_stride);
+      s_u[e] = v;
+    }
+    __syncthreads();
+  }
+  const int o = lane;
+  if (o0 + o >= sl.out_dim) return;
+  for (int r = warp; r < TN && t0 + r < p.num_tokens; r += kMmaWarps) {
     float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < kMmaWarps; ++v) sum += s_sum[(v * kMmaOuts + o) * SUM_PITCH + r];
@@ -298,16 +323,405 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2)
     if (slot >= 0) {
       const int kmax = slot_kmax(p, slot);
       const T* b = static_cast<const T*>(sl.B) + slot * sl.B_slot_stride + (long long)(o0 + o) * p.R;
-      const float* ur = u + ((long long)row * p.n_slices + j) * p.R;
-      for (int k = 0; k < kmax; ++k) {
-        float v = 0.f;
-        for (int c = 0; c < w.nsplit; ++c) v += ur[c * w.plane_stride + k];
-        sum = fmaf(value(b[k]), v, sum);
+      const float* ur = s_u + r * p.R;
+      int k = 0;
+      if (wide_b) {
+#pragma unroll 2
+        for (; k + 8 <= kmax; k += 8) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(b + k));
+          const uint32_t bits[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum = fmaf(__uint_as_float(bits[e] << 16), ur[k + 2 * e], sum);
+            sum = fmaf(__uint_as_float(bits[e] & 0xffff0000u), ur[k + 2 * e + 1], sum);
+          }
+        }
       }
+      for (; k < kmax; ++k) sum = fmaf(value(b[k]), ur[k], sum);
       if (sl.bias) sum += value(static_cast<const T*>(sl.bias)[slot * sl.bias_slot_stride + o0 + o]);
     }
-    put(static_cast<T*>(sl.y) + row * sl.y_row_stride + o0 + o, sum);
+    put(static_cast<T*>(sl.y) + (t0 + r) * sl.y_row_stride + o0 + o, sum);
   }
+}
+
+// Few rows.  x stays in shared memory and a CTA per SM goes through tile after
+// tile of 32 outputs: 16 warps in teams, which share a tile's inputs out and
+// only meet to sum.  Each warp's ring of copies runs on across its tiles, so
+// memory never waits for a start or an end.
+//
+// Unpacking is what bounds this (the shifts and masks run at half rate), and
+// fp16 takes fewer of them than bf16: its ten mantissa bits hold a nibble where
+// it lies, 1024 + code from bits 0-3 and 1024 + 16 code from bits 4-7, less the
+// zero (any byte) by one exact fused multiply-add.  So x is taken to fp16 by a
+// power of two for each row that brings its largest value to 2^14: what that
+// cuts off is below 2^-39 of the largest, under fp32's own rounding.  The sums
+// are divided by that power.  (A row with an infinity or a NaN stays as it is.)
+//
+// A block is 256 inputs of 32 outputs, so a row's copies are whole lines.
+constexpr int kFewWarps = 16, kFewAhead = 2, kFewBlock = 256;
+constexpr int kFewPitch = kFewBlock / 2 + 16;  // bytes of a row of a block: 8 rows' words fall on 32 banks
+constexpr int kFewStage = kMmaOuts * kFewPitch;
+constexpr int kFewSmemMost = 226 * 1024;
+constexpr int kFewRing = kFewWarps * kFewAhead * kFewStage;
+
+struct FewWork {
+  int tile_begin[LORA_MAX_SLICES + 1];   // first tile of 32 outputs of each slice
+  unsigned per_group[LORA_MAX_SLICES];   // ceil(2^32 / units of a group), 0 for one: unit -> group
+  int team;                              // warps that share a tile: 1, 2, 4, 8 or 16
+  int x_pitch;                           // bytes of a row of x in shared memory
+  int nsplit;
+  long long plane_stride;
+  int wait_first;
+};
+
+template <int NT>
+constexpr int few_sum_bytes() {
+  return kFewWarps * 32 * 8 * NT * 4;
+}
+
+// D = A B (FIRST) or D += A B, fp16 operands.
+template <bool FIRST>
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  if constexpr (FIRST)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// (w & mask) | magic in one instruction; magic stays in its register.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "n"(MASK), "r"(magic));
+  return d;
+}
+
+// Word of 8 codes -> the fp16 pairs (0,4) (1,5) (2,6) (3,7) of code - zero;
+// even: 1024 + zero, odd: -(64 + zero), magic: 1024, sixteenth: 1/16, twice each.
+__device__ __forceinline__ void unpack_f16(uint32_t w, uint32_t even, uint32_t odd, uint32_t magic, uint32_t sixteenth,
+                                           uint32_t (&v)[4]) {
+  const uint32_t w8 = w >> 8;
+  v[0] = sub_f16x2(pick<0x000f000fu>(w, magic), even);
+  v[1] = fma_f16x2(pick<0x00f000f0u>(w, magic), sixteenth, odd);
+  v[2] = sub_f16x2(pick<0x000f000fu>(w8, magic), even);
+  v[3] = fma_f16x2(pick<0x00f000f0u>(w8, magic), sixteenth, odd);
+}
+
+// Word `word` of a block's row, all outputs and rows of x.
+template <int NT, bool FIRST>
+__device__ __forceinline__ void few_word(const uint8_t* at, const uint8_t* const (&xrow)[NT], int k_bytes, int word,
+                                         const uint32_t (&even)[2][2], const uint32_t (&odd)[2][2], uint32_t magic,
+                                         uint32_t sixteenth, float (&acc)[2][NT][4]) {
+  uint32_t a[2][2][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      unpack_f16(*reinterpret_cast<const uint32_t*>(at + (m * 16 + h * 8) * kFewPitch + word * 16), even[m][h],
+                 odd[m][h], magic, sixteenth, a[m][h]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const uint4 x = *reinterpret_cast<const uint4*>(xrow[n] + k_bytes + word * 64);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      mma_f16_16816<FIRST>(acc[m][n], a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
+      mma_f16_16816<false>(acc[m][n], a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
+    }
+  }
+}
+
+// One block from the ring: at, this thread's first word; xrow, its columns of x;
+// raw, this lane's output's scales and zeros; left, the block's inputs.
+template <int NT, int WPG, bool FULL>
+__device__ __forceinline__ void few_block(const uint8_t* at, const uint8_t* const (&xrow)[NT], int k_bytes,
+                                          const uint32_t (&raw)[8 / WPG], int left, float (&y)[2][NT][4]) {
+  static_assert(kMmaOuts == 32, "");
+  const int g = (threadIdx.x & 31) >> 2;
+  uint32_t magic, sixteenth;  // opaque, so that they stay in registers
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+  asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(sixteenth));
+#pragma unroll
+  for (int c = 0; c < 8 / WPG; ++c) {
+    if (!FULL && c * 32 * WPG >= left) break;
+    uint32_t even[2][2], odd[2][2];
+    float scale[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t v = __shfl_sync(0xffffffffu, raw[c], m * 16 + h * 8 + g);
+        scale[m][h] = __uint_as_float(v & 0xffff0000u);
+        even[m][h] = (v & 0xffu) * 0x10001u + magic;     // 1024 + zero
+        odd[m][h] = sub_f16x2(0x63806380u, even[m][h]);  // 960 - (1024 + zero) = -(64 + zero)
+      }
+    float acc[2][NT][4];
+    few_word<NT, true>(at, xrow, k_bytes, c * WPG, even, odd, magic, sixteenth, acc);
+#pragma unroll
+    for (int i = 1; i < WPG; ++i) {
+      if (!FULL && (c * WPG + i) * 32 >= left) break;
+      few_word<NT, false>(at, xrow, k_bytes, c * WPG + i, even, odd, magic, sixteenth, acc);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[m][n][e] = fmaf(scale[m][e >> 1], acc[m][n][e], y[m][n][e]);
+  }
+}
+
+template <int NT, int WPG>
+__global__ void __launch_bounds__(kFewWarps * 32, 1)
+    q4_few_kernel(const __grid_constant__ ProblemDesc p, const __grid_constant__ Q4Weights wts,
+                  const __grid_constant__ FewWork w, const float* __restrict__ u) {
+  constexpr int MW = kMmaOuts / 16, GROUPS = 8 / WPG, ELEMS = MW * NT * 4;
+  using T = __nv_bfloat16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_ok, s_slot[8 * NT];
+  __shared__ unsigned s_top[8 * NT];  // bits of a row's largest |x|
+  float* s_part = reinterpret_cast<float*>(smem + kFewRing);             // [warps][ELEMS][32]
+  uint8_t* s_x = smem + kFewRing + few_sum_bytes<NT>();                  // [rows][x_pitch]
+  float* s_u = reinterpret_cast<float*>(s_x + p.num_tokens * w.x_pitch);  // [routed rows][slices * R]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = warp & (w.team - 1), per_cta = kFewWarps / w.team, team = blockIdx.x * per_cta + warp / w.team;
+  const int teams = gridDim.x * per_cta, tiles = w.tile_begin[p.n_slices];
+  if (w.wait_first) pdl_wait();
+  const int nb = (p.in_dim + kFewBlock - 1) / kFewBlock;
+  const int b_lo = nb * rank / w.team, b_hi = nb * (rank + 1) / w.team;
+  uint8_t* ring = smem + warp * kFewAhead * kFewStage;
+  auto slice_of = [&](int tile) {
+    int j = 0;
+    while (j + 1 < p.n_slices && tile >= w.tile_begin[j + 1]) ++j;
+    return j;
+  };
+
+  // What is loaded next: block lb of tile lt, whose rows' addresses are kept.
+  // Outputs past the slice's last read its last row and are not stored.
+  int lt = team, lb = b_lo, stage_in = 0;
+  const uint8_t* qrow[kMmaOuts / 8];
+  const uint16_t* srow = nullptr;  // this lane's output
+  const uint8_t* zrow = nullptr;
+  unsigned per_group = 0;
+  auto aim = [&] {
+    if (lt >= tiles) return;
+    const int j = slice_of(lt);
+    const Q4Desc& d = wts.w[j];
+    const int o0 = (lt - w.tile_begin[j]) * kMmaOuts, last = p.sl[j].out_dim - 1;
+#pragma unroll
+    for (int i = 0; i < kMmaOuts / 8; ++i) qrow[i] = d.q + (long long)min(o0 + i * 8 + g, last) * d.q_stride + t * 16;
+    const long long o = min(o0 + lane, last);
+    srow = static_cast<const uint16_t*>(d.scales) + o * d.s_stride;
+    zrow = d.zeros ? d.zeros + o * d.z_stride : nullptr;
+    per_group = w.per_group[j];
+  };
+  aim();
+  auto load = [&](uint32_t (&sz)[GROUPS]) {
+    if (lt < tiles && lb < b_hi) {
+      uint8_t* dst = ring + stage_in * kFewStage + g * kFewPitch + t * 16;
+      const int k = lb * kFewBlock + t * 32;
+      if ((lb + 1) * kFewBlock <= p.in_dim) {
+#pragma unroll
+        for (int i = 0; i < kMmaOuts / 8; ++i) {
+          const uint8_t* src = qrow[i] + lb * (kFewBlock / 2);
+          cp_async16(dst + i * 8 * kFewPitch, src);
+          cp_async16(dst + i * 8 * kFewPitch + 64, src + 64);
+        }
+      } else {  // what is not loaded is not used
+#pragma unroll
+        for (int i = 0; i < kMmaOuts / 8; ++i) {
+          const uint8_t* src = qrow[i] + lb * (kFewBlock / 2);
+          if (k < p.in_dim) cp_async16(dst + i * 8 * kFewPitch, src);
+          if (k + 128 < p.in_dim) cp_async16(dst + i * 8 * kFewPitch + 64, src + 64);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < GROUPS; ++c) {
+        const int unit = lb * GROUPS + c;
+        if (unit * 32 * WPG < p.in_dim) {
+          const unsigned grp = per_group == 0 ? unit : __umulhi(unit, per_group);
+          sz[c] = (uint32_t)__ldg(srow + grp) << 16 | (zrow ? __ldg(zrow + grp) : 8u);
+        }
+      }
+      stage_in = stage_in + 1 == kFewAhead ? 0 : stage_in + 1;
+      if (++lb == b_hi) {
+        lb = b_lo;
+        lt += teams;
+        aim();
+      }
+    }
+    cp_async_commit();
+  };
+  uint32_t raw[kFewAhead][GROUPS] = {};  // the present block's first
+#pragma unroll
+  for (int i = 0; i < kFewAhead; ++i) load(raw[i]);
+
+  if (warp == 0) {
+    const bool ok = p.G == 0 || warp_check_routing(p);
+    if (lane == 0) s_ok = ok;
+    for (int r = lane; r < 8 * NT; r += 32) s_slot[r] = ok && r < p.end ? p.lora_ids[group_of_row(p, r)] : -1;
+  }
+  if (threadIdx.x < 8 * NT) s_top[threadIdx.x] = 0;
+  __syncthreads();
+  const int chunks = p.in_dim / 8, all = p.num_tokens * chunks;
+  auto x_at = [&](int r, int c) {
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + r * p.x_row_stride) + c);
+  };
+  for (int e = threadIdx.x; e < all; e += kFewWarps * 32) {
+    const int r = e / chunks;
+    const uint4 x = x_at(r, e - r * chunks);
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+      top = max(top, max(v & 0x7fffu, v >> 16 & 0x7fffu));
+    }
+    const unsigned mask = __activemask();
+    if (__match_any_sync(mask, r) == mask) {
+      top = __reduce_max_sync(mask, top);
+      if (lane == __ffs(mask) - 1) atomicMax(&s_top[r], top);
+    } else {
+      atomicMax(&s_top[r], top);
+    }
+  }
+  __syncthreads();
+  // The exponent that brings a row's largest value to 2^14.
+  auto lift = [&](int r) {
+    const unsigned top = s_top[r];
+    return top >= 0x7f80u ? 0 : min(14 + 127 - (int)(top >> 7), 120);
+  };
+  for (int e = threadIdx.x; e < all; e += kFewWarps * 32) {
+    const int r = e / chunks, c = e - r * chunks;
+    const uint4 x = x_at(r, c);
+    const float f = __uint_as_float((unsigned)(127 + lift(r)) << 23);
+    auto pair = [&](uint32_t lo, uint32_t hi) {
+      uint32_t v;
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(__uint_as_float(hi) * f), "f"(__uint_as_float(lo) * f));
+      return v;
+    };
+    constexpr uint32_t kTop = 0xffff0000u;
+    *reinterpret_cast<uint4*>(s_x + r * w.x_pitch + c * 16) =
+        make_uint4(pair(x.x << 16, x.z << 16), pair(x.x & kTop, x.z & kTop), pair(x.y << 16, x.w << 16),
+                   pair(x.y & kTop, x.w & kTop));
+  }
+  __syncthreads();
+  const uint8_t* xrow[NT];  // columns past the batch's rows are the last row's and are not stored
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xrow[n] = s_x + min(n * 8 + g, p.num_tokens - 1) * w.x_pitch + t * 16;
+
+  const bool with_u = p.end > 0;
+  bool have_u = false;
+  auto take_u = [&] {  // the whole CTA, once
+    if (!w.wait_first) pdl_wait();
+    if (s_ok)
+      for (int e = threadIdx.x; e < p.end * p.n_slices * p.R; e += kFewWarps * 32) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < w.nsplit; ++c) v += __ldcg(u + c * w.plane_stride + e);
+        s_u[e] = v;
+      }
+    __syncthreads();
+    have_u = true;
+  };
+  int stage = 0;
+  float y[MW][NT][4] = {};
+  auto team_sync = [&] {
+    __syncwarp();
+    if (w.team > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / w.team), "r"(w.team * 32) : "memory");
+  };
+  // The end of a tile: the team's sums, the delta, the outputs.
+  auto finish = [&](int tile) {
+    float* mine = s_part + warp * ELEMS * 32 + lane;
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          mine[((m * NT + n) * 4 + e) * 32] = y[m][n][e];
+          y[m][n][e] = 0.f;
+        }
+    if (with_u && !have_u) take_u();
+    team_sync();
+    const int j = slice_of(tile);
+    const SliceDesc& sl = p.sl[j];
+    const int o = (tile - w.tile_begin[j]) * kMmaOuts + lane;
+    if (o < sl.out_dim && s_ok) {
+      const bool wide_b = p.R % 8 == 0 && ((reinterpret_cast<uintptr_t>(sl.B) | (uintptr_t)(sl.B_slot_stride * 2)) & 15) == 0;
+      for (int r = rank; r < p.num_tokens; r += w.team) {
+        // Output lane, row r lie in element e of lane 4 (o % 8) + (r % 8) / 2.
+        const int e = ((lane >> 4) * NT + (r >> 3)) * 4 + ((lane >> 3) & 1) * 2 + (r & 1);
+        const float* part = s_part + ((warp - rank) * ELEMS + e) * 32 + (lane & 7) * 4 + ((r & 7) >> 1);
+        float sum = 0.f;
+        for (int v = 0; v < w.team; ++v) sum += part[v * ELEMS * 32];
+        sum *= __uint_as_float((unsigned)(127 - lift(r)) << 23);
+        const int slot = s_slot[r];
+        if (slot >= 0) {
+          const int kmax = slot_kmax(p, slot);
+          const T* b = static_cast<const T*>(sl.B) + slot * sl.B_slot_stride + (long long)o * p.R;
+          const float* ur = s_u + (r * p.n_slices + j) * p.R;
+          int k = 0;
+          if (wide_b) {
+#pragma unroll 2
+            for (; k + 8 <= kmax; k += 8) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(b + k));
+              const uint32_t bits[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                sum = fmaf(__uint_as_float(bits[q] << 16), ur[k + 2 * q], sum);
+                sum = fmaf(__uint_as_float(bits[q] & 0xffff0000u), ur[k + 2 * q + 1], sum);
+              }
+            }
+          }
+          for (; k < kmax; ++k) sum = fmaf(value(b[k]), ur[k], sum);
+          if (sl.bias) sum += value(static_cast<const T*>(sl.bias)[slot * sl.bias_slot_stride + o]);
+        }
+        put(static_cast<T*>(sl.y) + r * sl.y_row_stride + o, sum);
+      }
+    }
+    team_sync();  // the sums are read
+  };
+  int tile = team, blk = b_lo;
+  if (b_lo == b_hi) {  // more warps than blocks: this one only helps to finish
+    for (; tile < tiles; tile += teams) finish(tile);
+  }
+#pragma unroll 1
+  while (tile < tiles) {
+    cp_async_wait<kFewAhead - 1>();
+    __syncwarp();
+    const uint8_t* at = ring + stage * kFewStage + g * kFewPitch + t * 4;
+    const int left = p.in_dim - blk * kFewBlock;
+    if (left >= kFewBlock) few_block<NT, WPG, true>(at, xrow, blk * kFewBlock * 2, raw[0], left, y);
+    else few_block<NT, WPG, false>(at, xrow, blk * kFewBlock * 2, raw[0], left, y);
+    stage = stage + 1 == kFewAhead ? 0 : stage + 1;
+    __syncwarp();
+#pragma unroll
+    for (int i = 1; i < kFewAhead; ++i)
+#pragma unroll
+      for (int c = 0; c < GROUPS; ++c) raw[i - 1][c] = raw[i][c];
+    load(raw[kFewAhead - 1]);
+    if (++blk == b_hi) {
+      finish(tile);
+      blk = b_lo;
+      tile += teams;
+    }
+  }
+  cp_async_wait<0>();
+  if (with_u && !have_u) take_u();  // the others wait for the whole CTA
 }
 
 // Words of a thread that surely share a group in every slice; 0: not one.
@@ -360,6 +774,83 @@ cudaError_t launch_q4_mma(const ProblemDesc& p, const Q4Weights& wts, Q4Work w, 
   return noted(cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, WPG>, p, wts, w, u), LORA_PATH_MMA_Q4);
 }
 
+// Warps to a team: what gives the fewest steps of a block, counting a tile's
+// end as three quarters of one.
+int few_team(int tiles, int nb, int sms) {
+  int best = 16;
+  long long least = LLONG_MAX;
+  for (int team = 16; team >= 1; team /= 2) {
+    const long long at_once = (long long)std::min<long long>(sms, ((long long)tiles * team + kFewWarps - 1) / kFewWarps) *
+                              (kFewWarps / team);
+    const long long steps = (tiles + at_once - 1) / at_once * (4 * ((nb + team - 1) / team) + 3);
+    if (steps < least) {
+      least = steps;
+      best = team;
+    }
+  }
+  return best;
+}
+
+int few_x_pitch(const ProblemDesc& p) { return p.in_dim * 2 + (p.in_dim % 64 == 0 ? 64 : 0); }
+
+// Shared memory of the kernel for few rows; it is taken while that fits.
+template <int NT>
+long long few_smem(const ProblemDesc& p) {
+  return kFewRing + few_sum_bytes<NT>() + (long long)p.num_tokens * few_x_pitch(p) + 4LL * p.end * p.n_slices * p.R;
+}
+
+template <int NT, int WPG>
+cudaError_t launch_q4_few(const ProblemDesc& p, const Q4Weights& wts, const Q4Work& q, const float* u, cudaStream_t s) {
+  FewWork w{};
+  int tiles = 0;
+  for (int j = 0; j < p.n_slices; ++j) {
+    w.tile_begin[j] = tiles;
+    tiles += (p.sl[j].out_dim + kMmaOuts - 1) / kMmaOuts;
+  }
+  w.tile_begin[p.n_slices] = tiles;
+  const int sms = std::max(device_sm_count(), 1);
+  w.team = few_team(tiles, (p.in_dim + kFewBlock - 1) / kFewBlock, sms);
+  for (int j = 0; j < p.n_slices; ++j) {
+    const int g = wts.w[j].group, units = g >= p.in_dim ? INT_MAX : g / (32 * WPG);
+    w.per_group[j] = units == 1 ? 0u : (unsigned)((1ULL << 32) / units + ((1ULL << 32) % units != 0));
+  }
+  w.x_pitch = few_x_pitch(p);
+  w.nsplit = q.nsplit;
+  w.plane_stride = q.plane_stride;
+  w.wait_first = q.wait_first;
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(q4_few_kernel<NT, WPG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmemMost);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(sms, ((long long)tiles * w.team + kFewWarps - 1) / kFewWarps));
+  cfg.blockDim = dim3(kFewWarps * 32);
+  cfg.dynamicSmemBytes = (size_t)few_smem<NT>(p);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return noted(cudaLaunchKernelEx(&cfg, q4_few_kernel<NT, WPG>, p, wts, w, u), LORA_PATH_MMA_Q4);
+}
+
+template <int NT>
+cudaError_t launch_q4_few_words(const ProblemDesc& p, const Q4Weights& wts, const Q4Work& w, const float* u,
+                                cudaStream_t s) {
+  switch (q4_words_per_group(p, wts)) {
+    case 4: return launch_q4_few<NT, 4>(p, wts, w, u, s);
+    case 2: return launch_q4_few<NT, 2>(p, wts, w, u, s);
+    default: return launch_q4_few<NT, 1>(p, wts, w, u, s);
+  }
+}
+
 template <int NT>
 cudaError_t launch_q4_words(const ProblemDesc& p, const Q4Weights& wts, const Q4Work& w, const float* u, cudaStream_t s) {
   switch (q4_words_per_group(p, wts)) {
@@ -374,7 +865,7 @@ cudaError_t launch_q4_words(const ProblemDesc& p, const Q4Weights& wts, const Q4
 bool q4_fast_ok(const ProblemDesc& p, const Q4Weights& w) {
   if (p.dtype != LORA_DTYPE_BF16 || p.in_dim % 32 != 0 || p.token_rows) return false;
   if ((reinterpret_cast<uintptr_t>(p.x) & 15) != 0 || p.x_row_stride % 8 != 0) return false;
-  if ((p.num_tokens + 31) / 32 > 65535 || kMmaRing + q4_scale_bytes(p, w) > kMmaSmemMost) return false;
+  if ((p.num_tokens + 31) / 32 > 65535 || p.R > 256 || kMmaRing + q4_scale_bytes(p, w) > kMmaSmemMost) return false;
   for (int j = 0; j < p.n_slices; ++j)
     if ((reinterpret_cast<uintptr_t>(w.w[j].q) & 15) != 0 || w.w[j].q_stride % 16 != 0) return false;
   return q4_words_per_group(p, w) > 0;
@@ -386,6 +877,8 @@ cudaError_t launch_q4(const ProblemDesc& p, const Q4Weights& wts, const float* u
   w.nsplit = nsplit;
   w.plane_stride = (long long)p.end * p.n_slices * p.R;
   w.wait_first = after_shrink ? 0 : 1;
+  if (p.num_tokens <= 8 && few_smem<1>(p) <= kFewSmemMost) return launch_q4_few_words<1>(p, wts, w, u, s);
+  if (p.num_tokens <= 16 && few_smem<2>(p) <= kFewSmemMost) return launch_q4_few_words<2>(p, wts, w, u, s);
   if (p.num_tokens <= 8) return launch_q4_words<1>(p, wts, w, u, s);
   if (p.num_tokens <= 16) return launch_q4_words<2>(p, wts, w, u, s);
   return launch_q4_words<4>(p, wts, w, u, s);
