@@ -290,8 +290,4 @@ cudaError_t launch_tree(const TreeDesc& p, void* workspace, cudaStream_t s) {
   return tree_tc_ok(p) ? launch_tree_tc(p, workspace, s) : launch_tree_generic(p, workspace, s);
 }
 
-bool tree_tc_ok(const TreeDesc&) { return false; }
-size_t tree_tc_workspace(const TreeDesc&) { return 0; }
-cudaError_t launch_tree_tc(TreeDesc p, void* workspace, cudaStream_t s) { return launch_tree_generic(p, workspace, s); }
-
 }  // namespace lora

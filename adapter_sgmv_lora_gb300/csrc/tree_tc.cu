@@ -1,0 +1,650 @@
+// tree_tc.cu -- tree attention of bf16 caches on the tensor cores (tcgen05).
+// The frame is tree.cuh.
+//
+// A chunk is 128 rows, the 128 lanes of TMEM: rows that share a key/value head
+// fill an instruction even where each drafted token alone is one row of a
+// product, and every key and value is loaded once for all of them.  Tiles of
+// TT cached tokens (a stage is 32 KB at most) go through
+//   S = Q K^T      [128 x TT]  Q and K in shared memory, S in TMEM
+//   P = 2^(S - m)  a thread a row; back into TMEM over S
+//   O = P V        [128 x HV]  P from TMEM, V in shared memory as it lies
+// Two groups of four softmax warps take the tiles in turn, each with its own S
+// and O in TMEM and its own running (m, l, O) in registers, so one's softmax
+// runs under the other's products; at the end of a stream the two are joined.
+// O's tiles are summed apart and taken into registers rounded: accumulated by
+// the instruction, which cuts sums off, long contexts lose a bit every step,
+// and a rescaling never has to wait for the products.
+//
+// P enters as two bf16 terms, the first cut off and the second rounded, 16 bits
+// together: one term alone shows in outputs.  The second is taken from p (1 +
+// 2^-17), so that it is never zero and an infinite value stays one; the factor
+// comes off in the end.
+//
+// Warps: 0 loads K, 1 loads V, 2 loads Q, 3 issues the products, 4 to 11 are
+// the softmax.  Loads are 16-byte asynchronous copies, a page may hold any
+// number of tokens in any stride order.  Every wait is bounded.
+#include "tree.cuh"
+
+namespace lora {
+namespace {
+
+constexpr int kTcThreads = 384;
+constexpr float kTcLift = 1.f + 7.62939453125e-6f;  // 1 + 2^-17
+
+// HK: padded width of Q and K.  HV: columns of V a stream takes.
+template <int HK_>
+struct TcCfg {
+  static constexpr int HK = HK_, HV = HK > 128 ? 128 : HK;
+  static constexpr int TT = HK > 128 ? 64 : 128;
+  using S = TreeShape<128, TT, HV, 2>;
+  static constexpr int Q_BYTES = 128 * HK * 2, K_BYTES = TT * HK * 2, V_BYTES = TT * HV * 2;
+  static constexpr int NS = HK == 64 ? 5 : 3;  // stages of K, and of V
+  static constexpr int SMEM = Q_BYTES + NS * (K_BYTES + V_BYTES) + 1024;
+};
+
+// Byte offset of 16-byte chunk c of row r in blocks of [rows][64 columns] with
+// the 128-byte swizzle.
+template <int ROWS>
+__device__ __forceinline__ uint32_t tc_at(int r, int c) {
+  return (c >> 3) * (ROWS * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16;
+}
+
+// Shared-memory descriptor of an operand whose rows are K and whose columns
+// (64 to a 128-byte swizzled row) are the product's: blocks of 64 columns
+// `block` bytes apart, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr, uint32_t block) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kTransposeB = 1u << 16;  // instruction descriptor: B's columns are contiguous
+
+// D (+)= A B, A in TMEM.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Moves registers between warpgroups (the launch gives every thread 168).
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+constexpr int kTcFlags = 8;  // tiles whose notes are kept: more than can be in flight
+
+struct TcShared {
+  uint64_t kfull[5], kempty[5], vfull[5], vempty[5];
+  uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], ofree[2], done;
+  uint32_t tmem;
+  int fail;                        // a wait ran out
+  int ended;                       // one of the softmax groups gave up
+  int bad[kTcFlags];               // a tile has a page outside the cache
+  unsigned odd[kTcFlags][4];       // its drafted tokens whose values are not all finite
+  TreePiece piece;
+};
+
+template <int HK>
+__global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_constant__ TreeDesc p) {
+  using C = TcCfg<HK>;
+  using S = typename C::S;
+  constexpr int TT = C::TT, HV = C::HV, NS = C::NS;
+  using T = __nv_bfloat16;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) TcShared sh;
+  __shared__ float2 s_stat[128];
+  uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sk = sq + C::Q_BYTES;
+  uint8_t* sv = sk + NS * C::K_BYTES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.x;
+  const int hd = p.cache.head_dim;
+  pdl_launch_dependents();
+  if (warp == 0) {
+    const TreePiece piece = tree_piece<S>(p, u, u == 0);
+    if (lane == 0) {
+      sh.piece = piece;
+      sh.fail = sh.ended = 0;
+      for (int i = 0; i < NS; ++i) {
+        mbar_init(&sh.kfull[i], 32);
+        mbar_init(&sh.kempty[i], 1);
+        mbar_init(&sh.vfull[i], 32);
+        mbar_init(&sh.vempty[i], 1);
+      }
+      mbar_init(&sh.qfull, 32);
+      mbar_init(&sh.qempty, 1);
+      mbar_init(&sh.done, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.sfull[i], 1);
+        mbar_init(&sh.pfull[i], 128);
+        mbar_init(&sh.ofull[i], 1);
+        mbar_init(&sh.ofree[i], 128);
+      }
+      fence_mbar_init();
+    }
+  } else if (warp == 3) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+  // TMEM columns: S and P of the two groups, then O of the two.
+  auto s_col = [&](int w) { return tmem + w * 128; };
+  auto o_col = [&](int w) { return tmem + 256 + w * 128; };
+  const TreePiece piece = sh.piece;
+  TreeSegment<S> g;
+  g.first(p, piece);
+  bool dead = false;  // a wait ran out: nothing more is waited for
+  // 72 x 128 + 216 x 256 = 168 x 384.
+  if (warp >= 4) {
+    take_registers<216>();
+    // ---- softmax: a thread is row `row` of the chunk in every tile of its group
+    const int w = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const float scale = p.scale * kTreeLog2e;
+    int suse = 0;               // tiles of this group so far
+    int tile_no = 0;            // of this CTA
+    int4 split = make_int4(0, 0, 0, 0);
+    while (g.valid) {
+      const long long crow = (long long)g.chunk() * 128 + row;
+      const long long rows = (long long)g.s.n * p.group;
+      const bool live = crow < rows;
+      const int draft = live ? (int)(crow / p.group) : g.s.n - 1;
+      const int head = g.kv_head(p) * p.group + (int)(live ? crow % p.group : 0);
+      const unsigned long long* mask = p.masks ? p.masks + (long long)(g.s.row0 + draft) * p.words : nullptr;
+      const int n = g.t1 - g.t0;
+      float m = kTreeNone, l = 0.f;
+      float2 o[HV / 2];
+#pragma unroll
+      for (int e = 0; e < HV / 2; ++e) o[e] = make_float2(0.f, 0.f);
+      bool bad = false;
+      for (int i = w; i < n; i += 2) {
+        const int t = g.t0 + i, flag = (tile_no + i) % kTcFlags;
+        if (!dead && !mbar_wait(&sh.sfull[w], suse & 1)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);  // tcgen05.ld below needs the whole warp
+        if (dead) break;
+        tc_fence_after_sync();
+        bad |= sh.bad[flag] != 0;
+        const int d0 = t * TT - g.s.ctx;       // the tile's first token among the drafted ones
+        const bool drafts = d0 + TT > 0;
+        float top = kTreeNone;
+#pragma unroll
+        for (int c = 0; c < TT / 32; ++c) {
+          float s[32];
+          tmem_ld32(s_col(w) + lanes + c * 32, s);
+          if (drafts) {
+            const unsigned sees = tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, sees >> e & 1 ? s[e] * scale : kTreeNone);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e] * scale);
+          }
+        }
+        const float now = fmaxf(m, top), base = now == kTreeNone ? 0.f : now;
+        const float keep = tree_pow2(m - base);
+        m = now;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < TT / 32; ++c) {
+          float s[32];
+          tmem_ld32(s_col(w) + lanes + c * 32, s);
+          uint32_t out[32];  // 16 columns of first terms, 16 of second ones
+          unsigned sees = 0xffffffffu;
+          if (drafts) sees = tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = fma_f32x2(make_float2(s[e], s[e + 1]), make_float2(scale, scale), make_float2(-base, -base));
+            float a = tree_pow2(x.x), b = tree_pow2(x.y);
+            if (drafts) {
+              if (!(sees >> e & 1)) a = 0.f;
+              if (!(sees >> (e + 1) & 1)) b = 0.f;
+            }
+            sum = add_f32x2(sum, make_float2(a, b));
+            const uint32_t ab = __float_as_uint(a), bb = __float_as_uint(b);
+            out[e / 2] = __byte_perm(ab, bb, 0x7632);
+            const float2 rest = fma_f32x2(make_float2(a, b), make_float2(kTcLift, kTcLift),
+                                          make_float2(__uint_as_float((ab & 0xffff0000u) | 0x80000000u),
+                                                      __uint_as_float((bb & 0xffff0000u) | 0x80000000u)));
+            out[16 + e / 2] = round_pack_bf16x2(rest.x, rest.y);
+          }
+          tmem_st32(s_col(w) + lanes + c * 32, out);
+        }
+        l = fmaf(l, keep, sum.x + sum.y);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&sh.pfull[w]);
+        if (!mbar_wait(&sh.ofull[w], suse & 1)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < HV / 32; ++c) {
+          float v[32];
+          tmem_ld32(o_col(w) + lanes + c * 32, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[c * 16 + e] = fma_f32x2(o[c * 16 + e], make_float2(keep, keep), make_float2(v[2 * e], v[2 * e + 1]));
+        }
+        if (drafts) {
+          // Values that are not finite, for the rows that see them.
+#pragma unroll 1
+          for (int c = 0; c < TT / 32; ++c) {
+            unsigned who = sh.odd[flag][c] & tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
+            while (who) {
+              const int j = t * TT + c * 32 + __ffs(who) - 1;
+              who &= who - 1;
+              const int pg = (int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift);
+              const int page = p.tables[g.seq * p.table_stride + pg];
+              const T* v = static_cast<const T*>(p.cache.v) + page * p.cache.page_stride +
+                           (j - pg * p.cache.page_size) * p.cache.token_stride + g.kv_head(p) * p.cache.head_stride +
+                           g.part(p) * HV;
+#pragma unroll
+              for (int e = 0; e < HV / 2; e += 4) {
+                uint32_t v4[4] = {0, 0, 0, 0};
+                if (2 * e < hd - g.part(p) * HV)
+                  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                               : "=r"(v4[0]), "=r"(v4[1]), "=r"(v4[2]), "=r"(v4[3])
+                               : "l"(v + 2 * e)
+                               : "memory");
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if ((v4[q] & 0x7f80u) == 0x7f80u) o[e + q].x += __uint_as_float(v4[q] << 16);
+                  if ((v4[q] & 0x7f800000u) == 0x7f800000u) o[e + q].y += __uint_as_float(v4[q] & 0xffff0000u);
+                }
+              }
+            }
+          }
+        }
+        tc_fence_before_sync();
+        if (i + 2 < n || w == 0) mbar_arrive(&sh.ofree[w]);  // the second group's last: below
+        ++suse;
+      }
+      // The second group leaves what it has where the first can read it.  Both
+      // meet here whatever happened, and end together where one gave up.
+      if (n > 1 && w == 1 && !dead) {
+#pragma unroll
+        for (int c = 0; c < HV / 32; ++c) {
+          uint32_t v[32];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            v[2 * e] = __float_as_uint(o[c * 16 + e].x);
+            v[2 * e + 1] = __float_as_uint(o[c * 16 + e].y);
+          }
+          tmem_st32(o_col(1) + lanes + c * 32, v);
+        }
+        tmem_wait_st();
+        s_stat[row] = make_float2(m, bad ? -1.f : l);
+        tc_fence_before_sync();
+      }
+      if (dead) {
+        sh.fail = 1;
+        sh.ended = 1;
+      }
+      __syncwarp();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const bool ended = sh.ended != 0;
+      if (n > 1 && w == 0 && !ended) {
+        tc_fence_after_sync();
+        const float2 st = s_stat[row];
+        const float now = fmaxf(m, st.x);
+        const bool none = st.x == kTreeNone;  // nothing seen: its output is zero
+        const float mine = m == kTreeNone ? 0.f : tree_pow2(m - now), other = none ? 0.f : tree_pow2(st.x - now);
+        bad |= st.y < 0.f;
+        l = l * mine + (none ? 0.f : fabsf(st.y) * other);
+#pragma unroll
+        for (int c = 0; c < HV / 32; ++c) {
+          float v[32];
+          tmem_ld32(o_col(1) + lanes + c * 32, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = make_float2(o[c * 16 + e].x * mine, o[c * 16 + e].y * mine);
+            o[c * 16 + e] = none ? x : fma_f32x2(make_float2(v[2 * e], v[2 * e + 1]), make_float2(other, other), x);
+          }
+        }
+        m = now;
+        tc_fence_before_sync();
+      }
+      __syncwarp();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (ended) break;
+      if (n > 1 && w == 1) mbar_arrive(&sh.ofree[1]);
+      if (w == 0) {
+        const bool whole = g.whole();
+        const long long slot = tree_slot<S>(g, u);
+        const int part = g.part(p);
+        if (!whole) {
+          float4* dst = reinterpret_cast<float4*>(p.partial) + slot * (HV / 4) * 128 + row;
+#pragma unroll
+          for (int e = 0; e < HV / 4; ++e) {
+            constexpr float kOff = 1.f / kTcLift;
+            dst[e * 128] = make_float4(o[2 * e].x * kOff, o[2 * e].y * kOff, o[2 * e + 1].x * kOff, o[2 * e + 1].y * kOff);
+          }
+          p.stats[slot * 128 + row] = make_float2(m, bad ? -1.f : l);
+        } else if (live) {
+          if (bad) {
+            atomicOr(p.status, LORA_DEV_BAD_PAGE);
+          } else {
+            const float inv = l == 0.f ? 0.f : 1.f / (l * kTcLift);
+            T* out = static_cast<T*>(p.out.data) + (g.s.row0 + draft) * p.out.row_stride + head * p.out.head_stride + part * HV;
+            const int width = min(HV, hd - part * HV);
+#pragma unroll
+            for (int e = 0; e < HV / 8; ++e)
+              if (8 * e < width) {
+                const float2 *v = o + 4 * e;
+                *reinterpret_cast<uint4*>(out + 8 * e) =
+                    make_uint4(round_pack_bf16x2(v[0].x * inv, v[0].y * inv), round_pack_bf16x2(v[1].x * inv, v[1].y * inv),
+                               round_pack_bf16x2(v[2].x * inv, v[2].y * inv), round_pack_bf16x2(v[3].x * inv, v[3].y * inv));
+              }
+            if (part == 0 && p.lse) p.lse[(long long)(g.s.row0 + draft) * p.num_heads + head] = (m + log2f(l)) * kTreeLn2;
+          }
+        }
+        if (g.t0 == 0 && !whole) split = make_int4(g.seq, g.stream, tree_sharers<S>(p, piece, g, u), 0);
+      }
+      tile_no += n;
+      g.next(p);
+    }
+    if (w == 0 && row == 0) p.splits[u] = split;
+  } else {
+    give_registers<72>();
+  if (warp < 2) {
+    // ---- loads of K (warp 0) or V (warp 1): a row is C16 chunks of 16 bytes
+    constexpr int RPT = TT / 32;  // rows whose offsets a lane looks up
+    const bool is_k = warp == 0;
+    uint64_t* full = is_k ? sh.kfull : sh.vfull;
+    uint64_t* empty = is_k ? sh.kempty : sh.vempty;
+    uint8_t* stages = is_k ? sk : sv;
+    const T* src = static_cast<const T*>(is_k ? p.cache.k : p.cache.v);
+    int tile_no = 0;  // of this CTA
+    // Tiles whose copies are on their way, the oldest first.
+    struct Note {
+      int stage, flag, draft_lo, draft_hi;
+    };
+    Note n0{}, n1{}, n2{};
+    int waiting = 0;
+    // The oldest has landed: it is made visible and handed over.
+    auto hand_over = [&] {
+      if (waiting == 3) cp_async_wait<2>();
+      else if (waiting == 2) cp_async_wait<1>();
+      else cp_async_wait<0>();
+      __syncwarp();
+      if (!is_k && n0.draft_hi > n0.draft_lo) {
+        // Drafted tokens' values that are infinite or NaN would reach rows
+        // that do not see them (0 times them is NaN): they become 0 here and
+        // the rows that see them take them apart.
+        unsigned* odd = sh.odd[n0.flag];
+        if (lane < 4) odd[lane] = 0;
+        __syncwarp();
+        uint8_t* st = stages + n0.stage * C::V_BYTES;
+        for (int e = lane; e < (n0.draft_hi - n0.draft_lo) * (HV / 8); e += 32) {
+          const int r = n0.draft_lo + e / (HV / 8);
+          uint4* at = reinterpret_cast<uint4*>(st + tc_at<TT>(r, e % (HV / 8)));
+          const uint4 v = *at;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if ((w[i] & 0x7f80u) == 0x7f80u) {
+              w[i] &= 0xffff0000u;
+              any = true;
+            }
+            if ((w[i] & 0x7f800000u) == 0x7f800000u) {
+              w[i] &= 0xffffu;
+              any = true;
+            }
+          }
+          if (any) {
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            atomicOr(&odd[r >> 5], 1u << (r & 31));
+          }
+        }
+        __syncwarp();
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&full[n0.stage]);
+      n0 = n1;
+      n1 = n2;
+      --waiting;
+    };
+    while (g.valid) {
+      const int kv = g.kv_head(p);
+      const long long head = (long long)kv * p.cache.head_stride + (is_k ? 0 : (long long)g.part(p) * HV);
+      const int width = is_k ? hd : min(HV, hd - g.part(p) * HV);  // columns that exist
+      const int* table = p.tables + g.seq * p.table_stride;
+      auto look_up = [&](int t, int (&page)[RPT]) {
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+          const int j = min(t * TT + i * 32 + lane, g.s.len - 1);
+          page[i] = table[(int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift)];
+        }
+      };
+      int page[RPT];
+      look_up(g.t0, page);
+      for (int t = g.t0; t < g.t1; ++t) {
+        long long off[RPT];
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+          const int j = t * TT + i * 32 + lane;
+          const int n = (int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift);
+          const bool none = j >= g.s.len, out = !none && (unsigned)page[i] >= (unsigned)p.cache.num_pages;
+          bad |= out;
+          off[i] = none || out ? -1
+                               : page[i] * p.cache.page_stride + (long long)(j - n * p.cache.page_size) * p.cache.token_stride + head;
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (t + 1 < g.t1) look_up(t + 1, page);
+        const int stage = tile_no % NS, flag = tile_no % kTcFlags;
+        if (tile_no >= NS && !dead) {
+          // While the stage is still in use, what has landed is handed over.
+          while (waiting > 0 && !__all_sync(0xffffffffu, mbar_test(&empty[stage], (tile_no / NS - 1) & 1))) hand_over();
+          if (!mbar_wait(&empty[stage], (tile_no / NS - 1) & 1)) dead = true;
+          dead = __any_sync(0xffffffffu, dead);
+        }
+        if (dead) {
+          if (lane == 0) sh.fail = 1;
+          g.valid = false;
+          break;
+        }
+        if (is_k && lane == 0) sh.bad[flag] = bad;
+        uint8_t* st = stages + stage * (is_k ? C::K_BYTES : C::V_BYTES);
+        auto copy = [&](auto chunks) {
+          constexpr int C16 = decltype(chunks)::value, ROWS = 32 / C16;  // chunks of a row, rows a step
+          const int c = lane % C16, sub = lane / C16;
+          const bool exists = c * 8 < width;
+#pragma unroll
+          for (int i = 0; i < TT / ROWS; ++i) {
+            const int r = i * ROWS + sub;
+            const long long o = __shfl_sync(0xffffffffu, off[i * ROWS / 32], r & 31);
+            const bool in = o >= 0 && exists;
+            cp_async16_zfill(st + tc_at<TT>(r, c), src + (in ? o + c * 8 : 0), in ? 16 : 0);
+          }
+        };
+        if constexpr (HK == HV) {
+          copy(std::integral_constant<int, HK / 8>());
+        } else {
+          if (is_k) copy(std::integral_constant<int, HK / 8>());
+          else copy(std::integral_constant<int, HV / 8>());
+        }
+        cp_async_commit();
+        const Note note{stage, flag, max(0, g.s.ctx - t * TT), min(TT, g.s.len - t * TT)};
+        if (waiting == 0) n0 = note;
+        else if (waiting == 1) n1 = note;
+        else n2 = note;
+        if (++waiting == 3) hand_over();
+        ++tile_no;
+      }
+      if (g.valid) g.next(p);
+    }
+    while (waiting > 0) hand_over();
+    cp_async_wait<0>();
+  } else if (warp == 2) {
+    // ---- loads of Q: a chunk's rows, once a segment
+    int seg_no = 0;
+    while (g.valid) {
+      if (seg_no > 0 && !mbar_wait(&sh.qempty, (seg_no - 1) & 1)) dead = true;
+      if (__any_sync(0xffffffffu, dead)) break;
+      const int kv = g.kv_head(p);
+      const long long row0 = (long long)g.chunk() * 128, rows = (long long)g.s.n * p.group - row0;
+      constexpr int C16 = HK / 8, ROWS = 32 / C16;
+      const int c = lane % C16, sub = lane / C16;
+      for (int i = 0; i < 128 / ROWS; ++i) {
+        const int r = i * ROWS + sub;
+        const bool in = r < rows && c * 8 < hd;
+        const T* src = static_cast<const T*>(p.q.data);
+        if (in) {
+          const int n = (int)((row0 + r) / p.group), h = kv * p.group + (int)((row0 + r) % p.group);
+          src += (g.s.row0 + n) * p.q.row_stride + h * p.q.head_stride + c * 8;
+        }
+        cp_async16_zfill(sq + tc_at<128>(r, c), src, in ? 16 : 0);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.qfull);
+      ++seg_no;
+      g.next(p);
+    }
+    cp_async_wait<0>();
+  } else if (warp == 3) {
+    // ---- the products, issued by one lane
+    if (lane == 0) {
+      constexpr uint32_t s_idesc = idesc_bf16_f32(128, TT), o_idesc = idesc_bf16_f32(128, HV) | kTransposeB;
+      int seg_no = 0, kt = 0, vt = 0;   // segments, tiles of K and of V so far
+      int puse[2] = {0, 0};             // tiles so far of each group
+      bool ok = true;
+      const uint32_t qa = smem_addr(sq);
+      while (g.valid && ok) {
+        const int n = g.t1 - g.t0;
+        if (!(ok = mbar_wait(&sh.qfull, seg_no & 1))) break;
+        auto scores = [&](int i) {
+          const int w = i & 1, st = kt % NS;
+          if (!(ok = mbar_wait(&sh.kfull[st], (kt / NS) & 1))) return;
+          tc_fence_after_sync();
+          const uint32_t ka = smem_addr(sk + st * C::K_BYTES);
+#pragma unroll
+          for (int k = 0; k < HK / 16; ++k)
+            tc_mma_bf16(s_col(w), sw128_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32),
+                        sw128_desc(ka + (k >> 2) * (TT * 128) + (k & 3) * 32), s_idesc, k > 0);
+          tc_commit(&sh.kempty[st]);
+          tc_commit(&sh.sfull[w]);
+          if (i + 1 == n) tc_commit(&sh.qempty);
+          ++kt;
+        };
+        scores(0);
+        for (int i = 0; i < n && ok; ++i) {
+          // The next tile's scores go into the other group's columns, whose
+          // probabilities the products issued before have read.
+          if (i + 1 < n) scores(i + 1);
+          if (!ok) break;
+          const int w = i & 1, st = vt % NS;
+          if (!(ok = mbar_wait(&sh.vfull[st], (vt / NS) & 1))) break;
+          if (!(ok = mbar_wait(&sh.pfull[w], puse[w] & 1))) break;
+          if (puse[w] > 0 && !(ok = mbar_wait(&sh.ofree[w], (puse[w] - 1) & 1))) break;
+          tc_fence_after_sync();
+          const uint32_t va = smem_addr(sv + st * C::V_BYTES);
+#pragma unroll
+          for (int k = 0; k < TT / 16; ++k)
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+              tc_mma_bf16_ts(o_col(w), s_col(w) + (k >> 1) * 32 + term * 16 + (k & 1) * 8,
+                             sw128_desc_mn(va + k * 2048, TT * 128), o_idesc, (k > 0 || term > 0));
+          tc_commit(&sh.vempty[st]);
+          tc_commit(&sh.ofull[w]);
+          ++puse[w];
+          ++vt;
+        }
+        if (!ok) break;
+        ++seg_no;
+        g.next(p);
+      }
+      if (!ok) atomicExch(&sh.fail, 1);
+      tc_commit(&sh.done);
+    }
+    __syncwarp();
+  }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 3) {
+    (void)mbar_wait(&sh.done, 0);  // products in flight end before their columns are released
+    if (sh.fail && lane == 0) atomicOr(p.status, LORA_DEV_TIMEOUT);
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HK>
+cudaError_t launch_tc(TreeDesc p, void* workspace, cudaStream_t s) {
+  using C = TcCfg<HK>;
+  static std::atomic<unsigned long long> done{0};
+  tree_fill(tree_sizes<typename C::S>(), p, std::min(std::max(device_sm_count(), 1), kMaxSmsForWorkspace), workspace);
+  cudaError_t e = tree_allow_smem(tree_tc_kernel<HK>, C::SMEM, done);
+  if (e != cudaSuccess) return e;
+  tree_tc_kernel<HK><<<p.pieces, kTcThreads, C::SMEM, s>>>(p);
+  if ((e = noted(cudaGetLastError(), LORA_PATH_TC_TREE)) != cudaSuccess) return e;
+  return launch_tree_join<typename C::S, __nv_bfloat16>(p, s);
+}
+
+}  // namespace
+
+// bf16 rows of whole 16-byte chunks on 16-byte boundaries.  A head wider than
+// a stream's part of V is read by several CTAs, so its output may not be its
+// query.
+bool tree_tc_ok(const TreeDesc& p) {
+  const CacheDesc& c = p.cache;
+  const auto low = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) |
+                   reinterpret_cast<uintptr_t>(p.q.data) | reinterpret_cast<uintptr_t>(p.out.data);
+  return p.dtype == LORA_DTYPE_BF16 && (low & 15) == 0 && c.head_dim % 8 == 0 && c.page_stride % 8 == 0 &&
+         c.token_stride % 8 == 0 && c.head_stride % 8 == 0 && p.q.row_stride % 8 == 0 && p.q.head_stride % 8 == 0 &&
+         p.out.row_stride % 8 == 0 && p.out.head_stride % 8 == 0 && !(c.head_dim > 128 && p.q.data == p.out.data);
+}
+
+size_t tree_tc_workspace(const TreeDesc& p) {
+  auto bytes = [&](auto cfg) {
+    const TreeSizes z = tree_sizes<typename decltype(cfg)::S>();
+    return tree_bytes(z, tree_pieces(z, p, kMaxSmsForWorkspace));
+  };
+  const int hd = p.cache.head_dim;
+  return hd <= 64 ? bytes(TcCfg<64>{}) : hd <= 128 ? bytes(TcCfg<128>{}) : bytes(TcCfg<256>{});
+}
+
+cudaError_t launch_tree_tc(TreeDesc p, void* workspace, cudaStream_t s) {
+  if (p.cache.head_dim <= 64) return launch_tc<64>(p, workspace, s);
+  if (p.cache.head_dim <= 128) return launch_tc<128>(p, workspace, s);
+  return launch_tc<256>(p, workspace, s);
+}
+
+}  // namespace lora
