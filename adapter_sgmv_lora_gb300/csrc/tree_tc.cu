@@ -198,43 +198,55 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
         bad |= sh.bad[flag] != 0;
         const int d0 = t * TT - g.s.ctx;       // the tile's first token among the drafted ones
         const bool drafts = d0 + TT > 0;
+        // What the row sees of 32 tokens.
+        auto sees_of = [&](int c) { return drafts ? tree_sees(p, mask, draft, d0 + c * 32, g.s.n) : 0xffffffffu; };
         float top = kTreeNone;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < TT / 32; ++c) {
           float s[32];
           tmem_ld32(s_col(w) + lanes + c * 32, s);
-          if (drafts) {
-            const unsigned sees = tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, sees >> e & 1 ? s[e] * scale : kTreeNone);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e] * scale);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = mul_f32x2(make_float2(s[e], s[e + 1]), make_float2(scale, scale));
+            s[e] = x.x;
+            s[e + 1] = x.y;
           }
+          const unsigned sees = sees_of(c);
+          if (!__all_sync(0xffffffffu, sees == 0xffffffffu)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(sees >> e & 1)) s[e] = kTreeNone;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
         }
         const float now = fmaxf(m, top), base = now == kTreeNone ? 0.f : now;
         const float keep = tree_pow2(m - base);
         m = now;
         float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < TT / 32; ++c) {
           float s[32];
           tmem_ld32(s_col(w) + lanes + c * 32, s);
-          uint32_t out[32];  // 16 columns of first terms, 16 of second ones
-          unsigned sees = 0xffffffffu;
-          if (drafts) sees = tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float2 x = fma_f32x2(make_float2(s[e], s[e + 1]), make_float2(scale, scale), make_float2(-base, -base));
-            float a = tree_pow2(x.x), b = tree_pow2(x.y);
-            if (drafts) {
-              if (!(sees >> e & 1)) a = 0.f;
-              if (!(sees >> (e + 1) & 1)) b = 0.f;
-            }
-            sum = add_f32x2(sum, make_float2(a, b));
-            const uint32_t ab = __float_as_uint(a), bb = __float_as_uint(b);
+            s[e] = tree_pow2(x.x);
+            s[e + 1] = tree_pow2(x.y);
+          }
+          const unsigned sees = sees_of(c);
+          if (!__all_sync(0xffffffffu, sees == 0xffffffffu)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(sees >> e & 1)) s[e] = 0.f;
+          }
+          uint32_t out[32];  // 16 columns of first terms, 16 of second ones
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            sum = add_f32x2(sum, make_float2(s[e], s[e + 1]));
+            const uint32_t ab = __float_as_uint(s[e]), bb = __float_as_uint(s[e + 1]);
             out[e / 2] = __byte_perm(ab, bb, 0x7632);
-            const float2 rest = fma_f32x2(make_float2(a, b), make_float2(kTcLift, kTcLift),
+            const float2 rest = fma_f32x2(make_float2(s[e], s[e + 1]), make_float2(kTcLift, kTcLift),
                                           make_float2(__uint_as_float((ab & 0xffff0000u) | 0x80000000u),
                                                       __uint_as_float((bb & 0xffff0000u) | 0x80000000u)));
             out[16 + e / 2] = round_pack_bf16x2(rest.x, rest.y);
@@ -387,28 +399,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
     uint8_t* stages = is_k ? sk : sv;
     const T* src = static_cast<const T*>(is_k ? p.cache.k : p.cache.v);
     int tile_no = 0;  // of this CTA
-    // Tiles whose copies are on their way, the oldest first.
-    struct Note {
-      int stage, flag, draft_lo, draft_hi;
-    };
-    Note n0{}, n1{}, n2{};
-    int waiting = 0;
+    // Tiles whose copies are on their way, the oldest first: their drafted
+    // tokens, the first and the one behind the last.
+    int n0 = 0, n1 = 0, n2 = 0, waiting = 0;
     // The oldest has landed: it is made visible and handed over.
     auto hand_over = [&] {
       if (waiting == 3) cp_async_wait<2>();
       else if (waiting == 2) cp_async_wait<1>();
       else cp_async_wait<0>();
       __syncwarp();
-      if (!is_k && n0.draft_hi > n0.draft_lo) {
+      const int handed = tile_no - waiting, draft_lo = n0 & 0xffff, draft_hi = n0 >> 16;
+      if (!is_k && draft_hi > draft_lo) {
         // Drafted tokens' values that are infinite or NaN would reach rows
         // that do not see them (0 times them is NaN): they become 0 here and
         // the rows that see them take them apart.
-        unsigned* odd = sh.odd[n0.flag];
+        unsigned* odd = sh.odd[handed % kTcFlags];
         if (lane < 4) odd[lane] = 0;
         __syncwarp();
-        uint8_t* st = stages + n0.stage * C::V_BYTES;
-        for (int e = lane; e < (n0.draft_hi - n0.draft_lo) * (HV / 8); e += 32) {
-          const int r = n0.draft_lo + e / (HV / 8);
+        uint8_t* st = stages + handed % NS * C::V_BYTES;
+        for (int e = lane; e < (draft_hi - draft_lo) * (HV / 8); e += 32) {
+          const int r = draft_lo + e / (HV / 8);
           uint4* at = reinterpret_cast<uint4*>(st + tc_at<TT>(r, e % (HV / 8)));
           const uint4 v = *at;
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -432,7 +442,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
         __syncwarp();
       }
       fence_proxy_async_smem();
-      mbar_arrive(&full[n0.stage]);
+      mbar_arrive(&full[handed % NS]);
       n0 = n1;
       n1 = n2;
       --waiting;
@@ -483,7 +493,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
           constexpr int C16 = decltype(chunks)::value, ROWS = 32 / C16;  // chunks of a row, rows a step
           const int c = lane % C16, sub = lane / C16;
           const bool exists = c * 8 < width;
-#pragma unroll
+#pragma unroll 8
           for (int i = 0; i < TT / ROWS; ++i) {
             const int r = i * ROWS + sub;
             const long long o = __shfl_sync(0xffffffffu, off[i * ROWS / 32], r & 31);
@@ -498,12 +508,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
           else copy(std::integral_constant<int, HV / 8>());
         }
         cp_async_commit();
-        const Note note{stage, flag, max(0, g.s.ctx - t * TT), min(TT, g.s.len - t * TT)};
+        const int note = max(0, min(TT, g.s.ctx - t * TT)) | min(TT, g.s.len - t * TT) << 16;
         if (waiting == 0) n0 = note;
         else if (waiting == 1) n1 = note;
         else n2 = note;
-        if (++waiting == 3) hand_over();
         ++tile_no;
+        if (++waiting == 3) hand_over();
       }
       if (g.valid) g.next(p);
     }
