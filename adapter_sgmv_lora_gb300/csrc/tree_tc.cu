@@ -23,6 +23,9 @@
 // Warps: 0 loads K, 1 loads V, 2 loads Q, 3 issues the products, 4 to 11 are
 // the softmax.  Loads are 16-byte asynchronous copies, a page may hold any
 // number of tokens in any stride order.  Every wait is bounded.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "tree.cuh"
 
 namespace lora {
@@ -77,6 +80,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Moves registers between warpgroups (the launch gives every thread 168).
@@ -101,10 +111,37 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// A box of a 4-D tensor map into shared memory; completion counted in bytes.
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Boxes of 64 columns.  K and V: [page][head][token][column], `rows` tokens a
+// box, a power of two that page_size is a multiple of, so that no box crosses
+// a page.  Q: [row][head][column], the group's heads of 128 / group rows, where
+// group divides 128 (q_boxes).
+struct TcMaps {
+  CUtensorMap k, v, q;
+  int rows;
+  int q_boxes;
+};
+
 constexpr int kTcFlags = 8;  // tiles whose notes are kept: more than can be in flight
 
 struct TcShared {
   uint64_t kfull[5], kempty[5], vfull[5], vempty[5];
+  uint64_t land[2];                // V tiles that are looked through before they are handed over
   uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], ofree[2], done;
   uint32_t tmem;
   int fail;                        // a wait ran out
@@ -114,8 +151,10 @@ struct TcShared {
   TreePiece piece;
 };
 
-template <int HK>
-__global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_constant__ TreeDesc p) {
+// BOXES: K and V come in boxes (pages of a multiple of 8 tokens), else row by row.
+template <int HK, bool BOXES>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tree_tc_kernel(const __grid_constant__ TreeDesc p, const __grid_constant__ TcMaps maps) {
   using C = TcCfg<HK>;
   using S = typename C::S;
   constexpr int TT = C::TT, HV = C::HV, NS = C::NS;
@@ -135,12 +174,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
       sh.piece = piece;
       sh.fail = sh.ended = 0;
       for (int i = 0; i < NS; ++i) {
-        mbar_init(&sh.kfull[i], 32);
+        mbar_init(&sh.kfull[i], BOXES ? 1 : 32);
         mbar_init(&sh.kempty[i], 1);
-        mbar_init(&sh.vfull[i], 32);
+        mbar_init(&sh.vfull[i], BOXES ? 1 : 32);
         mbar_init(&sh.vempty[i], 1);
       }
-      mbar_init(&sh.qfull, 32);
+      mbar_init(&sh.qfull, BOXES && maps.q_boxes ? 1 : 32);
+      mbar_init(&sh.land[0], 1);
+      mbar_init(&sh.land[1], 1);
       mbar_init(&sh.qempty, 1);
       mbar_init(&sh.done, 1);
       for (int i = 0; i < 2; ++i) {
@@ -240,18 +281,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
             for (int e = 0; e < 32; ++e)
               if (!(sees >> e & 1)) s[e] = 0.f;
           }
-          uint32_t out[32];  // 16 columns of first terms, 16 of second ones
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            sum = add_f32x2(sum, make_float2(s[e], s[e + 1]));
-            const uint32_t ab = __float_as_uint(s[e]), bb = __float_as_uint(s[e + 1]);
-            out[e / 2] = __byte_perm(ab, bb, 0x7632);
-            const float2 rest = fma_f32x2(make_float2(s[e], s[e + 1]), make_float2(kTcLift, kTcLift),
-                                          make_float2(__uint_as_float((ab & 0xffff0000u) | 0x80000000u),
-                                                      __uint_as_float((bb & 0xffff0000u) | 0x80000000u)));
-            out[16 + e / 2] = round_pack_bf16x2(rest.x, rest.y);
+          for (int half = 0; half < 2; ++half) {  // 16 tokens: 8 columns of first terms, 8 of second ones
+            uint32_t out[16];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int e = half * 16 + q * 2;
+              sum = add_f32x2(sum, make_float2(s[e], s[e + 1]));
+              const uint32_t ab = __float_as_uint(s[e]), bb = __float_as_uint(s[e + 1]);
+              out[q] = __byte_perm(ab, bb, 0x7632);
+              const float2 rest = fma_f32x2(make_float2(s[e], s[e + 1]), make_float2(kTcLift, kTcLift),
+                                            make_float2(__uint_as_float((ab & 0xffff0000u) | 0x80000000u),
+                                                        __uint_as_float((bb & 0xffff0000u) | 0x80000000u)));
+              out[8 + q] = round_pack_bf16x2(rest.x, rest.y);
+            }
+            tmem_st16(s_col(w) + lanes + c * 32 + half * 16, out);
           }
-          tmem_st32(s_col(w) + lanes + c * 32, out);
         }
         l = fmaf(l, keep, sum.x + sum.y);
         tmem_wait_st();
@@ -390,7 +435,112 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
     if (w == 0 && row == 0) p.splits[u] = split;
   } else {
     give_registers<72>();
-  if (warp < 2) {
+  if (BOXES && warp < 2) {
+    // ---- loads of K (warp 0) or V (warp 1), a box a lane
+    const bool is_k = warp == 0;
+    uint64_t* full = is_k ? sh.kfull : sh.vfull;
+    uint64_t* empty = is_k ? sh.kempty : sh.vempty;
+    const void* map = is_k ? &maps.k : &maps.v;
+    const int box = maps.rows, blocks = (is_k ? HK : HV) / 64;
+    int tile_no = 0, looked = 0;
+    // A tile of V that is looked through once it has landed: its stage and
+    // flag, first drafted token, tokens.
+    struct Look {
+      int tile, lo, hi;
+      bool open;
+    } look{};
+    auto look_through = [&] {
+      if (!look.open) return;
+      look.open = false;
+      if (!mbar_wait(&sh.land[looked & 1], (looked >> 1) & 1)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      ++looked;
+      if (dead) return;
+      // Drafted tokens' values that are infinite or NaN would reach rows that
+      // do not see them (0 times them is NaN): they become 0 here and the rows
+      // that see them take them apart.  What lies behind the last token too.
+      unsigned* odd = sh.odd[look.tile % kTcFlags];
+      if (lane < 4) odd[lane] = 0;
+      __syncwarp();
+      uint8_t* st = sv + look.tile % NS * C::V_BYTES;
+      for (int e = lane; e < (TT - look.lo) * (HV / 8); e += 32) {
+        const int r = look.lo + e / (HV / 8);
+        uint4* at = reinterpret_cast<uint4*>(st + tc_at<TT>(r, e % (HV / 8)));
+        if (r >= look.hi) {
+          *at = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        const uint4 v = *at;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if ((w[i] & 0x7f80u) == 0x7f80u) {
+            w[i] &= 0xffff0000u;
+            any = true;
+          }
+          if ((w[i] & 0x7f800000u) == 0x7f800000u) {
+            w[i] &= 0xffffu;
+            any = true;
+          }
+        }
+        if (any) {
+          *at = make_uint4(w[0], w[1], w[2], w[3]);
+          atomicOr(&odd[r >> 5], 1u << (r & 31));
+        }
+      }
+      __syncwarp();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[look.tile % NS]);
+    };
+    int issued = 0;  // tiles that are looked through, so far issued
+    while (g.valid) {
+      const int kv = g.kv_head(p), col = is_k ? 0 : g.part(p) * HV;
+      const int* table = p.tables + g.seq * p.table_stride;
+      auto look_up = [&](int t) {  // the page of this lane's box
+        const int j = min(t * TT + min(lane * box, TT - box), g.s.len - 1);
+        return table[(int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift)];
+      };
+      int page = look_up(g.t0);
+      for (int t = g.t0; t < g.t1; ++t) {
+        const int j = t * TT + lane * box, tokens = min(TT, g.s.len - t * TT);
+        const bool mine = lane * box < tokens;
+        const int slot = j - (int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift) * p.cache.page_size;
+        const bool out = mine && (unsigned)page >= (unsigned)p.cache.num_pages;
+        const bool bad = __any_sync(0xffffffffu, out);
+        const int from = out ? p.cache.num_pages : page;  // behind the last page: zeros
+        if (t + 1 < g.t1) page = look_up(t + 1);
+        const int stage = tile_no % NS;
+        if (tile_no >= NS && !dead && !mbar_wait(&empty[stage], (tile_no / NS - 1) & 1)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+        if (is_k && lane == 0) sh.bad[tile_no % kTcFlags] = bad;
+        const bool through = !is_k && t * TT + TT > g.s.ctx;
+        uint64_t* bar = through ? &sh.land[issued & 1] : &full[stage];
+        if (lane == 0) mbar_arrive_expect_tx(bar, (tokens + box - 1) / box * box * blocks * 128);
+        __syncwarp();
+        if (mine) {
+          uint8_t* dst = (is_k ? sk + stage * C::K_BYTES : sv + stage * C::V_BYTES) + lane * box * 128;
+          for (int b = 0; b < blocks; ++b) tma_load_4d(dst + b * (TT * 128), map, col + b * 64, slot, kv, from, bar);
+        }
+        look_through();  // the one before, with these on their way
+        if (through) {
+          look = Look{tile_no, max(0, g.s.ctx - t * TT), tokens, true};
+          ++issued;
+        }
+        ++tile_no;
+      }
+      if (dead) break;
+      g.next(p);
+    }
+    look_through();
+    if (dead) {  // copies in flight land before the block ends
+      if (lane == 0) sh.fail = 1;
+      if (look.open) (void)mbar_wait(&sh.land[looked & 1], (looked >> 1) & 1);
+      for (int i = max(0, tile_no - NS); i < tile_no; ++i) (void)mbar_wait(&full[i % NS], (i / NS) & 1);
+    }
+  } else if (!BOXES && warp < 2) {
     // ---- loads of K (warp 0) or V (warp 1): a row is C16 chunks of 16 bytes
     constexpr int RPT = TT / 32;  // rows whose offsets a lane looks up
     const bool is_k = warp == 0;
@@ -526,6 +676,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
       if (seg_no > 0 && !mbar_wait(&sh.qempty, (seg_no - 1) & 1)) dead = true;
       if (__any_sync(0xffffffffu, dead)) break;
       const int kv = g.kv_head(p);
+      if (BOXES && maps.q_boxes) {
+        // Rows behind the sequence's are other sequences' or zero: of no effect.
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.qfull, C::Q_BYTES);
+          for (int b = 0; b < HK / 64; ++b)
+            tma_load_3d(sq + b * (128 * 128), &maps.q, b * 64, kv * p.group, g.s.row0 + g.chunk() * (128 / p.group), &sh.qfull);
+        }
+        __syncwarp();
+        ++seg_no;
+        g.next(p);
+        continue;
+      }
       const long long row0 = (long long)g.chunk() * 128, rows = (long long)g.s.n * p.group - row0;
       constexpr int C16 = HK / 8, ROWS = 32 / C16;
       const int c = lane % C16, sub = lane / C16;
@@ -588,7 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
           for (int k = 0; k < TT / 16; ++k)
 #pragma unroll
             for (int term = 0; term < 2; ++term)
-              tc_mma_bf16_ts(o_col(w), s_col(w) + (k >> 1) * 32 + term * 16 + (k & 1) * 8,
+              tc_mma_bf16_ts(o_col(w), s_col(w) + k * 16 + term * 8,
                              sw128_desc_mn(va + k * 2048, TT * 128), o_idesc, (k > 0 || term > 0));
           tc_commit(&sh.vempty[st]);
           tc_commit(&sh.ofull[w]);
@@ -616,16 +778,70 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
   }
 }
 
-template <int HK>
-cudaError_t launch_tc(TreeDesc p, void* workspace, cudaStream_t s) {
+PFN_cuTensorMapEncodeTiled_v12000 tree_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// The maps of K, V and Q; false: rows are copied one by one.
+template <int TT>
+bool encode_maps(const TreeDesc& p, TcMaps* m) {
+  const CacheDesc& c = p.cache;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tree_encode_fn();
+  m->rows = std::min(TT, c.page_size & -c.page_size);
+  if (!enc || m->rows < 8) return false;
+  // A dimension of one element has any stride; the map wants a legal one.
+  auto stride = [](long long elements, long long count) -> cuuint64_t { return count > 1 ? (cuuint64_t)elements * 2 : 16; };
+  auto legal = [](cuuint64_t bytes) { return bytes > 0 && bytes % 16 == 0 && bytes < (1ULL << 40); };
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  auto encode = [&](CUtensorMap* map, int rank, void* data, const cuuint64_t* dims, const cuuint64_t* strides,
+                    const cuuint32_t* box) {
+    for (int i = 0; i + 1 < rank; ++i)
+      if (!legal(strides[i])) return false;
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, data, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+  };
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_kv_heads,
+                              (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {stride(c.token_stride, c.page_size), stride(c.head_stride, c.num_kv_heads),
+                                 stride(c.page_stride, c.num_pages)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)m->rows, 1, 1};
+  if (!encode(&m->k, 4, c.k, dims, strides, box) || !encode(&m->v, 4, c.v, dims, strides, box)) return false;
+  m->q_boxes = 0;
+  if (128 % p.group == 0) {
+    const cuuint64_t qdims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)p.num_heads, (cuuint64_t)p.num_rows};
+    const cuuint64_t qstrides[2] = {stride(p.q.head_stride, p.num_heads), stride(p.q.row_stride, p.num_rows)};
+    const cuuint32_t qbox[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(128 / p.group)};
+    m->q_boxes = encode(&m->q, 3, p.q.data, qdims, qstrides, qbox);
+  }
+  return true;
+}
+
+template <int HK, bool BOXES>
+cudaError_t launch_tc(TreeDesc p, const TcMaps& maps, void* workspace, cudaStream_t s) {
   using C = TcCfg<HK>;
   static std::atomic<unsigned long long> done{0};
   tree_fill(tree_sizes<typename C::S>(), p, std::min(std::max(device_sm_count(), 1), kMaxSmsForWorkspace), workspace);
-  cudaError_t e = tree_allow_smem(tree_tc_kernel<HK>, C::SMEM, done);
+  cudaError_t e = tree_allow_smem(tree_tc_kernel<HK, BOXES>, C::SMEM, done);
   if (e != cudaSuccess) return e;
-  tree_tc_kernel<HK><<<p.pieces, kTcThreads, C::SMEM, s>>>(p);
+  tree_tc_kernel<HK, BOXES><<<p.pieces, kTcThreads, C::SMEM, s>>>(p, maps);
   if ((e = noted(cudaGetLastError(), LORA_PATH_TC_TREE)) != cudaSuccess) return e;
   return launch_tree_join<typename C::S, __nv_bfloat16>(p, s);
+}
+
+template <int HK>
+cudaError_t launch_tc(const TreeDesc& p, void* workspace, cudaStream_t s) {
+  TcMaps maps{};
+  return encode_maps<TcCfg<HK>::TT>(p, &maps) ? launch_tc<HK, true>(p, maps, workspace, s)
+                                              : launch_tc<HK, false>(p, maps, workspace, s);
 }
 
 }  // namespace
