@@ -6,14 +6,14 @@
 // product, and every key and value is loaded once for all of them.  Tiles of
 // TT cached tokens (a stage is 32 KB at most) go through
 //   S = Q K^T      [128 x TT]  Q and K in shared memory, S in TMEM
-//   P = 2^(S - m)  a thread a row; back into TMEM over S
+//   P = 2^(S - m)  two threads a row, back into TMEM over S
 //   O = P V        [128 x HV]  P from TMEM, V in shared memory as it lies
-// Two groups of four softmax warps take the tiles in turn, each with its own S
-// and O in TMEM and its own running (m, l, O) in registers, so one's softmax
-// runs under the other's products; at the end of a stream the two are joined.
-// O's tiles are summed apart and taken into registers rounded: accumulated by
-// the instruction, which cuts sums off, long contexts lose a bit every step,
-// and a rescaling never has to wait for the products.
+// S and O have two buffers each: the next scores and the last tile's output are
+// under way while a tile's softmax runs.  A thread holds half a row's scores at
+// once and half of its running O; the halves exchange their maximum through
+// shared memory.  O's tiles are summed apart and taken into registers rounded:
+// accumulated by the instruction, which cuts sums off, long contexts lose a bit
+// every step, and a rescaling would have to wait for the products.
 //
 // P enters as two bf16 terms, the first cut off and the second rounded, 16 bits
 // together: one term alone shows in outputs.  The second is taken from p (1 +
@@ -42,7 +42,7 @@ struct TcCfg {
   using S = TreeShape<128, TT, HV, 2>;
   static constexpr int Q_BYTES = 128 * HK * 2, K_BYTES = TT * HK * 2, V_BYTES = TT * HV * 2;
   static constexpr int NS = HK == 64 ? 5 : 3;  // stages of K, and of V
-  static constexpr int SMEM = Q_BYTES + NS * (K_BYTES + V_BYTES) + 1024;
+  static constexpr int SMEM = Q_BYTES + NS * (K_BYTES + V_BYTES);
 };
 
 // Byte offset of 16-byte chunk c of row r in blocks of [rows][64 columns] with
@@ -70,22 +70,33 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// N consecutive columns of this warp's lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld_columns(uint32_t taddr, float (&v)[N]) {
+  static_assert(N == 32 || N == 64, "");
+  uint32_t r[N];
+#pragma unroll
+  for (int c = 0; c < N; c += 32)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[c]), "=r"(r[c + 1]), "=r"(r[c + 2]), "=r"(r[c + 3]), "=r"(r[c + 4]), "=r"(r[c + 5]), "=r"(r[c + 6]),
+          "=r"(r[c + 7]), "=r"(r[c + 8]), "=r"(r[c + 9]), "=r"(r[c + 10]), "=r"(r[c + 11]), "=r"(r[c + 12]),
+          "=r"(r[c + 13]), "=r"(r[c + 14]), "=r"(r[c + 15]), "=r"(r[c + 16]), "=r"(r[c + 17]), "=r"(r[c + 18]),
+          "=r"(r[c + 19]), "=r"(r[c + 20]), "=r"(r[c + 21]), "=r"(r[c + 22]), "=r"(r[c + 23]), "=r"(r[c + 24]),
+          "=r"(r[c + 25]), "=r"(r[c + 26]), "=r"(r[c + 27]), "=r"(r[c + 28]), "=r"(r[c + 29]), "=r"(r[c + 30]),
+          "=r"(r[c + 31])
+        : "r"(taddr + c));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -145,7 +156,8 @@ struct TcShared {
   uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], ofree[2], done;
   uint32_t tmem;
   int fail;                        // a wait ran out
-  int ended;                       // one of the softmax groups gave up
+  int ended[2];                    // a softmax thread gave up, by turns
+  float swap[2][2][128];           // what the halves of a row tell each other, by turns
   int bad[kTcFlags];               // a tile has a page outside the cache
   unsigned odd[kTcFlags][4];       // its drafted tokens whose values are not all finite
   TreePiece piece;
@@ -159,10 +171,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using S = typename C::S;
   constexpr int TT = C::TT, HV = C::HV, NS = C::NS;
   using T = __nv_bfloat16;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t sq[];  // the swizzle wants whole 1024 bytes
   __shared__ __align__(8) TcShared sh;
-  __shared__ float2 s_stat[128];
-  uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sk = sq + C::Q_BYTES;
   uint8_t* sv = sk + NS * C::K_BYTES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.x;
@@ -172,7 +182,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const TreePiece piece = tree_piece<S>(p, u, u == 0);
     if (lane == 0) {
       sh.piece = piece;
-      sh.fail = sh.ended = 0;
+      sh.fail = sh.ended[0] = sh.ended[1] = 0;
       for (int i = 0; i < NS; ++i) {
         mbar_init(&sh.kfull[i], BOXES ? 1 : 32);
         mbar_init(&sh.kempty[i], 1);
@@ -186,9 +196,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sh.done, 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.sfull[i], 1);
-        mbar_init(&sh.pfull[i], 128);
+        mbar_init(&sh.pfull[i], 256);
         mbar_init(&sh.ofull[i], 1);
-        mbar_init(&sh.ofree[i], 128);
+        mbar_init(&sh.ofree[i], 256);
       }
       fence_mbar_init();
     }
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sh.tmem;
-  // TMEM columns: S and P of the two groups, then O of the two.
+  // TMEM columns: S and P of two tiles, then O of two.
   auto s_col = [&](int w) { return tmem + w * 128; };
   auto o_col = [&](int w) { return tmem + 256 + w * 128; };
   const TreePiece piece = sh.piece;
@@ -210,127 +220,65 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // 72 x 128 + 216 x 256 = 168 x 384.
   if (warp >= 4) {
     take_registers<216>();
-    // ---- softmax: a thread is row `row` of the chunk in every tile of its group
-    const int w = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    // ---- softmax: a thread is half a row, tokens and columns of the output
+    constexpr int ST = TT / 2, OC = HV / 2;  // of a thread
+    const int h = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float scale = p.scale * kTreeLog2e;
-    int suse = 0;               // tiles of this group so far
     int tile_no = 0;            // of this CTA
+    int syncs = 0;              // of the 256 threads
     int4 split = make_int4(0, 0, 0, 0);
-    while (g.valid) {
+    // All 256 threads; true where one of them had given up before.
+    auto meet = [&] {
+      const int slot = syncs++ & 1;
+      if (dead) sh.ended[slot] = 1;
+      __syncwarp();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      return sh.ended[slot] != 0;
+    };
+    bool over = false;
+    while (g.valid && !over) {
       const long long crow = (long long)g.chunk() * 128 + row;
-      const long long rows = (long long)g.s.n * p.group;
-      const bool live = crow < rows;
+      const bool live = crow < (long long)g.s.n * p.group;
       const int draft = live ? (int)(crow / p.group) : g.s.n - 1;
       const int head = g.kv_head(p) * p.group + (int)(live ? crow % p.group : 0);
       const unsigned long long* mask = p.masks ? p.masks + (long long)(g.s.row0 + draft) * p.words : nullptr;
-      const int n = g.t1 - g.t0;
-      float m = kTreeNone, l = 0.f;
-      float2 o[HV / 2];
+      float m = kTreeNone, l = 0.f, kept = 0.f;  // kept: what the tile before scales O by
+      float2 o[OC / 2];
 #pragma unroll
-      for (int e = 0; e < HV / 2; ++e) o[e] = make_float2(0.f, 0.f);
+      for (int e = 0; e < OC / 2; ++e) o[e] = make_float2(0.f, 0.f);
       bool bad = false;
-      for (int i = w; i < n; i += 2) {
-        const int t = g.t0 + i, flag = (tile_no + i) % kTcFlags;
-        if (!dead && !mbar_wait(&sh.sfull[w], suse & 1)) dead = true;
+      // Takes up the output of tile t, number i of this CTA.
+      auto fold = [&](int t, int i) {
+        const int b = i & 1;
+        if (!dead && !mbar_wait(&sh.ofull[b], (i >> 1) & 1)) dead = true;
         dead = __any_sync(0xffffffffu, dead);  // tcgen05.ld below needs the whole warp
-        if (dead) break;
+        if (dead) return;
         tc_fence_after_sync();
-        bad |= sh.bad[flag] != 0;
-        const int d0 = t * TT - g.s.ctx;       // the tile's first token among the drafted ones
-        const bool drafts = d0 + TT > 0;
-        // What the row sees of 32 tokens.
-        auto sees_of = [&](int c) { return drafts ? tree_sees(p, mask, draft, d0 + c * 32, g.s.n) : 0xffffffffu; };
-        float top = kTreeNone;
-#pragma unroll 1
-        for (int c = 0; c < TT / 32; ++c) {
-          float s[32];
-          tmem_ld32(s_col(w) + lanes + c * 32, s);
+        float v[OC];
+        tmem_ld_columns<OC>(o_col(b) + lanes + h * OC, v);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = mul_f32x2(make_float2(s[e], s[e + 1]), make_float2(scale, scale));
-            s[e] = x.x;
-            s[e + 1] = x.y;
-          }
-          const unsigned sees = sees_of(c);
-          if (!__all_sync(0xffffffffu, sees == 0xffffffffu)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(sees >> e & 1)) s[e] = kTreeNone;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
-        }
-        const float now = fmaxf(m, top), base = now == kTreeNone ? 0.f : now;
-        const float keep = tree_pow2(m - base);
-        m = now;
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int c = 0; c < TT / 32; ++c) {
-          float s[32];
-          tmem_ld32(s_col(w) + lanes + c * 32, s);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = fma_f32x2(make_float2(s[e], s[e + 1]), make_float2(scale, scale), make_float2(-base, -base));
-            s[e] = tree_pow2(x.x);
-            s[e + 1] = tree_pow2(x.y);
-          }
-          const unsigned sees = sees_of(c);
-          if (!__all_sync(0xffffffffu, sees == 0xffffffffu)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(sees >> e & 1)) s[e] = 0.f;
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // 16 tokens: 8 columns of first terms, 8 of second ones
-            uint32_t out[16];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int e = half * 16 + q * 2;
-              sum = add_f32x2(sum, make_float2(s[e], s[e + 1]));
-              const uint32_t ab = __float_as_uint(s[e]), bb = __float_as_uint(s[e + 1]);
-              out[q] = __byte_perm(ab, bb, 0x7632);
-              const float2 rest = fma_f32x2(make_float2(s[e], s[e + 1]), make_float2(kTcLift, kTcLift),
-                                            make_float2(__uint_as_float((ab & 0xffff0000u) | 0x80000000u),
-                                                        __uint_as_float((bb & 0xffff0000u) | 0x80000000u)));
-              out[8 + q] = round_pack_bf16x2(rest.x, rest.y);
-            }
-            tmem_st16(s_col(w) + lanes + c * 32 + half * 16, out);
-          }
-        }
-        l = fmaf(l, keep, sum.x + sum.y);
-        tmem_wait_st();
+        for (int e = 0; e < OC / 2; ++e)
+          o[e] = fma_f32x2(o[e], make_float2(kept, kept), make_float2(v[2 * e], v[2 * e + 1]));
         tc_fence_before_sync();
-        mbar_arrive(&sh.pfull[w]);
-        if (!mbar_wait(&sh.ofull[w], suse & 1)) dead = true;
-        dead = __any_sync(0xffffffffu, dead);
-        if (dead) break;
-        tc_fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < HV / 32; ++c) {
-          float v[32];
-          tmem_ld32(o_col(w) + lanes + c * 32, v);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[c * 16 + e] = fma_f32x2(o[c * 16 + e], make_float2(keep, keep), make_float2(v[2 * e], v[2 * e + 1]));
-        }
-        if (drafts) {
+        const int d0 = t * TT - g.s.ctx;
+        if (d0 + TT > 0) {
           // Values that are not finite, for the rows that see them.
 #pragma unroll 1
           for (int c = 0; c < TT / 32; ++c) {
-            unsigned who = sh.odd[flag][c] & tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
+            unsigned who = sh.odd[i % kTcFlags][c];
+            if (who) who &= tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
             while (who) {
               const int j = t * TT + c * 32 + __ffs(who) - 1;
               who &= who - 1;
               const int pg = (int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift);
-              const int page = p.tables[g.seq * p.table_stride + pg];
+              const int page = p.tables[g.seq * p.table_stride + pg], col = g.part(p) * HV + h * OC;
               const T* v = static_cast<const T*>(p.cache.v) + page * p.cache.page_stride +
-                           (j - pg * p.cache.page_size) * p.cache.token_stride + g.kv_head(p) * p.cache.head_stride +
-                           g.part(p) * HV;
+                           (j - pg * p.cache.page_size) * p.cache.token_stride + g.kv_head(p) * p.cache.head_stride + col;
 #pragma unroll
-              for (int e = 0; e < HV / 2; e += 4) {
+              for (int e = 0; e < OC / 2; e += 4) {
                 uint32_t v4[4] = {0, 0, 0, 0};
-                if (2 * e < hd - g.part(p) * HV)
+                if (col + 2 * e < hd)
                   asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
                                : "=r"(v4[0]), "=r"(v4[1]), "=r"(v4[2]), "=r"(v4[3])
                                : "l"(v + 2 * e)
@@ -344,95 +292,114 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-        tc_fence_before_sync();
-        if (i + 2 < n || w == 0) mbar_arrive(&sh.ofree[w]);  // the second group's last: below
-        ++suse;
-      }
-      // The second group leaves what it has where the first can read it.  Both
-      // meet here whatever happened, and end together where one gave up.
-      if (n > 1 && w == 1 && !dead) {
+        mbar_arrive(&sh.ofree[b]);
+      };
+      for (int t = g.t0; t < g.t1; ++t, ++tile_no) {
+        const int b = tile_no & 1;
+        if (!dead && !mbar_wait(&sh.sfull[b], (tile_no >> 1) & 1)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        float s[ST];
+        float top = kTreeNone;
+        if (!dead) {
+          tc_fence_after_sync();
+          bad |= sh.bad[tile_no % kTcFlags] != 0;
+          tmem_ld_columns<ST>(s_col(b) + lanes + h * ST, s);
 #pragma unroll
-        for (int c = 0; c < HV / 32; ++c) {
-          uint32_t v[32];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            v[2 * e] = __float_as_uint(o[c * 16 + e].x);
-            v[2 * e + 1] = __float_as_uint(o[c * 16 + e].y);
+          for (int e = 0; e < ST; e += 2) {
+            const float2 x = mul_f32x2(make_float2(s[e], s[e + 1]), make_float2(scale, scale));
+            s[e] = x.x;
+            s[e + 1] = x.y;
           }
-          tmem_st32(o_col(1) + lanes + c * 32, v);
-        }
-        tmem_wait_st();
-        s_stat[row] = make_float2(m, bad ? -1.f : l);
-        tc_fence_before_sync();
-      }
-      if (dead) {
-        sh.fail = 1;
-        sh.ended = 1;
-      }
-      __syncwarp();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const bool ended = sh.ended != 0;
-      if (n > 1 && w == 0 && !ended) {
-        tc_fence_after_sync();
-        const float2 st = s_stat[row];
-        const float now = fmaxf(m, st.x);
-        const bool none = st.x == kTreeNone;  // nothing seen: its output is zero
-        const float mine = m == kTreeNone ? 0.f : tree_pow2(m - now), other = none ? 0.f : tree_pow2(st.x - now);
-        bad |= st.y < 0.f;
-        l = l * mine + (none ? 0.f : fabsf(st.y) * other);
+          const int d0 = t * TT + h * ST - g.s.ctx;  // this half's first token among the drafted ones
+          if (d0 + ST > 0) {
 #pragma unroll
-        for (int c = 0; c < HV / 32; ++c) {
-          float v[32];
-          tmem_ld32(o_col(1) + lanes + c * 32, v);
+            for (int c = 0; c < ST / 32; ++c) {
+              const unsigned sees = tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = make_float2(o[c * 16 + e].x * mine, o[c * 16 + e].y * mine);
-            o[c * 16 + e] = none ? x : fma_f32x2(make_float2(v[2 * e], v[2 * e + 1]), make_float2(other, other), x);
+              for (int e = 0; e < 32; ++e)
+                if (!(sees >> e & 1)) s[c * 32 + e] = kTreeNone;
+            }
           }
+          float tops[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int e = 4; e < ST; e += 4)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tops[q] = fmaxf(tops[q], s[e + q]);
+          top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+          sh.swap[syncs & 1][h][row] = top;
         }
+        if (meet()) {
+          over = true;
+          break;
+        }
+        const float now = fmaxf(m, fmaxf(top, sh.swap[(syncs - 1) & 1][h ^ 1][row])), base = now == kTreeNone ? 0.f : now;
+        const float keep = tree_pow2(m - base);
         m = now;
-        tc_fence_before_sync();
-      }
-      __syncwarp();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (ended) break;
-      if (n > 1 && w == 1) mbar_arrive(&sh.ofree[1]);
-      if (w == 0) {
-        const bool whole = g.whole();
-        const long long slot = tree_slot<S>(g, u);
-        const int part = g.part(p);
-        if (!whole) {
-          float4* dst = reinterpret_cast<float4*>(p.partial) + slot * (HV / 4) * 128 + row;
+        float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int e = 0; e < HV / 4; ++e) {
-            constexpr float kOff = 1.f / kTcLift;
-            dst[e * 128] = make_float4(o[2 * e].x * kOff, o[2 * e].y * kOff, o[2 * e + 1].x * kOff, o[2 * e + 1].y * kOff);
-          }
-          p.stats[slot * 128 + row] = make_float2(m, bad ? -1.f : l);
-        } else if (live) {
-          if (bad) {
-            atomicOr(p.status, LORA_DEV_BAD_PAGE);
-          } else {
-            const float inv = l == 0.f ? 0.f : 1.f / (l * kTcLift);
-            T* out = static_cast<T*>(p.out.data) + (g.s.row0 + draft) * p.out.row_stride + head * p.out.head_stride + part * HV;
-            const int width = min(HV, hd - part * HV);
+        for (int c = 0; c < ST / 16; ++c) {  // 16 tokens: 8 columns of first terms, 8 of second ones
+          uint32_t out[16];
 #pragma unroll
-            for (int e = 0; e < HV / 8; ++e)
-              if (8 * e < width) {
-                const float2 *v = o + 4 * e;
-                *reinterpret_cast<uint4*>(out + 8 * e) =
-                    make_uint4(round_pack_bf16x2(v[0].x * inv, v[0].y * inv), round_pack_bf16x2(v[1].x * inv, v[1].y * inv),
-                               round_pack_bf16x2(v[2].x * inv, v[2].y * inv), round_pack_bf16x2(v[3].x * inv, v[3].y * inv));
-              }
-            if (part == 0 && p.lse) p.lse[(long long)(g.s.row0 + draft) * p.num_heads + head] = (m + log2f(l)) * kTreeLn2;
+          for (int q = 0; q < 8; ++q) {
+            const float2 x = add_f32x2(make_float2(s[c * 16 + 2 * q], s[c * 16 + 2 * q + 1]), make_float2(-base, -base));
+            const float2 w = make_float2(tree_pow2(x.x), tree_pow2(x.y));
+            sums[q & 1] = add_f32x2(sums[q & 1], w);
+            const uint32_t ab = __float_as_uint(w.x), bb = __float_as_uint(w.y);
+            out[q] = __byte_perm(ab, bb, 0x7632);
+            const float2 rest = fma_f32x2(w, make_float2(kTcLift, kTcLift),
+                                          make_float2(__uint_as_float((ab & 0xffff0000u) | 0x80000000u),
+                                                      __uint_as_float((bb & 0xffff0000u) | 0x80000000u)));
+            out[8 + q] = round_pack_bf16x2(rest.x, rest.y);
           }
+          tmem_st16(s_col(b) + lanes + h * ST + c * 16, out);
         }
-        if (g.t0 == 0 && !whole) split = make_int4(g.seq, g.stream, tree_sharers<S>(p, piece, g, u), 0);
+        l = fmaf(l, keep, (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y));
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&sh.pfull[b]);
+        if (t > g.t0) fold(t - 1, tile_no - 1);  // under this tile's products
+        kept = keep;
       }
-      tile_no += n;
+      if (over) break;
+      fold(g.t1 - 1, tile_no - 1);
+      sh.swap[syncs & 1][h][row] = l;
+      if (meet()) break;
+      l += sh.swap[(syncs - 1) & 1][h ^ 1][row];
+      const bool whole = g.whole();
+      const long long slot = tree_slot<S>(g, u);
+      const int part = g.part(p);
+      if (!whole) {
+        float4* dst = reinterpret_cast<float4*>(p.partial) + (slot * (HV / 4) + h * (OC / 4)) * 128 + row;
+#pragma unroll
+        for (int e = 0; e < OC / 4; ++e) {
+          constexpr float kOff = 1.f / kTcLift;
+          dst[e * 128] = make_float4(o[2 * e].x * kOff, o[2 * e].y * kOff, o[2 * e + 1].x * kOff, o[2 * e + 1].y * kOff);
+        }
+        if (h == 0) p.stats[slot * 128 + row] = make_float2(m, bad ? -1.f : l);
+      } else if (live) {
+        if (bad) {
+          if (h == 0) atomicOr(p.status, LORA_DEV_BAD_PAGE);
+        } else {
+          const float inv = l == 0.f ? 0.f : 1.f / (l * kTcLift);
+          const int col = part * HV + h * OC;
+          T* out = static_cast<T*>(p.out.data) + (g.s.row0 + draft) * p.out.row_stride + head * p.out.head_stride + col;
+#pragma unroll
+          for (int e = 0; e < OC / 8; ++e)
+            if (col + 8 * e < hd) {
+              const float2* v = o + 4 * e;
+              *reinterpret_cast<uint4*>(out + 8 * e) =
+                  make_uint4(round_pack_bf16x2(v[0].x * inv, v[0].y * inv), round_pack_bf16x2(v[1].x * inv, v[1].y * inv),
+                             round_pack_bf16x2(v[2].x * inv, v[2].y * inv), round_pack_bf16x2(v[3].x * inv, v[3].y * inv));
+            }
+          if (h == 0 && part == 0 && p.lse)
+            p.lse[(long long)(g.s.row0 + draft) * p.num_heads + head] = (m + log2f(l)) * kTreeLn2;
+        }
+      }
+      if (g.t0 == 0 && !whole) split = make_int4(g.seq, g.stream, tree_sharers<S>(p, piece, g, u), 0);
       g.next(p);
     }
-    if (w == 0 && row == 0) p.splits[u] = split;
+    if (dead) sh.fail = 1;
+    if (h == 0 && row == 0) p.splits[u] = split;
   } else {
     give_registers<72>();
   if (BOXES && warp < 2) {
@@ -713,48 +680,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---- the products, issued by one lane
     if (lane == 0) {
       constexpr uint32_t s_idesc = idesc_bf16_f32(128, TT), o_idesc = idesc_bf16_f32(128, HV) | kTransposeB;
-      int seg_no = 0, kt = 0, vt = 0;   // segments, tiles of K and of V so far
-      int puse[2] = {0, 0};             // tiles so far of each group
+      int seg_no = 0, kt = 0, vt = 0;  // segments, tiles of K and of V so far
       bool ok = true;
       const uint32_t qa = smem_addr(sq);
       while (g.valid && ok) {
         const int n = g.t1 - g.t0;
         if (!(ok = mbar_wait(&sh.qfull, seg_no & 1))) break;
         auto scores = [&](int i) {
-          const int w = i & 1, st = kt % NS;
+          const int st = kt % NS;
           if (!(ok = mbar_wait(&sh.kfull[st], (kt / NS) & 1))) return;
           tc_fence_after_sync();
           const uint32_t ka = smem_addr(sk + st * C::K_BYTES);
 #pragma unroll
           for (int k = 0; k < HK / 16; ++k)
-            tc_mma_bf16(s_col(w), sw128_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32),
+            tc_mma_bf16(s_col(kt & 1), sw128_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32),
                         sw128_desc(ka + (k >> 2) * (TT * 128) + (k & 3) * 32), s_idesc, k > 0);
           tc_commit(&sh.kempty[st]);
-          tc_commit(&sh.sfull[w]);
+          tc_commit(&sh.sfull[kt & 1]);
           if (i + 1 == n) tc_commit(&sh.qempty);
           ++kt;
         };
         scores(0);
         for (int i = 0; i < n && ok; ++i) {
-          // The next tile's scores go into the other group's columns, whose
+          // The next tile's scores go into the other columns, whose
           // probabilities the products issued before have read.
           if (i + 1 < n) scores(i + 1);
           if (!ok) break;
-          const int w = i & 1, st = vt % NS;
+          const int b = vt & 1, st = vt % NS;
           if (!(ok = mbar_wait(&sh.vfull[st], (vt / NS) & 1))) break;
-          if (!(ok = mbar_wait(&sh.pfull[w], puse[w] & 1))) break;
-          if (puse[w] > 0 && !(ok = mbar_wait(&sh.ofree[w], (puse[w] - 1) & 1))) break;
+          if (!(ok = mbar_wait(&sh.pfull[b], (vt >> 1) & 1))) break;
+          if (vt >= 2 && !(ok = mbar_wait(&sh.ofree[b], ((vt >> 1) - 1) & 1))) break;
           tc_fence_after_sync();
           const uint32_t va = smem_addr(sv + st * C::V_BYTES);
 #pragma unroll
           for (int k = 0; k < TT / 16; ++k)
 #pragma unroll
             for (int term = 0; term < 2; ++term)
-              tc_mma_bf16_ts(o_col(w), s_col(w) + k * 16 + term * 8,
-                             sw128_desc_mn(va + k * 2048, TT * 128), o_idesc, (k > 0 || term > 0));
+              tc_mma_bf16_ts(o_col(b), s_col(b) + k * 16 + term * 8, sw128_desc_mn(va + k * 2048, TT * 128), o_idesc,
+                             (k > 0 || term > 0));
           tc_commit(&sh.vempty[st]);
-          tc_commit(&sh.ofull[w]);
-          ++puse[w];
+          tc_commit(&sh.ofull[b]);
           ++vt;
         }
         if (!ok) break;
