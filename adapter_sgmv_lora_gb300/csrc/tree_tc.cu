@@ -94,9 +94,16 @@ __device__ __forceinline__ void tmem_ld_columns(uint32_t taddr, float (&v)[N]) {
           "=r"(r[c + 25]), "=r"(r[c + 26]), "=r"(r[c + 27]), "=r"(r[c + 28]), "=r"(r[c + 29]), "=r"(r[c + 30]),
           "=r"(r[c + 31])
         : "r"(taddr + c));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+// What was asked for above is there after this, in the registers that are
+// pinned behind it: nothing that uses them moves before the wait.
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void pin(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -148,15 +155,32 @@ struct TcMaps {
   int q_boxes;
 };
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// A barrier serves one thread at a time, so one lane speaks for its warp (256
+// threads on each of a tile's barriers took most of its time: trees of 64 on
+// the 70B attention 460 us, so @@).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
 constexpr int kTcFlags = 8;  // tiles whose notes are kept: more than can be in flight
 
 struct TcShared {
   uint64_t kfull[5], kempty[5], vfull[5], vempty[5];
+  uint64_t told[2];                // the halves of the rows have said something
   uint64_t land[2];                // V tiles that are looked through before they are handed over
   uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], ofree[2], done;
   uint32_t tmem;
   int fail;                        // a wait ran out
-  int ended[2];                    // a softmax thread gave up, by turns
   float swap[2][2][128];           // what the halves of a row tell each other, by turns
   int bad[kTcFlags];               // a tile has a page outside the cache
   unsigned odd[kTcFlags][4];       // its drafted tokens whose values are not all finite
@@ -182,23 +206,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const TreePiece piece = tree_piece<S>(p, u, u == 0);
     if (lane == 0) {
       sh.piece = piece;
-      sh.fail = sh.ended[0] = sh.ended[1] = 0;
+      sh.fail = 0;
       for (int i = 0; i < NS; ++i) {
-        mbar_init(&sh.kfull[i], BOXES ? 1 : 32);
+        mbar_init(&sh.kfull[i], 1);
         mbar_init(&sh.kempty[i], 1);
-        mbar_init(&sh.vfull[i], BOXES ? 1 : 32);
+        mbar_init(&sh.vfull[i], 1);
         mbar_init(&sh.vempty[i], 1);
       }
-      mbar_init(&sh.qfull, BOXES && maps.q_boxes ? 1 : 32);
+      mbar_init(&sh.qfull, 1);
+      mbar_init(&sh.told[0], 8);
+      mbar_init(&sh.told[1], 8);
       mbar_init(&sh.land[0], 1);
       mbar_init(&sh.land[1], 1);
       mbar_init(&sh.qempty, 1);
       mbar_init(&sh.done, 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.sfull[i], 1);
-        mbar_init(&sh.pfull[i], 256);
+        mbar_init(&sh.pfull[i], 8);
         mbar_init(&sh.ofull[i], 1);
-        mbar_init(&sh.ofree[i], 256);
+        mbar_init(&sh.ofree[i], 8);
       }
       fence_mbar_init();
     }
@@ -217,9 +243,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   TreeSegment<S> g;
   g.first(p, piece);
   bool dead = false;  // a wait ran out: nothing more is waited for
-  // 72 x 128 + 216 x 256 = 168 x 384.
+  // 88 x 128 + 208 x 256 = 168 x 384.
   if (warp >= 4) {
-    take_registers<216>();
+    take_registers<208>();
     // ---- softmax: a thread is half a row, tokens and columns of the output
     constexpr int ST = TT / 2, OC = HV / 2;  // of a thread
     const int h = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
@@ -228,111 +254,97 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int tile_no = 0;            // of this CTA
     int syncs = 0;              // of the 256 threads
     int4 split = make_int4(0, 0, 0, 0);
-    // All 256 threads; true where one of them had given up before.
-    auto meet = [&] {
-      const int slot = syncs++ & 1;
-      if (dead) sh.ended[slot] = 1;
-      __syncwarp();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      return sh.ended[slot] != 0;
+    // Tells the other half of the row a value, and learns its own.
+    auto tell = [&](float v) {
+      sh.swap[syncs & 1][h][row] = v;
+      warp_arrive(&sh.told[syncs & 1]);
     };
-    bool over = false;
-    while (g.valid && !over) {
+    auto learn = [&] {
+      if (!dead && !warp_wait(&sh.told[syncs & 1], (syncs >> 1) & 1)) dead = true;
+      return sh.swap[syncs++ & 1][h ^ 1][row];
+    };
+    while (g.valid && !dead) {
       const long long crow = (long long)g.chunk() * 128 + row;
       const bool live = crow < (long long)g.s.n * p.group;
       const int draft = live ? (int)(crow / p.group) : g.s.n - 1;
       const int head = g.kv_head(p) * p.group + (int)(live ? crow % p.group : 0);
       const unsigned long long* mask = p.masks ? p.masks + (long long)(g.s.row0 + draft) * p.words : nullptr;
-      float m = kTreeNone, l = 0.f, kept = 0.f;  // kept: what the tile before scales O by
+      float m = kTreeNone, l = 0.f;
+      const int first_no = tile_no;
+      float kept0 = 0.f, kept1 = 0.f;  // what the tiles two and one before scale O by
       float2 o[OC / 2];
 #pragma unroll
       for (int e = 0; e < OC / 2; ++e) o[e] = make_float2(0.f, 0.f);
-      bool bad = false;
+      bool bad = false, strange = false;  // a page outside the cache; values of drafted tokens that are not finite
       // Takes up the output of tile t, number i of this CTA.
-      auto fold = [&](int t, int i) {
-        const int b = i & 1;
-        if (!dead && !mbar_wait(&sh.ofull[b], (i >> 1) & 1)) dead = true;
-        dead = __any_sync(0xffffffffu, dead);  // tcgen05.ld below needs the whole warp
-        if (dead) return;
+      auto fold = [&](float kept, int t, int i) {
+        if (dead || !warp_wait(&sh.ofull[i & 1], (i >> 1) & 1)) {
+          dead = true;
+          return;
+        }
         tc_fence_after_sync();
-        float v[OC];
-        tmem_ld_columns<OC>(o_col(b) + lanes + h * OC, v);
 #pragma unroll
-        for (int e = 0; e < OC / 2; ++e)
-          o[e] = fma_f32x2(o[e], make_float2(kept, kept), make_float2(v[2 * e], v[2 * e + 1]));
+        for (int c = 0; c < OC; c += 32) {
+          float v[32];
+          tmem_ld_columns<32>(o_col(i & 1) + lanes + h * OC + c, v);
+          tmem_wait_ld();
+          pin(v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[c / 2 + e] = fma_f32x2(o[c / 2 + e], make_float2(kept, kept), make_float2(v[2 * e], v[2 * e + 1]));
+        }
+        if (t * TT + TT > g.s.ctx) {
+          const unsigned* odd = sh.odd[i % kTcFlags];
+          strange |= (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+        }
         tc_fence_before_sync();
-        const int d0 = t * TT - g.s.ctx;
-        if (d0 + TT > 0) {
-          // Values that are not finite, for the rows that see them.
-#pragma unroll 1
-          for (int c = 0; c < TT / 32; ++c) {
-            unsigned who = sh.odd[i % kTcFlags][c];
-            if (who) who &= tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
-            while (who) {
-              const int j = t * TT + c * 32 + __ffs(who) - 1;
-              who &= who - 1;
-              const int pg = (int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift);
-              const int page = p.tables[g.seq * p.table_stride + pg], col = g.part(p) * HV + h * OC;
-              const T* v = static_cast<const T*>(p.cache.v) + page * p.cache.page_stride +
-                           (j - pg * p.cache.page_size) * p.cache.token_stride + g.kv_head(p) * p.cache.head_stride + col;
-#pragma unroll
-              for (int e = 0; e < OC / 2; e += 4) {
-                uint32_t v4[4] = {0, 0, 0, 0};
-                if (col + 2 * e < hd)
-                  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                               : "=r"(v4[0]), "=r"(v4[1]), "=r"(v4[2]), "=r"(v4[3])
-                               : "l"(v + 2 * e)
-                               : "memory");
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  if ((v4[q] & 0x7f80u) == 0x7f80u) o[e + q].x += __uint_as_float(v4[q] << 16);
-                  if ((v4[q] & 0x7f800000u) == 0x7f800000u) o[e + q].y += __uint_as_float(v4[q] & 0xffff0000u);
-                }
-              }
-            }
-          }
-        }
-        mbar_arrive(&sh.ofree[b]);
+        warp_arrive(&sh.ofree[i & 1]);
       };
-      for (int t = g.t0; t < g.t1; ++t, ++tile_no) {
-        const int b = tile_no & 1;
-        if (!dead && !mbar_wait(&sh.sfull[b], (tile_no >> 1) & 1)) dead = true;
-        dead = __any_sync(0xffffffffu, dead);
-        float s[ST];
-        float top = kTreeNone;
-        if (!dead) {
-          tc_fence_after_sync();
-          bad |= sh.bad[tile_no % kTcFlags] != 0;
-          tmem_ld_columns<ST>(s_col(b) + lanes + h * ST, s);
+      // Two steps more than tiles: the output of a tile is taken up two later.
+#pragma unroll 1
+      for (int t = g.t0; t < g.t1 + 2; ++t) {
+        const int b = tile_no & 1, number = first_no + (t - g.t0);
+        const bool scores = t < g.t1;
+        float s[ST], top = kTreeNone;
+        if (scores) {
+        if (!warp_wait(&sh.sfull[b], (tile_no >> 1) & 1)) dead = true;
+        if (dead) break;
+        tc_fence_after_sync();
+        bad |= sh.bad[tile_no % kTcFlags] != 0;
+        tmem_ld_columns<ST>(s_col(b) + lanes + h * ST, s);
+        tmem_wait_ld();
+        pin(s);
 #pragma unroll
-          for (int e = 0; e < ST; e += 2) {
-            const float2 x = mul_f32x2(make_float2(s[e], s[e + 1]), make_float2(scale, scale));
-            s[e] = x.x;
-            s[e + 1] = x.y;
-          }
-          const int d0 = t * TT + h * ST - g.s.ctx;  // this half's first token among the drafted ones
-          if (d0 + ST > 0) {
-#pragma unroll
-            for (int c = 0; c < ST / 32; ++c) {
-              const unsigned sees = tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(sees >> e & 1)) s[c * 32 + e] = kTreeNone;
-            }
-          }
-          float tops[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int e = 4; e < ST; e += 4)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tops[q] = fmaxf(tops[q], s[e + q]);
-          top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-          sh.swap[syncs & 1][h][row] = top;
+        for (int e = 0; e < ST; e += 2) {
+          const float2 x = mul_f32x2(make_float2(s[e], s[e + 1]), make_float2(scale, scale));
+          s[e] = x.x;
+          s[e + 1] = x.y;
         }
-        if (meet()) {
-          over = true;
-          break;
+        const int d0 = t * TT + h * ST - g.s.ctx;  // this half's first token among the drafted ones
+        if (d0 + ST > 0) {
+#pragma unroll
+          for (int c = 0; c < ST / 32; ++c) {
+            const unsigned sees = tree_sees(p, mask, draft, d0 + c * 32, g.s.n);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(sees >> e & 1)) s[c * 32 + e] = kTreeNone;
+          }
         }
-        const float now = fmaxf(m, fmaxf(top, sh.swap[(syncs - 1) & 1][h ^ 1][row])), base = now == kTreeNone ? 0.f : now;
+        float tops[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int e = 4; e < ST; e += 4)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tops[q] = fmaxf(tops[q], s[e + q]);
+        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        tell(top);
+        }
+        if (t >= g.t0 + 2) fold(kept0, t - 2, number - 2);  // until the other half has spoken
+        if (dead) break;
+        if (!scores) {
+          kept0 = kept1;
+          continue;
+        }
+        const float now = fmaxf(m, fmaxf(top, learn())), base = now == kTreeNone ? 0.f : now;
         const float keep = tree_pow2(m - base);
         m = now;
         float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -356,17 +368,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         l = fmaf(l, keep, (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y));
         tmem_wait_st();
         tc_fence_before_sync();
-        mbar_arrive(&sh.pfull[b]);
-        if (t > g.t0) fold(t - 1, tile_no - 1);  // under this tile's products
-        kept = keep;
+        warp_arrive(&sh.pfull[b]);
+        kept0 = kept1;
+        kept1 = keep;
+        ++tile_no;
       }
-      if (over) break;
-      fold(g.t1 - 1, tile_no - 1);
-      sh.swap[syncs & 1][h][row] = l;
-      if (meet()) break;
-      l += sh.swap[(syncs - 1) & 1][h ^ 1][row];
+      if (dead) break;
+      tell(l);
+      l += learn();
+      if (dead) break;
       const bool whole = g.whole();
-      const long long slot = tree_slot<S>(g, u);
+      const long long slot = whole ? 0 : tree_slot<S>(g, u);
       const int part = g.part(p);
       if (!whole) {
         float4* dst = reinterpret_cast<float4*>(p.partial) + (slot * (HV / 4) + h * (OC / 4)) * 128 + row;
@@ -395,13 +407,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             p.lse[(long long)(g.s.row0 + draft) * p.num_heads + head] = (m + log2f(l)) * kTreeLn2;
         }
       }
+      if (strange && live && !bad) {
+        // They went into the products as 0: the rows that see them take them now.
+        const int col = part * HV + h * OC;
+        for (int j = max(g.s.ctx, g.t0 * TT); j < min(g.s.len, g.t1 * TT); ++j) {
+          const int d = j - g.s.ctx;
+          if (!(tree_sees(p, mask, draft, d & ~31, g.s.n) >> (d & 31) & 1)) continue;
+          const int pg = (int)(((unsigned long long)(unsigned)j * p.page_magic) >> p.page_shift);
+          const T* v = static_cast<const T*>(p.cache.v) + p.tables[g.seq * p.table_stride + pg] * p.cache.page_stride +
+                       (j - pg * p.cache.page_size) * p.cache.token_stride + g.kv_head(p) * p.cache.head_stride + col;
+          T* out = static_cast<T*>(p.out.data) + (g.s.row0 + draft) * p.out.row_stride + head * p.out.head_stride + col;
+          float* sum = p.partial + ((slot * (HV / 4) + h * (OC / 4)) * 128 + row) * 4;
+          for (int c = 0; c < min(OC, hd - col); ++c) {
+            const float x = __bfloat162float(v[c]);
+            if (fabsf(x) < __builtin_huge_valf()) continue;
+            if (whole) out[c] = __float2bfloat16_rn(__bfloat162float(out[c]) + x);
+            else sum[(c >> 2) * 512 + (c & 3)] += x;
+          }
+        }
+      }
       if (g.t0 == 0 && !whole) split = make_int4(g.seq, g.stream, tree_sharers<S>(p, piece, g, u), 0);
       g.next(p);
     }
     if (dead) sh.fail = 1;
     if (h == 0 && row == 0) p.splits[u] = split;
   } else {
-    give_registers<72>();
+    give_registers<88>();
   if (BOXES && warp < 2) {
     // ---- loads of K (warp 0) or V (warp 1), a box a lane
     const bool is_k = warp == 0;
@@ -419,8 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto look_through = [&] {
       if (!look.open) return;
       look.open = false;
-      if (!mbar_wait(&sh.land[looked & 1], (looked >> 1) & 1)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
+      if (!warp_wait(&sh.land[looked & 1], (looked >> 1) & 1)) dead = true;
       ++looked;
       if (dead) return;
       // Drafted tokens' values that are infinite or NaN would reach rows that
@@ -458,8 +488,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       __syncwarp();
       fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[look.tile % NS]);
+      warp_arrive(&full[look.tile % NS]);
     };
     int issued = 0;  // tiles that are looked through, so far issued
     while (g.valid) {
@@ -479,8 +508,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int from = out ? p.cache.num_pages : page;  // behind the last page: zeros
         if (t + 1 < g.t1) page = look_up(t + 1);
         const int stage = tile_no % NS;
-        if (tile_no >= NS && !dead && !mbar_wait(&empty[stage], (tile_no / NS - 1) & 1)) dead = true;
-        dead = __any_sync(0xffffffffu, dead);
+        if (tile_no >= NS && !dead && !warp_wait(&empty[stage], (tile_no / NS - 1) & 1)) dead = true;
         if (dead) break;
         if (is_k && lane == 0) sh.bad[tile_no % kTcFlags] = bad;
         const bool through = !is_k && t * TT + TT > g.s.ctx;
@@ -559,7 +587,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
       }
       fence_proxy_async_smem();
-      mbar_arrive(&full[handed % NS]);
+      warp_arrive(&full[handed % NS]);
       n0 = n1;
       n1 = n2;
       --waiting;
@@ -596,8 +624,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (tile_no >= NS && !dead) {
           // While the stage is still in use, what has landed is handed over.
           while (waiting > 0 && !__all_sync(0xffffffffu, mbar_test(&empty[stage], (tile_no / NS - 1) & 1))) hand_over();
-          if (!mbar_wait(&empty[stage], (tile_no / NS - 1) & 1)) dead = true;
-          dead = __any_sync(0xffffffffu, dead);
+          if (!warp_wait(&empty[stage], (tile_no / NS - 1) & 1)) dead = true;
         }
         if (dead) {
           if (lane == 0) sh.fail = 1;
@@ -640,8 +667,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---- loads of Q: a chunk's rows, once a segment
     int seg_no = 0;
     while (g.valid) {
-      if (seg_no > 0 && !mbar_wait(&sh.qempty, (seg_no - 1) & 1)) dead = true;
-      if (__any_sync(0xffffffffu, dead)) break;
+      if (seg_no > 0 && !warp_wait(&sh.qempty, (seg_no - 1) & 1)) break;
       const int kv = g.kv_head(p);
       if (BOXES && maps.q_boxes) {
         // Rows behind the sequence's are other sequences' or zero: of no effect.
@@ -671,62 +697,69 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       cp_async_commit();
       cp_async_wait<0>();
       fence_proxy_async_smem();
-      mbar_arrive(&sh.qfull);
+      warp_arrive(&sh.qfull);
       ++seg_no;
       g.next(p);
     }
     cp_async_wait<0>();
   } else if (warp == 3) {
-    // ---- the products, issued by one lane
-    if (lane == 0) {
-      constexpr uint32_t s_idesc = idesc_bf16_f32(128, TT), o_idesc = idesc_bf16_f32(128, HV) | kTransposeB;
-      int seg_no = 0, kt = 0, vt = 0;  // segments, tiles of K and of V so far
-      bool ok = true;
-      const uint32_t qa = smem_addr(sq);
-      while (g.valid && ok) {
-        const int n = g.t1 - g.t0;
-        if (!(ok = mbar_wait(&sh.qfull, seg_no & 1))) break;
-        auto scores = [&](int i) {
+    // ---- the products.  The whole warp goes along, so that what the
+    // instructions are given is uniform, and one lane issues them.
+    constexpr uint32_t s_idesc = idesc_bf16_f32(128, TT), o_idesc = idesc_bf16_f32(128, HV) | kTransposeB;
+    const bool leader = elect_one();
+    int seg_no = 0, kt = 0, vt = 0;  // segments, tiles of K and of V so far
+    bool ok = true;
+    const uint64_t qd = sw128_desc(smem_addr(sq)), kd0 = sw128_desc(smem_addr(sk)),
+                   vd0 = sw128_desc_mn(smem_addr(sv), TT * 128);
+    while (ok && __shfl_sync(0xffffffffu, (int)g.valid, 0)) {
+      const int n = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
+      if (!(ok = warp_wait(&sh.qfull, seg_no & 1))) break;
+#pragma unroll 1
+      for (int i = 0; i <= n; ++i) {
+        // A tile's scores go out before the output of the tile before, into
+        // the columns whose probabilities the products issued last have read.
+        if (i < n) {
           const int st = kt % NS;
-          if (!(ok = mbar_wait(&sh.kfull[st], (kt / NS) & 1))) return;
+          if (!(ok = warp_wait(&sh.kfull[st], (kt / NS) & 1))) break;
           tc_fence_after_sync();
-          const uint32_t ka = smem_addr(sk + st * C::K_BYTES);
+          const uint64_t kd = kd0 + st * (C::K_BYTES / 16);
+          const uint32_t d = s_col(kt & 1);
+          if (leader) {
 #pragma unroll
-          for (int k = 0; k < HK / 16; ++k)
-            tc_mma_bf16(s_col(kt & 1), sw128_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32),
-                        sw128_desc(ka + (k >> 2) * (TT * 128) + (k & 3) * 32), s_idesc, k > 0);
-          tc_commit(&sh.kempty[st]);
-          tc_commit(&sh.sfull[kt & 1]);
-          if (i + 1 == n) tc_commit(&sh.qempty);
+            for (int k = 0; k < HK / 16; ++k)
+              tc_mma_bf16(d, qd + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16,
+                          kd + ((k >> 2) * (TT * 128) + (k & 3) * 32) / 16, s_idesc, k > 0);
+            tc_commit(&sh.kempty[st]);
+            tc_commit(&sh.sfull[kt & 1]);
+            if (i + 1 == n) tc_commit(&sh.qempty);
+          }
+          __syncwarp();
           ++kt;
-        };
-        scores(0);
-        for (int i = 0; i < n && ok; ++i) {
-          // The next tile's scores go into the other columns, whose
-          // probabilities the products issued before have read.
-          if (i + 1 < n) scores(i + 1);
-          if (!ok) break;
-          const int b = vt & 1, st = vt % NS;
-          if (!(ok = mbar_wait(&sh.vfull[st], (vt / NS) & 1))) break;
-          if (!(ok = mbar_wait(&sh.pfull[b], (vt >> 1) & 1))) break;
-          if (vt >= 2 && !(ok = mbar_wait(&sh.ofree[b], ((vt >> 1) - 1) & 1))) break;
-          tc_fence_after_sync();
-          const uint32_t va = smem_addr(sv + st * C::V_BYTES);
+        }
+        if (i == 0) continue;
+        const int b = vt & 1, st = vt % NS;
+        if (!(ok = warp_wait(&sh.vfull[st], (vt / NS) & 1))) break;
+        if (!(ok = warp_wait(&sh.pfull[b], (vt >> 1) & 1))) break;
+        if (vt >= 2 && !(ok = warp_wait(&sh.ofree[b], ((vt >> 1) - 1) & 1))) break;
+        tc_fence_after_sync();
+        const uint64_t vd = vd0 + st * (C::V_BYTES / 16);
+        const uint32_t d = o_col(b), a = s_col(b);
+        if (leader) {
 #pragma unroll
-          for (int k = 0; k < TT / 16; ++k)
-#pragma unroll
-            for (int term = 0; term < 2; ++term)
-              tc_mma_bf16_ts(o_col(b), s_col(b) + k * 16 + term * 8, sw128_desc_mn(va + k * 2048, TT * 128), o_idesc,
-                             (k > 0 || term > 0));
+          for (int k = 0; k < TT / 8; ++k)  // the two terms in turn
+            tc_mma_bf16_ts(d, a + k * 8, vd + (k >> 1) * (2048 / 16), o_idesc, k > 0);
           tc_commit(&sh.vempty[st]);
           tc_commit(&sh.ofull[b]);
-          ++vt;
         }
-        if (!ok) break;
-        ++seg_no;
-        g.next(p);
+        __syncwarp();
+        ++vt;
       }
-      if (!ok) atomicExch(&sh.fail, 1);
+      if (!ok) break;
+      ++seg_no;
+      g.next(p);
+    }
+    if (leader) {
+      if (!ok) sh.fail = 1;
       tc_commit(&sh.done);
     }
     __syncwarp();
