@@ -169,7 +169,10 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  bool ok = false;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit && !ok; ++i) ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+  return ok;
 }
 
 constexpr int kTcFlags = 8;  // tiles whose notes are kept: more than can be in flight
