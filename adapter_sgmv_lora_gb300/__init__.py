@@ -45,8 +45,8 @@ PATH_PREP, PATH_BASE_GEMM = 0x80, 0x100
 PATH_ROPE, PATH_GENERIC_ROPE = 0x200, 0x400
 PATH_MMA_ATTENTION, PATH_GENERIC_ATTENTION, PATH_JOIN = 0x800, 0x1000, 0x2000
 PATH_PAGES = 0x4000
-PATH_MMA_Q4, PATH_TC_Q4, PATH_GENERIC_Q4 = 0x8000, 0x10000, 0x20000
-PATH_TC_TREE, PATH_GENERIC_TREE, PATH_KEEP = 0x40000, 0x80000, 0x100000
+PATH_MMA_Q4, PATH_GENERIC_Q4 = 0x8000, 0x10000
+PATH_TC_TREE, PATH_GENERIC_TREE, PATH_KEEP, PATH_TC_Q4 = 0x20000, 0x40000, 0x80000, 0x100000
 MAX_SLICES = 3
 
 

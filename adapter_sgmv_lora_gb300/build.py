@@ -18,7 +18,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "routing.cpp", "simple_kernels.cu", "sgmv_bf16.cu", "sgmv_tc.cu", "sgmv_base.cu",
            "attention_api.cu", "pages.cpp", "rope.cu", "attention_generic.cu", "attention_mma.cu",
-           "page_copy.cu", "q4.cu", "tree_generic.cu", "tree_tc.cu",
+           "page_copy.cu", "q4.cu", "q4_tc.cu", "tree_generic.cu", "tree_tc.cu",
            "keep_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",

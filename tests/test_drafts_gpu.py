@@ -187,6 +187,10 @@ Q4_CASES = [
 def test_q4(case, zeros):
     c = Q4Case(*case, zeros=zeros)
     c.run()
+    n, group, dtype = case[1], case[3], case[5]
+    fast = dtype == BF and n % 32 == 0 and (group % 32 == 0 or group >= n)
+    path = lk.lora_last_call_path()[0]
+    assert bool(path & (lk.PATH_MMA_Q4 | lk.PATH_TC_Q4)) == fast and bool(path & lk.PATH_GENERIC_Q4) == (not fast)
     c.check()
     first = c.y.clone()
     c.run()
@@ -221,6 +225,77 @@ def test_q4_extremes(T):
         c.x.fill_(3.0)
         c.run()
         c.check()
+
+
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 16])
+@pytest.mark.parametrize("n,group", [(96, 32), (320, 64), (512, 128), (1024, 1024)])
+def test_q4_many_outputs(T, n, group):
+    """More tiles of outputs than CTAs: few rows that walk them, odd ends, a slice that ends inside a tile."""
+    outs = [9800, 40, 233]
+    c = Q4Case(T, n, outs, group, 32, BF, [T // 3, None, T - T // 3 - T // 4], bias=True, ranks=True, x_gap=8, y_gap=7,
+               q_gap=16, extra_zero=T == 3)
+    c.run()
+    assert lk.lora_last_call_path()[0] & lk.PATH_MMA_Q4
+    c.check()
+    clean = c.y.clone()
+    if T > 1:
+        c.x[T - 1, n - 1] = NAN
+        c.x[0, 3] = float("inf")
+        c.run()
+        assert torch.equal(c.y[1:T - 1], clean[1:T - 1])
+        assert torch.isnan(c.y[T - 1]).all() and torch.isfinite(c.y[0]).sum() < 9800 // 2
+
+
+@pytest.mark.parametrize("T,n,group,outs,R", [
+    (300, 192, 64, [4000, 40], 16), (700, 640, 128, [2056, 1000, 77], 64), (513, 224, 192, [4096], 128),
+    (512, 96, 96, [5000], 8), (130, 320, 64, [16000], 256), (48, 256, 128, [9900, 300], 24), (401, 128, 128, [4130], 3)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_q4_many_rows(T, n, group, outs, R, zeros):
+    """Enough work for the kernel on tcgen05: odd ends, groups of one and two blocks, runs of rows within and across
+    tiles, base rows between a tile's runs and the end."""
+    counts = [T // 5, 1, None, 0, T // 10, T // 2 - 1]
+    c = Q4Case(T, n, outs, group, R, BF, counts, S=6, zeros=zeros, bias=True, ranks=R >= 16, x_gap=8, y_gap=3,
+               q_gap=16, extra_zero=zeros and T == 300)
+    c.run()
+    assert lk.lora_last_call_path()[0] & lk.PATH_TC_Q4
+    c.check()
+    clean = c.y.clone()
+    c.run()
+    assert torch.equal(c.y, clean)
+    # what a slot or a row holds stays with its own rows
+    c.x[T - 1, n - 1] = NAN
+    c.x[2, 1] = float("inf")
+    c.b[1] = NAN
+    c.run()
+    row = int(c.offs[1])
+    read = c.slot_ranks is None or int(c.slot_ranks[1]) > 0   # of a slot of rank 0 nothing is read
+    others = [t for t in range(T) if t not in (2, T - 1) and not (read and t == row)]
+    assert torch.equal(c.y[others], clean[others])
+    assert torch.isnan(c.y[T - 1]).all() and (not read or torch.isnan(c.y[row]).all())
+
+
+def test_q4_many_rows_streams_graph_and_bad_routing():
+    c = Q4Case(300, 256, [4000, 64], 64, 16, BF, [100, 0, 90])
+    want = c.run().clone()
+    assert lk.lora_last_call_path()[0] & lk.PATH_TC_Q4
+    c.y.fill_(NAN)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.run(stream=s)
+    s.synchronize()
+    assert torch.equal(c.y, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run()
+    c.y.fill_(NAN)
+    c.x.copy_(randn(c.x.shape, BF, 98))
+    g.replay()
+    c.check()
+    c.y.fill_(NAN)
+    c.routing.lora_ids.fill_(77)
+    c.run()
+    assert lk.lora_get_device_status() & lk.DEV_BAD_SLOT
+    assert torch.isnan(c.y).all()
 
 
 def test_q4_row_with_infinity_and_nan():
@@ -420,6 +495,8 @@ def test_tree(case, masks):
     dtype, (rows, ctx), H, Hk, hd, ps, order = case
     a = tree_case(list(rows), list(ctx), H, Hk, hd, ps, dtype, order, masks, pad=3)
     out, lse = run_tree(a)
+    tc = dtype == BF and hd % 8 == 0 and order != "gap"
+    assert lk.lora_last_call_path()[0] & ~lk.PATH_JOIN == (lk.PATH_TC_TREE if tc else lk.PATH_GENERIC_TREE)
     seqs = None if len(rows) < 30 else list(range(0, len(rows), 13)) + [len(rows) - 1]
     check_tree(a, out, lse, seqs=seqs)
     again, lse2 = run_tree(a)
