@@ -18,13 +18,13 @@
 // block's copies, waits and barriers take longer than its arithmetic, so several
 // are under way (all eight on one block at a time: gate and up of the 8B model,
 // 28672 outputs of 4096 inputs, 128 rows, 146 us, so 119; the delta's planes
-// summed by all of them and one thread issuing the products: 100).  Every wait is
+// summed by all of them and one thread issuing the products: 92).  Every wait is
 // bounded.
 //
-// Gate and up take 91 us for 64 rows, 100 for 128, 150 for 256; q4.cu's tiles
+// Gate and up take 80 us for 64 rows, 92 for 128, 137 for 256; q4.cu's tiles
 // 122, 229 and 441.  What bounds it is the way of a block through the barriers,
-// about 900 cycles whatever the rows: leaving out the unpacking saved 11%, three
-// of four products 12%, the scaling 2%, more stages nothing.
+// some 800 cycles whatever the rows: leaving out the unpacking saves 8%, with
+// three of four products and of the stores 15%, the scaling or x nothing.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -94,6 +94,12 @@ __device__ __forceinline__ uint4 unpack_in_order(uint32_t w, uint32_t low) {
     return sub_bf16x2((__byte_perm(even, odd, order) & 0x000f000fu) | 0x43004300u, low);
   };
   return make_uint4(pair(0x4400), pair(0x5511), pair(0x6622), pair(0x7733));
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // FOLD: blocks of 64 inputs whose products are summed before they are scaled.
@@ -342,14 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && mbar_wait(&sh.full[stage], turn);
       if (!ok) return;
       tc_fence_after_sync();
-      if (lane == 0) {
-        const uint32_t to = tmem + (m & 1) * 128;
-        tc_mma_bf16(to, a, x, idesc, first ? 0u : 1u);
+      const uint32_t to = tmem + (m & 1) * 128;
+      tc_mma_bf16(to, a, x, idesc, first ? 0u : 1u);
 #pragma unroll
-        for (int ks = 1; ks < kK / 16; ++ks) tc_mma_bf16(to, a + ks * 2, x + ks * 2, idesc, 1u);
-        tc_commit(&sh.empty[stage]);
-        if (last) tc_commit(&sh.sum[m & 1]);
-      }
+      for (int ks = 1; ks < kK / 16; ++ks) tc_mma_bf16(to, a + ks * 2, x + ks * 2, idesc, 1u);
+      tc_commit(&sh.empty[stage]);
+      if (last) tc_commit(&sh.sum[m & 1]);
       ++i;
       m += last;
       a += stage_bytes >> 4;
@@ -361,15 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         x = x0;
       }
     };
-    if (lane == 0) {
-    while (i < nb && ok) block(i % FOLD == 0, i % FOLD == FOLD - 1 || i == nb - 1);
-    for (int span = 0; span < p.R && ok; span += kSpan)
-      delta_blocks(sh, span, [&](int, int) {
-        block(true, true);
-        return ok;
-      });
-    }
-    if (lane == 0) {
+    // An elected thread, not lane 0: the products' operands are then known to be
+    // the warp's (trees on the 70B qkv 191 us, so 172).
+    if (elect_one()) {
+      while (i < nb && ok) block(i % FOLD == 0, i % FOLD == FOLD - 1 || i == nb - 1);
+      for (int span = 0; span < p.R && ok; span += kSpan)
+        delta_blocks(sh, span, [&](int, int) {
+          block(true, true);
+          return ok;
+        });
       if (!ok && good) sh.fail = 1;
       tc_commit(&sh.done);
     }
@@ -529,10 +533,10 @@ bool q4_tc_ok(const ProblemDesc& p, const Q4Weights& w) {
     small += (p.sl[j].out_dim + 31) / 32;
   }
   // A wave of this kernel takes what two and a half of q4.cu's 32 x 32 tiles do,
-  // two to an SM.  us here and there, 4096 inputs: 4096 outputs 60 and 46 (128
-  // rows), 54 and 59 (160), 62 and 151 (512); 10240 outputs 50 and 54 (48), 71
-  // and 108 (128), 186 and 387 (512); 28672 outputs 103 and 68 (32), 96 and 121
-  // (48), 130 and 272 (128), 412 and 1052 (512).
+  // two to an SM.  us here and there, 4096 inputs, rank 32: 4096 outputs 54
+  // and 46 (128 rows), 47 and 59 (160), 55 and 151 (512); 10240 outputs 42 and 54
+  // (48), 65 and 108 (128), 175 and 387 (512); 28672 outputs 80 and 68 (32), 81
+  // and 121 (48), 119 and 272 (128), 375 and 1052 (512).
   const long long waves = (tiles * row_tiles + sms - 1) / sms;
   const long long there = (small * ((p.num_tokens + 31) / 32) + 2 * sms - 1) / (2 * sms);
   return p.num_tokens > 16 && 2 * there > 5 * waves;
