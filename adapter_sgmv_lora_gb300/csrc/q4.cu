@@ -53,17 +53,28 @@ __global__ void __launch_bounds__(kWarps * 32) q4_simple_kernel(const __grid_con
     const int rows = min(kRows, p.num_tokens - t0);
     const T* x = static_cast<const T*>(p.x) + t0 * p.x_row_stride;
     float acc[kRows] = {};
+    int slot_of = -1, kmax_of = 0;  // of row t0 + lane
+    if (lane < rows && t0 + lane < p.end) {
+      slot_of = p.lora_ids[group_of_row(p, t0 + lane)];
+      kmax_of = slot_kmax(p, slot_of);
+    }
     for (int i = 2 * lane; i < p.in_dim; i += 64) {
       const int code = q[i >> 1], g = i / d.group, g1 = (i + 1) / d.group;
       const bool two = i + 1 < p.in_dim;
       const float w0 = value(scales[g]) * (float)((code & 15) - (zeros ? zeros[g] : 8));
       const float w1 = two ? value(scales[g1]) * (float)((code >> 4) - (zeros ? zeros[g1] : 8)) : 0.f;
+      // Rows past the last read it again, so that all loads are under way at once.
+      float x0[kRows], x1[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        if (r >= rows) break;
-        const T* xr = x + r * p.x_row_stride + i;
-        acc[r] = fmaf(w0, value(xr[0]), acc[r]);
-        if (two) acc[r] = fmaf(w1, value(xr[1]), acc[r]);
+        const T* xr = x + min(r, rows - 1) * p.x_row_stride + i;
+        x0[r] = value(xr[0]);
+        x1[r] = value(xr[two]);
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        acc[r] = fmaf(w0, x0[r], acc[r]);
+        if (two) acc[r] = fmaf(w1, x1[r], acc[r]);
       }
     }
 #pragma unroll
@@ -71,8 +82,7 @@ __global__ void __launch_bounds__(kWarps * 32) q4_simple_kernel(const __grid_con
       if (r >= rows) break;
       const int t = t0 + r;
       if (t < p.end) {
-        const int slot = p.lora_ids[group_of_row(p, t)];
-        const int kmax = slot_kmax(p, slot);
+        const int slot = __shfl_sync(0xffffffffu, slot_of, r), kmax = __shfl_sync(0xffffffffu, kmax_of, r);
         const T* b = static_cast<const T*>(sl.B) + slot * sl.B_slot_stride + (long long)col * p.R;
         const float* ur = u + ((long long)t * p.n_slices + j) * p.R;
         for (int k = lane; k < kmax; k += 32) acc[r] = fmaf(value(b[k]), ur[k], acc[r]);
