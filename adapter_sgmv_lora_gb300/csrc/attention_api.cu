@@ -165,6 +165,26 @@ lora_status_t validate_layers(const lora_kv_cache_t* caches, int32_t num_caches)
   return LORA_OK;
 }
 
+// Whether a tensor is among the layers' twice (moved rows would be moved again).
+lora_status_t refuse_repeats(const lora_kv_cache_t* caches, int32_t num_caches) {
+  uintptr_t few[512];
+  size_t size = 512;
+  uintptr_t* seen = few;
+  while (size < (size_t)num_caches * 4) size *= 2;  // at most half full
+  if (size > 512 && !(seen = static_cast<uintptr_t*>(std::malloc(size * sizeof(uintptr_t))))) return LORA_ERR_WORKSPACE;
+  std::fill(seen, seen + size, 0);
+  lora_status_t st = LORA_OK;
+  for (int64_t i = 0; i < 2 * (int64_t)num_caches && st == LORA_OK; ++i) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(i % 2 ? caches[i / 2].v : caches[i / 2].k);
+    size_t at = (p >> 4) * 0x9E3779B97F4A7C15ull >> 20 & (size - 1);
+    while (seen[at] != 0 && seen[at] != p) at = (at + 1) & (size - 1);
+    if (seen[at] == p) st = LORA_ERR_SHAPE;
+    seen[at] = p;
+  }
+  if (seen != few) std::free(seen);
+  return st;
+}
+
 lora_status_t validate_tree(const lora_tree_attention_t* a, const lora_kv_cache_t* c) {
   if (!a) return LORA_ERR_NULL;
   lora_status_t st = validate_cache(c);
@@ -332,8 +352,9 @@ extern "C" lora_status_t lora_kv_keep_rows(const lora_kv_cache_t* caches, int32_
     return LORA_ERR_SHAPE;
   if (keep->num_seqs > 1 && (keep->table_stride < keep->max_pages || keep->path_stride < keep->max_kept))
     return LORA_ERR_SHAPE;
-  const lora_status_t st = validate_layers(caches, num_caches);
+  lora_status_t st = validate_layers(caches, num_caches);
   if (st != LORA_OK) return st;
+  if ((st = refuse_repeats(caches, num_caches)) != LORA_OK) return st;
   if (keep->num_seqs == 0) return LORA_OK;
   if (!keep->lengths || !keep->row_offsets || (keep->max_pages > 0 && !keep->block_tables) ||
       (keep->max_kept > 0 && !keep->path))

@@ -674,7 +674,10 @@ typedef struct {
  * that does not ascend or names a token that the sequence does not have
  * LORA_DEV_BAD_ROW, a used page outside the cache LORA_DEV_BAD_PAGE; that
  * sequence and its new length are left as they were.
- * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_SHAPE, LORA_ERR_ALIGN.
+ * No tensor may be listed twice or overlap another.
+ * Errors: LORA_ERR_NULL, LORA_ERR_DTYPE, LORA_ERR_SHAPE (also a K or V listed
+ * twice), LORA_ERR_ALIGN, LORA_ERR_WORKSPACE (no host memory to check a long
+ * list).
  */
 lora_status_t lora_kv_keep_rows(const lora_kv_cache_t* caches, int32_t num_caches, const lora_keep_t* keep,
                                 lora_stream_t stream);

@@ -132,6 +132,20 @@ def test_keep_rows_refusals():
     assert L.lora_last_call_path(None) == 0
 
 
+def test_keep_rows_refuses_a_tensor_listed_twice():
+    """Its rows would be moved twice."""
+    L = lk.lib()
+    k = lk._Keep(num_seqs=0, max_kept=3, path_stride=3)
+    at = lambda i: _cache(k=4096 + 32 * i, v=4096 + 32 * i + 16)
+    for n in (1, 2, 64, 128, 129, 700):
+        layers = [at(i) for i in range(n)]
+        arr = (lk._KVCache * n)(*layers)
+        assert L.lora_kv_keep_rows(_ref(arr), n, _ref(k), None) == 0
+        for bad in (_cache(k=4096, v=4096), _cache(k=4096 + 32 * (n - 1) + 16, v=1 << 20), _cache(k=1 << 20, v=4096)):
+            arr = (lk._KVCache * (n + 1))(*layers, bad)
+            assert L.lora_kv_keep_rows(_ref(arr), n + 1, _ref(k), None) == 2
+
+
 def test_base_q4_refusals():
     L = lk.lib()
 
