@@ -333,6 +333,30 @@ def test_q4_streams_and_graph():
     c.check()
 
 
+@pytest.mark.parametrize("T,outs", [(2, [512]), (12, [512, 96]), (300, [4000, 40])])
+def test_q4_two_calls_at_once(T, outs):
+    """Two calls in flight on two streams, each with its workspace, and two captured graphs replayed likewise."""
+    cs = [Q4Case(T, 512, outs, 64, 16, BF, [T // 2, T - T // 2 - 1], seed=i) for i in range(2)]
+    want = [c.run().clone() for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    graphs = []
+    for c in cs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.run()
+    for replay in (False, True):
+        for c in cs:
+            c.y.fill_(NAN)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for c, s, g in zip(cs, streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay() if replay else c.run()
+        torch.cuda.synchronize()
+        for c, w in zip(cs, want):
+            assert torch.equal(c.y, w)
+
+
 def test_q4_bad_routing_writes_nothing():
     for dtype in (BF, F32):
         c = Q4Case(9, 256, [64], 64, 16, dtype, [4, 5])
