@@ -7,7 +7,7 @@
 // TT cached tokens (a stage is 32 KB at most) go through
 //   S = Q K^T      [128 x TT]  Q and K in shared memory, S in TMEM
 //   P = 2^(S - m)  two threads a row, back into TMEM over S
-//   O = P V        [128 x HV]  P from TMEM, V in shared memory as it lies
+//   O = P V        [128 x HV]  P from TMEM and shared memory, V as it lies
 // S and O have two buffers each: the next scores and the last tile's output are
 // under way while a tile's softmax runs.  A thread holds half a row's scores at
 // once and half of its running O; the halves exchange their maximum through
@@ -15,10 +15,16 @@
 // accumulated by the instruction, which cuts sums off, long contexts lose a bit
 // every step, and a rescaling would have to wait for the products.
 //
-// P enters as two bf16 terms, the first cut off and the second rounded, 16 bits
-// together: one term alone shows in outputs.  The second is taken from p (1 +
-// 2^-17), so that it is never zero and an infinite value stays one; the factor
-// comes off in the end.
+// P enters as three bf16 terms, two cut off and the last rounded, fp32's own 24
+// bits together.  Two terms, 16 bits, left 10400 of 2.92 M outputs of 48 ragged
+// trees off the bf16 value nearest to the result, three leave 1140 (fp32
+// arithmetic 1500), and cost 5 to 20% (94 us, so 99; 24 trees of 64 on the 70B
+// attention 431, so 491; 60 tokens against 131012 205, so 248).  What is left
+// for the second term is taken from p (1 + 2^-23), a factor that comes off in
+// the end, and for the third from (1 + 2^-17) times that (2^-24 p more at most):
+// so neither is ever zero, and an infinite value stays one.  The first two lie
+// in TMEM over S, which they fill; the third in shared memory, one tile's: its
+// products go first, so that it is free again by the time the next is written.
 //
 // Warps: 0 loads K, 1 loads V, 2 loads Q, 3 issues the products, 4 to 11 are
 // the softmax.  K and V come by TMA boxes where a page is whole eights of tokens,
@@ -41,7 +47,8 @@ namespace lora {
 namespace {
 
 constexpr int kTcThreads = 384;
-constexpr float kTcLift = 1.f + 7.62939453125e-6f;  // 1 + 2^-17
+constexpr float kTcLift = 1.f + 1.1920928955078125e-7f;   // 1 + 2^-23
+constexpr float kTcLift2 = 1.f + 7.62939453125e-6f;       // 1 + 2^-17
 
 // HK: padded width of Q and K.  HV: columns of V a stream takes.
 template <int HK_>
@@ -50,8 +57,10 @@ struct TcCfg {
   static constexpr int TT = HK > 128 ? 64 : 128;
   using S = TreeShape<128, TT, HV, 2>;
   static constexpr int Q_BYTES = 128 * HK * 2, K_BYTES = TT * HK * 2, V_BYTES = TT * HV * 2;
-  static constexpr int NS = HK == 64 ? 5 : 3;  // stages of K, and of V
-  static constexpr int SMEM = Q_BYTES + NS * (K_BYTES + V_BYTES);
+  static constexpr int P_BYTES = 128 * TT * 2;     // P's third terms
+  static constexpr int NS = HK == 64 ? 5 : HK == 128 ? 2 : 3;  // stages of K
+  static constexpr int NV = HK == 64 ? 5 : 3;                  // of V, which is held longer
+  static constexpr int SMEM = Q_BYTES + NS * K_BYTES + NV * V_BYTES + P_BYTES;
 };
 
 // Byte offset of 16-byte chunk c of row r in blocks of [rows][64 columns] with
@@ -138,6 +147,11 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// What the upper halves of two floats >= 0 hold, negated.
+__device__ __forceinline__ float2 minus_top(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float((a & 0xffff0000u) | 0x80000000u), __uint_as_float((b & 0xffff0000u) | 0x80000000u));
+}
+
 // A box of a 4-D tensor map into shared memory; completion counted in bytes.
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
   asm volatile(
@@ -190,7 +204,7 @@ struct TcShared {
   uint64_t kfull[5], kempty[5], vfull[5], vempty[5];
   uint64_t told[2];                // the halves of the rows have said something
   uint64_t land[2];                // V tiles that are looked through before they are handed over
-  uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], ofree[2], done;
+  uint64_t qfull, qempty, sfull[2], pfull[2], pfree, ofull[2], ofree[2], done;
   uint32_t tmem;
   int fail;                        // a wait ran out
   float swap[2][2][128];           // what the halves of a row tell each other, by turns
@@ -205,12 +219,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tree_tc_kernel(const __grid_constant__ TreeDesc p, const __grid_constant__ TcMaps maps) {
   using C = TcCfg<HK>;
   using S = typename C::S;
-  constexpr int TT = C::TT, HV = C::HV, NS = C::NS;
+  constexpr int TT = C::TT, HV = C::HV, NS = C::NS, NV = C::NV;
   using T = __nv_bfloat16;
   extern __shared__ __align__(1024) uint8_t sq[];  // the swizzle wants whole 1024 bytes
   __shared__ __align__(8) TcShared sh;
   uint8_t* sk = sq + C::Q_BYTES;
   uint8_t* sv = sk + NS * C::K_BYTES;
+  uint8_t* sp = sv + NV * C::V_BYTES;  // third terms, laid out as Q
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.x;
   const int hd = p.cache.head_dim;
   pdl_launch_dependents();
@@ -222,6 +237,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int i = 0; i < NS; ++i) {
         mbar_init(&sh.kfull[i], 1);
         mbar_init(&sh.kempty[i], 1);
+      }
+      for (int i = 0; i < NV; ++i) {
         mbar_init(&sh.vfull[i], 1);
         mbar_init(&sh.vempty[i], 1);
       }
@@ -231,6 +248,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sh.land[0], 1);
       mbar_init(&sh.land[1], 1);
       mbar_init(&sh.qempty, 1);
+      mbar_init(&sh.pfree, 1);
       mbar_init(&sh.done, 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.sfull[i], 1);
@@ -359,10 +377,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float now = fmaxf(m, fmaxf(top, learn())), base = now == kTreeNone ? 0.f : now;
         const float keep = tree_pow2(m - base);
         m = now;
+        // The third terms of the tile before have been read.
+        if (tile_no > 0 && !warp_wait(&sh.pfree, (tile_no - 1) & 1)) dead = true;
+        if (dead) break;
         float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < ST / 16; ++c) {  // 16 tokens: 8 columns of first terms, 8 of second ones
-          uint32_t out[16];
+          uint32_t out[16], third[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const float2 x = add_f32x2(make_float2(s[c * 16 + 2 * q], s[c * 16 + 2 * q + 1]), make_float2(-base, -base));
@@ -370,16 +391,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             sums[q & 1] = add_f32x2(sums[q & 1], w);
             const uint32_t ab = __float_as_uint(w.x), bb = __float_as_uint(w.y);
             out[q] = __byte_perm(ab, bb, 0x7632);
-            const float2 rest = fma_f32x2(w, make_float2(kTcLift, kTcLift),
-                                          make_float2(__uint_as_float((ab & 0xffff0000u) | 0x80000000u),
-                                                      __uint_as_float((bb & 0xffff0000u) | 0x80000000u)));
-            out[8 + q] = round_pack_bf16x2(rest.x, rest.y);
+            const float2 rest = fma_f32x2(w, make_float2(kTcLift, kTcLift), minus_top(ab, bb));
+            const uint32_t ar = __float_as_uint(rest.x), br = __float_as_uint(rest.y);
+            out[8 + q] = __byte_perm(ar, br, 0x7632);
+            const float2 last = fma_f32x2(rest, make_float2(kTcLift2, kTcLift2), minus_top(ar, br));
+            third[q] = round_pack_bf16x2(last.x, last.y);
           }
           tmem_st16(s_col(b) + lanes + h * ST + c * 16, out);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4*>(sp + tc_at<128>(row, (h * ST + c * 16) / 8 + q)) =
+                make_uint4(third[4 * q], third[4 * q + 1], third[4 * q + 2], third[4 * q + 3]);
         }
         l = fmaf(l, keep, (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y));
         tmem_wait_st();
         tc_fence_before_sync();
+        fence_proxy_async_smem();
         warp_arrive(&sh.pfull[b]);
         kept0 = kept1;
         kept1 = keep;
@@ -448,6 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (BOXES && warp < 2) {
     // ---- loads of K (warp 0) or V (warp 1), a box a lane
     const bool is_k = warp == 0;
+    const int ns = is_k ? NS : NV;
     uint64_t* full = is_k ? sh.kfull : sh.vfull;
     uint64_t* empty = is_k ? sh.kempty : sh.vempty;
     const void* map = is_k ? &maps.k : &maps.v;
@@ -471,7 +499,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       unsigned* odd = sh.odd[look.tile % kTcFlags];
       if (lane < 4) odd[lane] = 0;
       __syncwarp();
-      uint8_t* st = sv + look.tile % NS * C::V_BYTES;
+      uint8_t* st = sv + look.tile % NV * C::V_BYTES;
       for (int e = lane; e < (TT - look.lo) * (HV / 8); e += 32) {
         const int r = look.lo + e / (HV / 8);
         uint4* at = reinterpret_cast<uint4*>(st + tc_at<TT>(r, e % (HV / 8)));
@@ -500,7 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       __syncwarp();
       fence_proxy_async_smem();
-      warp_arrive(&full[look.tile % NS]);
+      warp_arrive(&full[look.tile % NV]);
     };
     int issued = 0;  // tiles that are looked through, so far issued
     while (g.valid) {
@@ -519,8 +547,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool bad = __any_sync(0xffffffffu, out);
         const int from = out ? p.cache.num_pages : page;  // behind the last page: zeros
         if (t + 1 < g.t1) page = look_up(t + 1);
-        const int stage = tile_no % NS;
-        if (tile_no >= NS && !dead && !warp_wait(&empty[stage], (tile_no / NS - 1) & 1)) dead = true;
+        const int stage = tile_no % ns;
+        if (tile_no >= ns) {
+          const uint32_t turn = (tile_no / ns - 1) & 1;
+          // While the stage is still in use, the tile that has landed is looked through.
+          if (look.open && !__all_sync(0xffffffffu, mbar_test(&empty[stage], turn))) look_through();
+          if (!dead && !warp_wait(&empty[stage], turn)) dead = true;
+        }
         if (dead) break;
         if (is_k && lane == 0) sh.bad[tile_no % kTcFlags] = bad;
         const bool through = !is_k && t * TT + TT > g.s.ctx;
@@ -545,12 +578,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (dead) {  // copies in flight land before the block ends
       if (lane == 0) sh.fail = 1;
       if (look.open) (void)mbar_wait(&sh.land[looked & 1], (looked >> 1) & 1);
-      for (int i = max(0, tile_no - NS); i < tile_no; ++i) (void)mbar_wait(&full[i % NS], (i / NS) & 1);
+      for (int i = max(0, tile_no - ns); i < tile_no; ++i) (void)mbar_wait(&full[i % ns], (i / ns) & 1);
     }
   } else if (!BOXES && warp < 2) {
     // ---- loads of K (warp 0) or V (warp 1): a row is C16 chunks of 16 bytes
     constexpr int RPT = TT / 32;  // rows whose offsets a lane looks up
     const bool is_k = warp == 0;
+    const int ns = is_k ? NS : NV;
     uint64_t* full = is_k ? sh.kfull : sh.vfull;
     uint64_t* empty = is_k ? sh.kempty : sh.vempty;
     uint8_t* stages = is_k ? sk : sv;
@@ -573,7 +607,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         unsigned* odd = sh.odd[handed % kTcFlags];
         if (lane < 4) odd[lane] = 0;
         __syncwarp();
-        uint8_t* st = stages + handed % NS * C::V_BYTES;
+        uint8_t* st = stages + handed % NV * C::V_BYTES;
         for (int e = lane; e < (draft_hi - draft_lo) * (HV / 8); e += 32) {
           const int r = draft_lo + e / (HV / 8);
           uint4* at = reinterpret_cast<uint4*>(st + tc_at<TT>(r, e % (HV / 8)));
@@ -599,7 +633,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
       }
       fence_proxy_async_smem();
-      warp_arrive(&full[handed % NS]);
+      warp_arrive(&full[handed % ns]);
       n0 = n1;
       n1 = n2;
       --waiting;
@@ -632,11 +666,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         bad = __any_sync(0xffffffffu, bad);
         if (t + 1 < g.t1) look_up(t + 1, page);
-        const int stage = tile_no % NS, flag = tile_no % kTcFlags;
-        if (tile_no >= NS && !dead) {
+        const int stage = tile_no % ns, flag = tile_no % kTcFlags;
+        if (tile_no >= ns && !dead) {
           // While the stage is still in use, what has landed is handed over.
-          while (waiting > 0 && !__all_sync(0xffffffffu, mbar_test(&empty[stage], (tile_no / NS - 1) & 1))) hand_over();
-          if (!warp_wait(&empty[stage], (tile_no / NS - 1) & 1)) dead = true;
+          while (waiting > 0 && !__all_sync(0xffffffffu, mbar_test(&empty[stage], (tile_no / ns - 1) & 1))) hand_over();
+          if (!warp_wait(&empty[stage], (tile_no / ns - 1) & 1)) dead = true;
         }
         if (dead) {
           if (lane == 0) sh.fail = 1;
@@ -722,7 +756,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int seg_no = 0, kt = 0, vt = 0;  // segments, tiles of K and of V so far
     bool ok = true;
     const uint64_t qd = sw128_desc(smem_addr(sq)), kd0 = sw128_desc(smem_addr(sk)),
-                   vd0 = sw128_desc_mn(smem_addr(sv), TT * 128);
+                   vd0 = sw128_desc_mn(smem_addr(sv), TT * 128), pd = sw128_desc(smem_addr(sp));
     while (ok && __shfl_sync(0xffffffffu, (int)g.valid, 0)) {
       const int n = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
       if (!(ok = warp_wait(&sh.qfull, seg_no & 1))) break;
@@ -749,17 +783,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ++kt;
         }
         if (i == 0) continue;
-        const int b = vt & 1, st = vt % NS;
-        if (!(ok = warp_wait(&sh.vfull[st], (vt / NS) & 1))) break;
+        const int b = vt & 1, st = vt % NV;
+        if (!(ok = warp_wait(&sh.vfull[st], (vt / NV) & 1))) break;
         if (!(ok = warp_wait(&sh.pfull[b], (vt >> 1) & 1))) break;
         if (vt >= 2 && !(ok = warp_wait(&sh.ofree[b], ((vt >> 1) - 1) & 1))) break;
         tc_fence_after_sync();
         const uint64_t vd = vd0 + st * (C::V_BYTES / 16);
         const uint32_t d = o_col(b), a = s_col(b);
         if (leader) {
+          // The third terms, whose place is wanted next; then the others in turn.
 #pragma unroll
-          for (int k = 0; k < TT / 8; ++k)  // the two terms in turn
-            tc_mma_bf16_ts(d, a + k * 8, vd + (k >> 1) * (2048 / 16), o_idesc, k > 0);
+          for (int k = 0; k < TT / 16; ++k)
+            tc_mma_bf16(d, pd + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16, vd + k * (2048 / 16), o_idesc, k > 0);
+          tc_commit(&sh.pfree);
+#pragma unroll
+          for (int k = 0; k < TT / 8; ++k)
+            tc_mma_bf16_ts(d, a + k * 8, vd + (k >> 1) * (2048 / 16), o_idesc, 1u);
           tc_commit(&sh.vempty[st]);
           tc_commit(&sh.ofull[b]);
         }
