@@ -20,8 +20,9 @@ between the projections ``lora_build_rope``, ``lora_rope_append``,
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
-from dataclasses import dataclass, field
+from dataclasses import dataclass, field, fields
 from typing import List, Optional, Sequence
 
 import numpy as np
@@ -896,16 +897,39 @@ class Q4Weight:
         _on_cuda(q=self.q, scales=self.scales, zeros=self.zeros)
 
 
+_problem_fields = operator.attrgetter("x", "max_num_loras", "max_lora_rank", "slot_ranks")
+_routing_fields = operator.attrgetter(*(f.name for f in fields(Routing)))
+_slice_fields = operator.attrgetter(*(f.name for f in fields(Slice)))
+
+
 @dataclass(frozen=True)
 class BaseQ4Problem:
     """One lora_base_q4_apply call: a problem, its routing and a Q4Weight per
-    slice.  Routing(None, None, 0, 0) adds no adapter."""
+    slice.  Routing(None, None, 0, 0) adds no adapter.  The call's arguments are
+    made ready here, and again by a call that finds a field of the problem, of
+    one of its slices or of the routing set to something else."""
     problem: Problem
     routing: Routing
     weights: Sequence[Q4Weight]
 
     def __post_init__(self):
         object.__setattr__(self, "weights", tuple(self.weights))
+        self._encode()
+
+    def _fields(self) -> list:
+        now = [*_problem_fields(self.problem), *_routing_fields(self.routing)]
+        for s in self.problem.slices:
+            now += _slice_fields(s)
+        return now
+
+    def _current(self) -> tuple:
+        """(addresses of the call's structs as the fields are now, what they were made from, what they point to)."""
+        now, seen = self._fields(), self._made[1]
+        if len(now) != len(seen) or not all(map(operator.is_, now, seen)):
+            self._encode()
+        return self._made
+
+    def _encode(self) -> None:
         x, slices = self.problem.x, self.problem.slices
         if len(self.weights) != len(slices):
             raise ValueError("one base weight per slice")
@@ -923,8 +947,8 @@ class BaseQ4Problem:
             arr[j] = _Q4Weight(w.q.data_ptr(), rows(w.q), w.scales.data_ptr(), rows(w.scales),
                                w.zeros.data_ptr() if w.zeros is not None else None,
                                rows(w.zeros) if w.zeros is not None else 0, w.group_size)
-        object.__setattr__(self, "_structs", (c, r, arr, self.routing._host_keep))  # what the structs point to
-        object.__setattr__(self, "_refs", tuple(ctypes.addressof(o) for o in (c, r, arr)))
+        object.__setattr__(self, "_made", (tuple(ctypes.addressof(o) for o in (c, r, arr)), self._fields(),
+                                           (c, r, arr, self.routing._host_keep)))
 
 
 def _on_current(t) -> None:
@@ -947,7 +971,8 @@ def lora_base_q4_apply(problem: BaseQ4Problem, workspace, stream=None) -> None:
     """The base projection on 4-bit weights with the LoRA delta joined before
     the one rounding (include/lora_sgmv.h); workspace as new_workspace makes it."""
     ws, nbytes = _workspace(workspace, problem.problem.x)
-    _check(lib().lora_base_q4_apply(*problem._refs, ws, nbytes, _stream_handle(stream)), "lora_base_q4_apply")
+    made = problem._current()
+    _check(lib().lora_base_q4_apply(*made[0], ws, nbytes, _stream_handle(stream)), "lora_base_q4_apply")
 
 
 def lora_build_tree(parents, words: Optional[int] = None) -> dict:
