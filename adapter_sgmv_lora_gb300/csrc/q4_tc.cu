@@ -11,7 +11,9 @@
 // so a weight is never rounded.  The delta is more of the same: 32 ranks of a
 // slot's B beside themselves against u as two bf16 terms, scale 1, taken over by
 // the columns of the slot's rows alone, so that what other slots hold cannot
-// reach them.
+// reach them.  Against u's second term, which may be zero or of the other sign,
+// an element of B that is not finite counts as zero: against the first it gives
+// its infinity or NaN.
 //
 // Warps 0 to 7 hold y, 8 to 15 load and unpack, 16 issues the products, 17 loads
 // x.  The unpacking warps work in pairs, each pair on every fourth block: a
@@ -94,6 +96,12 @@ __device__ __forceinline__ uint4 unpack_in_order(uint32_t w, uint32_t low) {
     return sub_bf16x2((__byte_perm(even, odd, order) & 0x000f000fu) | 0x43004300u, low);
   };
   return make_uint4(pair(0x4400), pair(0x5511), pair(0x6622), pair(0x7733));
+}
+
+// Zero in the place of what is infinite or NaN.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+  const uint32_t none = sub_bf16x2(v, v);  // 0, or NaN
+  return v & __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&none), __nv_bfloat162(0.f, 0.f));
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -276,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             v = make_uint4(bits[0], bits[1], bits[2], bits[3]);
           }
           *reinterpret_cast<uint4*>(dst + at(r + (c >> 2) * 64, c & 3)) = v;
-          *reinterpret_cast<uint4*>(dst + at(r + (c >> 2) * 64, 4 + (c & 3))) = v;
+          *reinterpret_cast<uint4*>(dst + at(r + (c >> 2) * 64, 4 + (c & 3))) =
+              make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
         }
         // u as two terms, of rows outside the run zero.
         const int k = k0 + (r & 3) * 8;
