@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(kThreads) keep_rows_kernel(const __grid_consta
   const long long n = (long long)p.offsets[b + 1] - first;
   const int* path = p.path + b * p.path_stride;
   if (threadIdx.x == 0) {
-    s_bad = (first < 0 || n < 0 || len < n || len > p.max_len) ? LORA_DEV_BAD_LENGTH : 0u;
+    // Without drafted tokens nothing is read, whatever the length, and the length stays.
+    s_bad = (first < 0 || n < 0 || (n > 0 && (len < n || len > p.max_len))) ? LORA_DEV_BAD_LENGTH : 0u;
     s_kept = p.max_kept;
   }
   __syncthreads();

@@ -669,8 +669,10 @@ typedef struct {
  * written.  The sequence then has new_lengths[b] tokens; what its pages hold
  * behind them is unspecified (lora_pages_trim gives the pages back).  Copies
  * are exact, gaps between strided rows are not touched.  Pages that are
- * written must not be shared (lora_pages_append saw to that).  A length or
- * offsets as refused by lora_tree_attention raise LORA_DEV_BAD_LENGTH, a path
+ * written must not be shared (lora_pages_append saw to that).  A sequence
+ * without drafted tokens keeps its length, which is not looked at.  Another's
+ * length that lora_tree_attention would refuse, or offsets that are negative or
+ * decrease, raise LORA_DEV_BAD_LENGTH, a path
  * that does not ascend or names a token that the sequence does not have
  * LORA_DEV_BAD_ROW, a used page outside the cache LORA_DEV_BAD_PAGE; that
  * sequence and its new length are left as they were.
