@@ -64,7 +64,7 @@ class AttentionLayer:
         self.caches = lk.KVCaches([self.cache])  # a model lists its layers here
         self.pages = lk.Pages(num_pages, page_size, max_seqs, max_pages)
         self.adapter = np.full(max_seqs, -1, dtype=np.int32)
-        self.drafts = None  # what verify left for keep
+        self.drafts = {}  # drafted tokens that verify left for keep, of each sequence
 
     def load_adapter(self, slot, rank, alpha, a_qkv, b_qkv, a_o, b_o):
         """Raw fp32 adapter: a_qkv[j] [rank, hidden], b_qkv[j] [out_j, rank] for q, k, v; a_o, b_o."""
@@ -88,10 +88,16 @@ class AttentionLayer:
             lk.lora_base_gemm_apply(p, routing, weights, workspace)
         return y
 
+    def _settled(self, seqs):
+        for s in seqs:
+            if s in self.drafts:
+                raise ValueError("sequence %d has drafted tokens: keep says first which of them stay" % s)
+
     def _append(self, seqs, counts, depths=None):
         """Rows and positions (depths[i] behind the sequence's end; None: one after the other) of counts[i] more
         tokens of seqs[i]; runs the copies that shared pages need.  Where the pages do not suffice for all of them
         the sequences stay as long as they were."""
+        self._settled(seqs)
         rows, positions, copies, starts = [], [], [], []
         try:
             for i, (s, n) in enumerate(zip(seqs, counts)):
@@ -151,47 +157,52 @@ class AttentionLayer:
     def verify(self, seqs, xs, parents):
         """A tree of drafted tokens of each sequence: token j of seqs[i] is xs[i][j] and follows drafted token
         parents[i][j] (-1: the cached context).  Returns the output rows [n_i, hidden] of each sequence, whose
-        rows stay in the cache until keep says which branch was accepted."""
+        rows stay in the cache until keep says which branch was accepted; until then it takes no other tokens and is
+        not forked."""
         counts = [x.shape[0] for x in xs]
         route = lk.lora_build_routing(self.adapter[seqs], counts, self.max_loras)
         order = [int(i) for i in route["perm"]]
         mine, n = [seqs[i] for i in order], [counts[i] for i in order]
         words = max(1, -(-max(counts) // 64))
         trees = [lk.lora_build_tree(parents[i], words) for i in order]
-        before = self.pages.lengths[mine].copy()
         q = self._store(torch.cat([xs[i] for i in order]), mine, n, route, [t["depths"] for t in trees])
         attn = torch.empty((sum(n), self.heads, self.head_dim), dtype=self.dtype, device=self.device)
         up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(self.device)
         offsets = np.concatenate(([0], np.cumsum(n))).astype(np.int32)
-        tables, lengths = up(self.pages.tables[mine]), up(self.pages.lengths[mine])
-        problem = lk.TreeAttentionProblem(q=q, out=attn, cache=self.cache, block_tables=tables, lengths=lengths,
-                                          row_offsets=up(offsets),
+        problem = lk.TreeAttentionProblem(q=q, out=attn, cache=self.cache, block_tables=up(self.pages.tables[mine]),
+                                          lengths=up(self.pages.lengths[mine]), row_offsets=up(offsets),
                                           masks=up(np.concatenate([t["masks"] for t in trees]).view(np.int64)))
         lk.lora_tree_attention(problem, lk.new_tree_attention_workspace(problem))
         y = self._project(attn.flatten(1), self.a_o, self.b_o, [self.hidden], self.w_o, route)
-        self.drafts = (mine, before, tables, lengths, problem.row_offsets)
+        self.drafts.update(zip(mine, n))
         rows = {s: y[a:b] for s, a, b in zip(mine, offsets, offsets[1:])}
         return [rows[s] for s in seqs]
 
     def keep(self, paths):
-        """Of the drafted tokens of the last verify keep paths[seq], a branch from its root on; a sequence that is
-        not named keeps none."""
-        mine, before, tables, lengths, offsets = self.drafts
-        self.drafts = None
+        """Of the drafted tokens that verify left keep paths[seq], a branch from its root on; a sequence that is not
+        named keeps none."""
+        mine, n = list(self.drafts), list(self.drafts.values())
+        self.drafts = {}
+        if not mine:
+            return
         kept = [list(paths.get(s, [])) for s in mine]
         path = np.full((len(mine), max(map(len, kept))), -1, dtype=np.int32)
         for row, k in zip(path, kept):
             row[:len(k)] = k
-        lk.lora_kv_keep_rows(lk.KeepRowsProblem(self.caches, tables, lengths, offsets,
-                                                torch.from_numpy(path).to(self.device)))
-        for s, start, k in zip(mine, before, kept):
-            self.pages.trim(s, int(start) + len(k))
+        up = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(self.device)
+        # the pages as they are now: compact may have moved them
+        lk.lora_kv_keep_rows(lk.KeepRowsProblem(self.caches, up(self.pages.tables[mine]), up(self.pages.lengths[mine]),
+                                                up(np.cumsum([0] + n)), up(path)))
+        for s, rows, k in zip(mine, n, kept):
+            self.pages.trim(s, int(self.pages.lengths[s]) - rows + len(k))
 
     def fork(self, parent, child):
+        self._settled([parent])
         self.pages.fork(parent, child)
         self.adapter[child] = self.adapter[parent]
 
     def end(self, seq):
+        self.drafts.pop(seq, None)
         self.pages.trim(seq, 0)
         self.adapter[seq] = -1
 
