@@ -23,8 +23,9 @@
 // for the second term is taken from p (1 + 2^-23), a factor that comes off in
 // the end, and for the third from (1 + 2^-17) times that (2^-24 p more at most):
 // so neither is ever zero, and an infinite value stays one.  The first two lie
-// in TMEM over S, which they fill; the third in shared memory, one tile's: its
-// products go first, so that it is free again by the time the next is written.
+// in TMEM over S, which they fill; the third in what else is free there.  At 128
+// wide nothing is, and it lies in shared memory, one tile's: its products go
+// first, so that it is free again by the time the next is written.
 //
 // Warps: 0 loads K, 1 loads V, 2 loads Q, 3 issues the products, 4 to 11 are
 // the softmax.  K and V come by TMA boxes where a page is whole eights of tokens,
@@ -57,7 +58,8 @@ struct TcCfg {
   static constexpr int TT = HK > 128 ? 64 : 128;
   using S = TreeShape<128, TT, HV, 2>;
   static constexpr int Q_BYTES = 128 * HK * 2, K_BYTES = TT * HK * 2, V_BYTES = TT * HV * 2;
-  static constexpr int P_BYTES = 128 * TT * 2;     // P's third terms
+  static constexpr bool THIRD_TMEM = HK != 128;    // where P's third terms lie
+  static constexpr int P_BYTES = THIRD_TMEM ? 0 : 128 * TT * 2;
   static constexpr int NS = HK == 64 ? 5 : HK == 128 ? 2 : 3;  // stages of K
   static constexpr int NV = HK == 64 ? 5 : 3;                  // of V, which is held longer
   static constexpr int SMEM = Q_BYTES + NS * K_BYTES + NV * V_BYTES + P_BYTES;
@@ -94,6 +96,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // N consecutive columns of this warp's lanes.
 template <int N>
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ __align__(8) TcShared sh;
   uint8_t* sk = sq + C::Q_BYTES;
   uint8_t* sv = sk + NS * C::K_BYTES;
-  uint8_t* sp = sv + NV * C::V_BYTES;  // third terms, laid out as Q
+  uint8_t* sp = sv + NV * C::V_BYTES;  // third terms where they have no TMEM, laid out as Q
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.x;
   const int hd = p.cache.head_dim;
   pdl_launch_dependents();
@@ -266,9 +273,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sh.tmem;
-  // TMEM columns: S and P of two tiles, then O of two.
+  // TMEM columns: S and P of two tiles, then O of two.  Third terms lie where
+  // tiles of 64 tokens or outputs of 64 columns leave room.
   auto s_col = [&](int w) { return tmem + w * 128; };
   auto o_col = [&](int w) { return tmem + 256 + w * 128; };
+  auto third_col = [&](int w) { return tmem + w * 128 + (TT == 64 ? 64 : 320); };
   const TreePiece piece = sh.piece;
   TreeSegment<S> g;
   g.first(p, piece);
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float keep = tree_pow2(m - base);
         m = now;
         // The third terms of the tile before have been read.
-        if (tile_no > 0 && !warp_wait(&sh.pfree, (tile_no - 1) & 1)) dead = true;
+        if (!C::THIRD_TMEM && tile_no > 0 && !warp_wait(&sh.pfree, (tile_no - 1) & 1)) dead = true;
         if (dead) break;
         float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -398,15 +407,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             third[q] = round_pack_bf16x2(last.x, last.y);
           }
           tmem_st16(s_col(b) + lanes + h * ST + c * 16, out);
+          if constexpr (C::THIRD_TMEM) {
+            tmem_st8(third_col(b) + lanes + (h * ST + c * 16) / 2, third);
+          } else {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<uint4*>(sp + tc_at<128>(row, (h * ST + c * 16) / 8 + q)) =
-                make_uint4(third[4 * q], third[4 * q + 1], third[4 * q + 2], third[4 * q + 3]);
+            for (int q = 0; q < 2; ++q)
+              *reinterpret_cast<uint4*>(sp + tc_at<128>(row, (h * ST + c * 16) / 8 + q)) =
+                  make_uint4(third[4 * q], third[4 * q + 1], third[4 * q + 2], third[4 * q + 3]);
+          }
         }
         l = fmaf(l, keep, (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y));
         tmem_wait_st();
         tc_fence_before_sync();
-        fence_proxy_async_smem();
+        if (!C::THIRD_TMEM) fence_proxy_async_smem();
         warp_arrive(&sh.pfull[b]);
         kept0 = kept1;
         kept1 = keep;
@@ -703,7 +716,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         else if (waiting == 1) n1 = note;
         else n2 = note;
         ++tile_no;
-        if (++waiting == 3) hand_over();
+        if (++waiting == min(ns, 3)) hand_over();
       }
       if (g.valid) g.next(p);
     }
@@ -794,8 +807,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // The third terms, whose place is wanted next; then the others in turn.
 #pragma unroll
           for (int k = 0; k < TT / 16; ++k)
-            tc_mma_bf16(d, pd + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16, vd + k * (2048 / 16), o_idesc, k > 0);
-          tc_commit(&sh.pfree);
+            if (C::THIRD_TMEM)
+              tc_mma_bf16_ts(d, third_col(b) + k * 8, vd + k * (2048 / 16), o_idesc, k > 0);
+            else
+              tc_mma_bf16(d, pd + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16, vd + k * (2048 / 16), o_idesc, k > 0);
+          if (!C::THIRD_TMEM) tc_commit(&sh.pfree);
 #pragma unroll
           for (int k = 0; k < TT / 8; ++k)
             tc_mma_bf16_ts(d, a + k * 8, vd + (k >> 1) * (2048 / 16), o_idesc, 1u);
