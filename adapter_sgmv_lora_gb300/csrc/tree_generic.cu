@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(kGenThreads, GenCfg<HD>::CTAS) tree_generic_ke
         if (row >= rows) break;
         const int i = (row0 + row) / p.group, h = kv * p.group + (row0 + row) % p.group;
         T* out = static_cast<T*>(p.out.data) + (g.s.row0 + i) * p.out.row_stride + h * p.out.head_stride;
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        const bool none = l[r] == 0.f;  // nothing seen, or -inf alone: 0, whatever the values
+        const float inv = 1.f / l[r];
 #pragma unroll
         for (int e = 0; e < VPL; ++e) {
           const int d = column(e);
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kGenThreads, GenCfg<HD>::CTAS) tree_generic_ke
           else if (!bad && d < hd) out[d] = [](float v) {
             if constexpr (sizeof(T) == 4) return v;
             else return __float2bfloat16_rn(v);
-          }(o[r][e] * inv);
+          }(none ? 0.f : o[r][e] * inv);
         }
         if (lane == 0) {
           if (!whole) p.stats[slot * MR + row] = make_float2(m[r], bad ? -1.f : l[r]);

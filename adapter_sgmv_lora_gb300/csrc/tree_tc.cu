@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (bad) {
           if (h == 0) atomicOr(p.status, LORA_DEV_BAD_PAGE);
         } else {
-          const float inv = l == 0.f ? 0.f : 1.f / (l * kTcLift);
+          const float inv = 1.f / (l * kTcLift);
+          const bool none = l == 0.f;  // nothing seen, or -inf alone: 0, whatever the values
           const int col = part * HV + h * OC;
           T* out = static_cast<T*>(p.out.data) + (g.s.row0 + draft) * p.out.row_stride + head * p.out.head_stride + col;
 #pragma unroll
@@ -452,15 +453,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (col + 8 * e < hd) {
               const float2* v = o + 4 * e;
               *reinterpret_cast<uint4*>(out + 8 * e) =
-                  make_uint4(round_pack_bf16x2(v[0].x * inv, v[0].y * inv), round_pack_bf16x2(v[1].x * inv, v[1].y * inv),
-                             round_pack_bf16x2(v[2].x * inv, v[2].y * inv), round_pack_bf16x2(v[3].x * inv, v[3].y * inv));
+                  none ? make_uint4(0, 0, 0, 0)
+                       : make_uint4(round_pack_bf16x2(v[0].x * inv, v[0].y * inv), round_pack_bf16x2(v[1].x * inv, v[1].y * inv),
+                                    round_pack_bf16x2(v[2].x * inv, v[2].y * inv), round_pack_bf16x2(v[3].x * inv, v[3].y * inv));
             }
           if (h == 0 && part == 0 && p.lse)
             p.lse[(long long)(g.s.row0 + draft) * p.num_heads + head] = (m + log2f(l)) * kTreeLn2;
         }
       }
-      if (strange && live && !bad) {
-        // They went into the products as 0: the rows that see them take them now.
+      if (strange && live && !bad && l != 0.f) {
+        // They went into the products as 0: the rows that see them take them
+        // now (where every score is -inf they have no weight).
         const int col = part * HV + h * OC;
         for (int j = max(g.s.ctx, g.t0 * TT); j < min(g.s.len, g.t1 * TT); ++j) {
           const int d = j - g.s.ctx;

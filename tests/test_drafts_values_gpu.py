@@ -80,3 +80,21 @@ def test_infinite_context_values(dtype, H, Hk, hd, ps, ctx):
         out[:rows[0], :, d] = 0
         a["v"][0][:, :, d] = 0
     check_tree(a, out, lse)
+
+
+@pytest.mark.parametrize("dtype,H,Hk,hd,ps", [(BF, 16, 2, 128, 16), (BF, 8, 2, 128, 5), (BF, 8, 2, 64, 16), (BF, 4, 1, 256, 16),
+                                              (BF, 4, 2, 33, 16), (F32, 8, 2, 64, 16)])
+@pytest.mark.parametrize("value", [1.0, float("inf"), float("nan")])
+@pytest.mark.parametrize("ctx", [0, 3, 200, 6000])
+def test_scores_of_minus_infinity_alone(dtype, H, Hk, hd, ps, value, ctx):
+    """A row whose every score is -inf gives 0 and lse -inf, whatever the values that have no weight."""
+    rows = [5, 3]
+    a = tree_case(rows, [ctx, 40], H, Hk, hd, ps, dtype, masks=None, seed=23)
+    tables = a["tables"].cpu().numpy()
+    a["q"].abs_().add_(0.5)
+    for j in range(ctx + rows[0]):
+        a["cache"].k[int(tables[0, j // ps]), j % ps, :, 0] = -float("inf")
+        a["cache"].v[int(tables[0, j // ps]), j % ps, :, 1:] = value
+    out, lse = run_tree(a)
+    assert torch.isneginf(lse[:rows[0]]).all() and (out[:rows[0]] == 0).all()
+    check_tree(a, out, lse, skip=(0,))
