@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2)
 // row's largest.  Where a row has smaller ones (its largest may meet a weight of
 // zero), an infinity or a NaN, all rows stay bf16 and so do the weights: the same
 // sums, five rows through the 8B gate and up with zeros 37.7 us, so 32.6 (one row
-// 34.1 and 28.9, 16 rows 44.4 either way).
+// 34.1 and 28.9, eight 40.0 and 35.1).
 //
 // A block is 256 inputs of 32 outputs, so a row's copies are whole lines.  One
 // row through the 8B gate and up (61 MB): 22.4 us, 2.7 TB/s, the unpacking pipe
@@ -932,16 +932,20 @@ cudaError_t launch_q4(const ProblemDesc& p, const Q4Weights& wts, const float* u
     const cudaError_t e = launch_q4_tc(p, wts, w, u, s);
     if (e != cudaErrorNotSupported) return e;
   }
-  // x in shared memory pays where the tiles of 32 outputs are more than the
-  // other kernel's CTAs that fit at once, and for the two smallest batches;
-  // else taking x in, row by row, costs more than it saves.  us so and the
-  // other way, 4096 inputs: 28672 outputs 27.2 and 36.3 (1 row), 35.4 and 39.6
-  // (8); 12288 outputs 20.2 and 23.2 (3), 25.7 and 24.3 (8); 8192 outputs 14.7
-  // and 15.3 (2), 16.4 and 15.4 (3), 20.0 and 16.1 (8); 6144 outputs 14.0 and
-  // 15.2 (1), 21.0 and 15.9 (8).
+  // x in shared memory pays for the two smallest batches, and where the tiles of
+  // 32 outputs are more than the other kernel's CTAs that fit at once and many
+  // enough for the time that taking x in costs, which goes with rows and inputs.
+  // us so and the other way:
+  //   4096 inputs   28672 outputs 27.7 and 36.2 (1 row), 37.1 and 39.4 (8);
+  //                 20480 29.2 and 32.9 (3), 31.3 and 33.3 (5), 34.1 and 34.0 (8);
+  //                 12288 20.7 and 23.3 (3), 21.4 and 23.1 (4), 24.7 and 23.6 (5);
+  //                 8192 15.0 and 15.3 (2), 17.0 and 15.6 (3), 21.8 and 16.4 (8)
+  //   8192 inputs   28672 50.6 and 58.4 (4); 14336 35.5 and 33.9 (3)
+  //   2048 inputs   28672 24.3 and 30.0 (8), 28.0 and 35.7 (9); 12288 18.9 and 18.8 (8)
+  //   1024 inputs   28672 26.3 and 31.2 (16); 12288 14.8 and 16.6 (8), 19.8 and 20.6 (16)
   int tiles = 0;
   for (int j = 0; j < p.n_slices; ++j) tiles += (p.sl[j].out_dim + kMmaOuts - 1) / kMmaOuts;
-  if (p.num_tokens <= 2 || tiles > 2 * device_sm_count()) {
+  if (p.num_tokens <= 2 || (tiles > 2 * device_sm_count() && (long long)p.num_tokens * p.in_dim <= 44LL * tiles)) {
     if (p.num_tokens <= 8 && few_smem<1>(p) <= kFewSmemMost) return launch_q4_few_words<1>(p, wts, w, u, s);
     if (p.num_tokens <= 16 && few_smem<2>(p) <= kFewSmemMost) return launch_q4_few_words<2>(p, wts, w, u, s);
   }
