@@ -97,7 +97,6 @@ class AttentionLayer:
         """Rows and positions (depths[i] behind the sequence's end; None: one after the other) of counts[i] more
         tokens of seqs[i]; runs the copies that shared pages need.  Where the pages do not suffice for all of them
         the sequences stay as long as they were."""
-        self._settled(seqs)
         rows, positions, copies, starts = [], [], [], []
         try:
             for i, (s, n) in enumerate(zip(seqs, counts)):
@@ -120,6 +119,7 @@ class AttentionLayer:
     def _store(self, x, seqs, counts, route, depths=None):
         """qkv of sorted rows, rotated; k and v into the cache.  Returns the rotated queries [T, heads, hd]."""
         H, Hk, hd = self.heads, self.kv_heads, self.head_dim
+        self._settled(seqs)
         rows, positions = self._append(seqs, counts, depths)
         y = self._project(x, self.a_qkv, self.b_qkv, self.qkv_dims, self.w_qkv, route)
         q, k, v = (y[:, a:b].unflatten(1, (-1, hd)) for a, b in ((0, H * hd), (H * hd, (H + Hk) * hd),
