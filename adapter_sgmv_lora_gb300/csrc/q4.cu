@@ -123,7 +123,8 @@ namespace {
 // stay within a group of 32.  The products are exact, a group's sum is fp32,
 // and its scale multiplies the sum.
 //
-// Bound by the instructions that unpack, for every 32 rows anew: gate and up of
+// Unpacks for every 32 rows anew; warps wait most for x and their copies (issue
+// slots a third taken, cold, 29 rows through 4096 outputs).  Gate and up of
 // the 8B model 51 us for 16 rows, 68 for 32, 122 for 64 (which q4_tc.cu takes
 // over).  Slower were 64 rows a CTA, one CTA an SM (150 for 64 rows: nothing runs
 // under a CTA's start and end), x in the ring beside the weights (170), the delta
@@ -352,8 +353,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2)
 // only meet to sum.  Each warp's ring of copies runs on across its tiles, so
 // memory never waits for a start or an end.
 //
-// Unpacking is what bounds this (the shifts and masks run at half rate), and
-// fp16 takes fewer of them than bf16: its ten mantissa bits hold a nibble where
+// Unpacking is most of the work (the shifts and masks run at half rate), and
+// fp16 takes fewer instructions than bf16: its ten mantissa bits hold a nibble where
 // it lies, 1024 + code from bits 0-3 and 1024 + 16 code from bits 4-7, less the
 // zero (any byte) by one exact fused multiply-add.  So x is taken to fp16 by a
 // power of two for each row that brings its largest value to 2^14; the sums are
@@ -364,8 +365,9 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2)
 // 34.1 and 28.9, eight 40.0 and 35.1).
 //
 // A block is 256 inputs of 32 outputs, so a row's copies are whole lines.  One
-// row through the 8B gate and up (61 MB): 22.4 us, 2.7 TB/s, the unpacking pipe
-// 44% busy and 47% of issue slots taken; the kernel above 30.3.
+// row through the 8B gate and up (61 MB): 22.2 us, 2.7 TB/s, the unpacking pipe
+// 44% busy and 47% of issue slots taken, so nothing is full: warps wait for their
+// copies and for one another at a tile's end.  The kernel above takes 30.3.
 constexpr int kFewWarps = 16, kFewAhead = 2, kFewBlock = 256;
 constexpr int kFewPitch = kFewBlock / 2 + 16;  // bytes of a row of a block: 8 rows' words fall on 32 banks
 constexpr int kFewStage = kMmaOuts * kFewPitch;

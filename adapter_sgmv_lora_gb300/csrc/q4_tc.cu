@@ -23,7 +23,7 @@
 // summed by all of them and one thread issuing the products: 92).  Every wait is
 // bounded.
 //
-// Gate and up take 80 us for 64 rows, 92 for 128, 137 for 256; q4.cu's tiles
+// Gate and up take 82 us for 64 rows, 96 for 128, 143 for 256; q4.cu's tiles
 // 122, 229 and 441.  What bounds it is the way of a block through the barriers,
 // some 800 cycles whatever the rows: leaving out the unpacking saves 8%, with
 // three of four products and of the stores 15%, the scaling or x nothing.

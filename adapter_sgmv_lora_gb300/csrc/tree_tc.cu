@@ -33,12 +33,13 @@
 // any stride order (boxes: 24 trees of 64 on the 70B attention 697 us, so 499; one
 // context of 131072 tokens 313, so 214).  Every wait is bounded.
 //
-// Those trees (24 contexts of 1024 to 8192 tokens, 64 over 8 heads) take 426 us,
-// 548 TFLOP/s counting P once; 60 tokens against 131012 192 us, 2.8 TB/s; 48
-// ragged trees over 128 to 2048 tokens 92 us, 2.9 TB/s.  What bounds it are the
-// hand-overs between loads, products and softmax (150 to 600 cycles each) and
-// instruction fetch: products, exponentials or loads left out one at a time
-// change its time by less than a tenth.
+// Those trees (24 contexts of 1024 to 8192 tokens, 64 over 8 heads) take 494 us,
+// 473 TFLOP/s counting P once; 60 tokens against 131012 248 us, 2.2 TB/s; 48
+// ragged trees over 128 to 2048 tokens 99 us, 2.7 TB/s.  What bounds it is the
+// chain of loads, scores, softmax and outputs, whose hand-overs take 150 to 600
+// cycles each (read by clocks in the kernel): issue slots are 42% taken, the
+// tensor pipe 43%, DRAM 44%, and with two terms products, exponentials or
+// loads left out one at a time changed its time by less than a tenth.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
