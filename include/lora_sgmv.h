@@ -628,9 +628,10 @@ size_t lora_tree_attention_workspace_bytes(const lora_tree_attention_t* attentio
  * NaN.  Scores, softmax sums and the output's accumulation are fp32; on the
  * tensor-core path (bf16; rows of cache, q and out on 16-byte boundaries) the
  * probabilities enter the product with V with fp32's 24 bits, as three bf16
- * terms.  A sequence without rows reads nothing.  A length below the sequence's rows or
- * above max_pages * page_size, or more rows than the masks have bits, raises
- * LORA_DEV_BAD_LENGTH, a used page id outside the cache LORA_DEV_BAD_PAGE; that
+ * terms.  An infinite value that a row sees with a probability of 0 in fp32 may
+ * make its column NaN.  A sequence without rows reads nothing.  A length below
+ * the sequence's rows or above max_pages * page_size, or more rows than the
+ * masks have bits, raises LORA_DEV_BAD_LENGTH, a used page id outside the cache LORA_DEV_BAD_PAGE; that
  * sequence's rows of out and lse are left as they were, the others are
  * computed.  Row offsets that decrease or leave [0, num_rows] raise
  * LORA_DEV_BAD_OFFSETS and nothing is computed.  The same arguments give the
